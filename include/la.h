@@ -306,6 +306,154 @@ la_status la_forward_noncausal_variant(const void *q, const void *k, const void 
 la_status la_decode_step_variant(const void *q, const void *k, const void *v, const void *beta, void *y,
                                  float *S, float *z, la_shape s, la_variant var, la_stream_t stream);
 
+/* ------------------------------------------- the layer around the attention
+ * A gated linear recurrence, layer norm and the clipping of gradients: what a
+ * recurrent layer's training and serving step runs next to the calls above.
+ * They share the conventions at the top except these: sizes are free (no set
+ * of head widths), and tensors are views with strides, whose pointers need
+ * their element's alignment only (16-byte aligned rows run wider loads).
+ * Strides are in elements, >= 0; 0 repeats an input.  An output's rows may
+ * not overlap one another (its dimensions nest: each stride at least the
+ * extent of the smaller ones), and an output may not start where an input or
+ * another output does unless the call says so.
+ */
+
+/* Rows of D contiguous channels: row (b, h, n) starts at data + b*sb + h*sh + n*sn. */
+typedef struct {
+    void *data;
+    long long sb, sh, sn;
+} la_view;
+
+/* Rows of C contiguous values: row r starts at data + r*stride. */
+typedef struct {
+    void *data;
+    long long stride;
+} la_rows;
+
+/*
+ * Gated linear recurrence.  Every channel of every sequence (b, h) keeps one
+ * number, h_t = a_t h_{t-1} + u_t, and out_t = h_t.  The gate g gives
+ *   LA_GATE_DECAY    a = g,             u = x
+ *   LA_GATE_LOG      a = e^g,           u = x
+ *   LA_GATE_SIGMOID  a = 1/(1 + e^-g),  u = (1 - a) x
+ * (LA_GATE_LOG and LA_GATE_SIGMOID give a with the relative accuracy of
+ * fp32 in both a and 1 - a, so that long memories keep their length.)
+ */
+typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOG = 1, LA_GATE_SIGMOID = 2 } la_gate;
+
+/*
+ * Forward over N tokens: x, g, out [B,H,N,D] of dtype s.dtype (s.M ignored;
+ * any B, H, N >= 0, D >= 1); the state is fp32.
+ *   h0: [B,H,D] contiguous fp32, the state before the first token (NULL: 0).
+ *   hN: [B,H,D] contiguous fp32, receives the state after the last token
+ *      (NULL: not wanted); it may be h0 itself.
+ *   lens: device pointer to B int32 lengths (clamped to [0, N]; NULL: all N):
+ *      rows of sequence b at or past lens[b] are not read, their rows of out
+ *      are 0, and hN is the state after lens[b] tokens (h0 for none).
+ * With N = 0 there is no token: hN receives h0 (or 0).
+ * D up to 2^31 - 64; more than 2^31 - 1 groups of 32 channels over all
+ * sequences are LA_ERR_UNSUPPORTED.
+ */
+la_status la_recurrence_forward(la_view x, la_view g, la_view out, const int *lens, la_shape s, la_gate gate,
+                                const float *h0, float *hN, la_stream_t stream);
+
+/*
+ * One token of every sequence: x, g, y [B,H,D] (views without the token
+ * dimension: sn and s.N are ignored), h [B,H,D] fp32 updated in place.  The
+ * same as la_recurrence_forward over one token with h0 = hN = h.
+ */
+la_status la_recurrence_step(la_view x, la_view g, la_view y, la_shape s, la_gate gate, float *h,
+                             la_stream_t stream);
+
+/*
+ * Backward of la_recurrence_forward: given dout = dL/dout and dhN = dL/dhN,
+ *   l_t = dout_t + a_{t+1} l_{t+1} (and dhN at the last token),
+ *   dx_t = l_t (times 1 - a_t, LA_GATE_SIGMOID),
+ *   dL/da_t = l_t h_{t-1} (l_t (h_{t-1} - x_t), LA_GATE_SIGMOID),
+ *   dg_t = dL/da_t times 1, a_t or a_t (1 - a_t),
+ *   dh0 = a_1 l_1.
+ *   out: the forward's output, which gives h_{t-1} as it was rounded there.
+ *   x: read by LA_GATE_SIGMOID only (else its data may be NULL).
+ *   dx, dg: [B,H,N,D] of dtype s.dtype; rows past a length are 0.
+ *   h0: as given to the forward (NULL: 0); dhN: [B,H,D] fp32 (NULL: 0);
+ *   dh0: [B,H,D] fp32, receives dL/dh0 (NULL: not wanted), and may be dhN
+ *      itself.  Chaining consecutive segments through dh0 -> dhN gives the
+ *      backward of the whole sequence.
+ */
+la_status la_recurrence_backward(la_view x, la_view g, la_view out, la_view dout, la_view dx, la_view dg,
+                                 const int *lens, la_shape s, la_gate gate, const float *h0, const float *dhN,
+                                 float *dh0, la_stream_t stream);
+
+/*
+ * Layer norm of every row, with the residual sum in front of it:
+ *   s = x + res (rounded to dtype: the stream the next layer adds to),
+ *   y = (s - mean(s)) rstd w + b,  rstd = 1/sqrt(var(s) + eps), var over C.
+ *   x, res, sum, y: rows of C values of dtype; res.data NULL: s = x;
+ *      sum.data NULL: s is not kept (without res it has to be NULL); sum may
+ *      be x or res itself (the stream updated in place, same stride).
+ *   w, b: C fp32 values each, or NULL (1 and 0).
+ *   mean, rstd: `rows` fp32 values for the backward (both NULL: not wanted).
+ *   1 <= C <= 16384 (else LA_ERR_UNSUPPORTED; C < 1 is invalid), eps >= 0.
+ */
+la_status la_layernorm_forward(la_rows x, la_rows res, la_rows sum, la_rows y, const float *w, const float *b,
+                               float *mean, float *rstd, long long rows, int C, la_dtype dtype, float eps,
+                               la_stream_t stream);
+
+/* Bytes of device workspace la_layernorm_backward needs; (size_t)-1 if the sizes are invalid. */
+size_t la_layernorm_workspace_bytes(long long rows, int C, la_dtype dtype);
+
+/*
+ * Backward of la_layernorm_forward: given dy = dL/dy and, where s was kept,
+ * dsum = dL/ds from the layers that read it, with xh = (s - mean) rstd:
+ *   ds = rstd (w dy - avg(w dy) - xh avg(w dy xh)) + dsum
+ *   dw = sum over rows of dy xh,  db = sum over rows of dy
+ * ds is the gradient of x and of res alike.
+ *   s: the forward's sum (x without res); mean, rstd: as it wrote them.
+ *   dsum.data NULL: 0.  dw, db: C fp32 values each, or NULL (not wanted).
+ *   workspace: la_layernorm_workspace_bytes(rows, C, dtype) bytes (per-CTA
+ *      column sums; they are added in a fixed order, so equal calls give
+ *      equal bits).
+ */
+la_status la_layernorm_backward(la_rows dy, la_rows s, la_rows dsum, la_rows ds, const float *w, const float *mean,
+                                const float *rstd, float *dw, float *db, long long rows, int C, la_dtype dtype,
+                                void *workspace, size_t ws_bytes, la_stream_t stream);
+
+/*
+ * One tensor of a list: n contiguous values at src, and dst for the calls
+ * that write (dst may be src).  src and dst need their element's alignment.
+ */
+typedef struct {
+    const void *src;
+    void *dst;
+    long long n;
+    la_dtype dtype;
+} la_tensor;
+
+/*
+ * Bytes of device workspace the two calls below need for `count` tensors;
+ * (size_t)-1 if count is negative.
+ */
+size_t la_grad_workspace_bytes(int count);
+
+/*
+ * Global norm over all tensors (a host array, read before the call returns):
+ *   *norm = sqrt(sum of the squares of every value of every tensor)
+ * (squares and sums in fp32 and in a fixed order, the last level in 64 bits).
+ *   norm: device pointer to one fp32 value.  No values at all give 0.
+ */
+la_status la_grad_norm(const la_tensor *tensors, int count, float *norm, void *workspace, size_t ws_bytes,
+                       la_stream_t stream);
+
+/*
+ * Clipping by the global norm: norm as above, then for every tensor
+ *   dst = min(1, max_norm / (norm + 1e-6)) src
+ * on the device, without a host round trip.  A norm that is NaN makes every
+ * value NaN; an infinite one makes finite values 0 (and infinite ones NaN).
+ *   max_norm: >= 0.
+ */
+la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
+                       size_t ws_bytes, la_stream_t stream);
+
 /*
  * Non-causal attention that allocates nothing, for callers that cannot
  * allocate device memory: code that only receives pointers from a host

@@ -33,11 +33,14 @@ EXPORTED = ("la_workspace_bytes", "la_forward_noncausal", "la_forward_causal", "
             "la_backward_noncausal", "la_forward_causal_varlen", "la_decode_steps",
             "la_feature_dim", "la_variant_workspace_bytes", "la_forward_causal_variant",
             "la_forward_noncausal_variant", "la_decode_step_variant", "la_checked_build",
-            "la_debug_inject_bounds")
+            "la_debug_inject_bounds", "la_recurrence_forward", "la_recurrence_step",
+            "la_recurrence_backward", "la_layernorm_forward", "la_layernorm_workspace_bytes",
+            "la_layernorm_backward", "la_grad_workspace_bytes", "la_grad_norm", "la_grad_clip")
 
 LA_FM = {"elu1": 0, "dpfp": 1, "poly2": 2}
 LA_NORM = {"den": 0, "sum": 1, "none": 2}
 LA_UPDATE = {"sum": 0, "delta": 1}
+LA_GATE = {"decay": 0, "log": 1, "sigmoid": 2}
 
 
 class LAError(RuntimeError):
@@ -54,6 +57,20 @@ class la_shape(ctypes.Structure):
 class la_variant(ctypes.Structure):
     _fields_ = [("feature_map", ctypes.c_int), ("nu", ctypes.c_int), ("norm", ctypes.c_int),
                 ("update", ctypes.c_int)]
+
+
+class la_view(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("sh", ctypes.c_longlong),
+                ("sn", ctypes.c_longlong)]
+
+
+class la_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_longlong)]
+
+
+class la_tensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_longlong),
+                ("dtype", ctypes.c_int)]
 
 
 def variant(fm: str = "elu1", nu: int = 1, norm: str = "den", update: str = "sum") -> la_variant:
@@ -131,6 +148,25 @@ def _load(path: str) -> ctypes.CDLL:
         L.la_checked_build.argtypes = []
         L.la_debug_inject_bounds.restype = None
         L.la_debug_inject_bounds.argtypes = [i]
+        ll, f = ctypes.c_longlong, ctypes.c_float
+        L.la_recurrence_forward.restype = i
+        L.la_recurrence_forward.argtypes = [la_view, la_view, la_view, vp, la_shape, i, vp, vp, vp]
+        L.la_recurrence_step.restype = i
+        L.la_recurrence_step.argtypes = [la_view, la_view, la_view, la_shape, i, vp, vp]
+        L.la_recurrence_backward.restype = i
+        L.la_recurrence_backward.argtypes = [la_view] * 6 + [vp, la_shape, i, vp, vp, vp, vp]
+        L.la_layernorm_forward.restype = i
+        L.la_layernorm_forward.argtypes = [la_rows] * 4 + [vp, vp, vp, vp, ll, i, i, f, vp]
+        L.la_layernorm_workspace_bytes.restype = sz
+        L.la_layernorm_workspace_bytes.argtypes = [ll, i, i]
+        L.la_layernorm_backward.restype = i
+        L.la_layernorm_backward.argtypes = [la_rows] * 4 + [vp, vp, vp, vp, vp, ll, i, i, vp, sz, vp]
+        L.la_grad_workspace_bytes.restype = sz
+        L.la_grad_workspace_bytes.argtypes = [i]
+        L.la_grad_norm.restype = i
+        L.la_grad_norm.argtypes = [vp, i, vp, vp, sz, vp]
+        L.la_grad_clip.restype = i
+        L.la_grad_clip.argtypes = [vp, i, f, vp, vp, sz, vp]
         _loaded[path] = L
     return L
 
@@ -396,6 +432,281 @@ def la_decode_step_variant(q, k, v, S, var: la_variant, z=None, beta=None, y=Non
                                       _stream(stream, q.device))
     _check(st, "la_decode_step_variant")
     return y
+
+
+# ------------------------------------------- the layer around the attention
+# These calls check shapes, types and devices here (the library sees pointers,
+# sizes and strides only), take views, and allocate what they return or need
+# as workspace on the stream that they launch on.
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _same_place(ref, **ts):
+    """Every tensor is on ref's CUDA device, which is the current one."""
+    _need(ref.is_cuda, "tensors must be on a CUDA device")
+    _need(ref.device.index == torch.cuda.current_device(), "tensors must be on the current CUDA device")
+    for name, t in ts.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, ref.device))
+
+
+def _empty(stream, shape, dtype, device):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):   # memory of the stream that uses it
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(name, t, shape, dtype):
+    if t is not None:
+        _need(tuple(t.shape) == tuple(shape), "%s must have shape %s" % (name, tuple(shape)))
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s" % (name, dtype))
+
+
+def _view(name, t, step: bool = False) -> la_view:
+    """Rows of [B,N,D] or [B,H,N,D] ([B,D] or [B,H,D] for a step) as a la_view."""
+    if t is None:
+        return la_view(None, 0, 0, 0)
+    st = t.stride()
+    _need(st[-1] == 1 or t.shape[-1] <= 1, "%s: the channels must be contiguous" % name)
+    sn = 0 if step else st[-2]
+    lead = len(st) - (1 if step else 2)
+    return la_view(t.data_ptr(), st[0], st[1] if lead == 2 else 0, sn)
+
+
+def _rec_shape(x, step: bool) -> la_shape:
+    lead = x.dim() - (1 if step else 2)
+    _need(lead in (1, 2), "x must be [B,D] or [B,H,D]" if step else "x must be [B,N,D] or [B,H,N,D]")
+    _need(x.shape[-1] >= 1, "x must have a channel")
+    B, H = x.shape[0], (x.shape[1] if lead == 2 else 1)
+    return la_shape(B, H, 1 if step else x.shape[-2], x.shape[-1], 0, _dtype_code(x.dtype))
+
+
+def _gate_code(gate: str) -> int:
+    _need(gate in LA_GATE, "gate must be one of %s" % ", ".join(LA_GATE))
+    return LA_GATE[gate]
+
+
+def _state(name, t, shape):
+    if t is not None:
+        _like(name, t, shape, torch.float32)
+        _contig(t)
+
+
+def _lens(lens, B):
+    if lens is not None:
+        if lens.dtype != torch.int32:
+            raise TypeError("lens must be torch.int32")
+        _need(tuple(lens.shape) == (B,), "lens must have shape (%d,)" % B)
+        _contig(lens)
+
+
+def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + u_t of every channel, out_t = h_t.
+
+    x, g: [B,N,D] or [B,H,N,D], any strides but the channels'.  gate: "decay"
+    (a = g, u = x), "log" (a = e^g, u = x) or "sigmoid" (a = sigmoid(g),
+    u = (1 - a) x).  h0, hN: fp32 states [B,D] or [B,H,D], read before the
+    first token and written after the last; hN may be h0.  lens: int32 [B];
+    rows past a length are 0.  Returns out."""
+    s = _rec_shape(x, False)
+    code = _gate_code(gate)
+    _like("g", g, x.shape, x.dtype)
+    _like("out", out, x.shape, x.dtype)
+    state = x.shape[:-2] + x.shape[-1:]
+    _state("h0", h0, state)
+    _state("hN", hN, state)
+    _lens(lens, x.shape[0])
+    _same_place(x, g=g, out=out, h0=h0, hN=hN, lens=lens)
+    if out is None:
+        out = _empty(stream, x.shape, x.dtype, x.device)
+    st = lib().la_recurrence_forward(_view("x", x), _view("g", g), _view("out", out), _ptr(lens), s, code, _ptr(h0),
+                                     _ptr(hN), _stream(stream, x.device))
+    _check(st, "la_recurrence_forward")
+    return out
+
+
+def la_recurrence_step(x, g, h, gate="sigmoid", y=None, stream=None):
+    """One token of the recurrence: x, g [B,D] or [B,H,D]; h the fp32 state of
+    the same shape, updated in place.  Returns y = h in x's type."""
+    s = _rec_shape(x, True)
+    code = _gate_code(gate)
+    _like("g", g, x.shape, x.dtype)
+    _like("y", y, x.shape, x.dtype)
+    _need(h is not None, "h is required")
+    _state("h", h, x.shape)
+    _same_place(x, g=g, y=y, h=h)
+    if y is None:
+        y = _empty(stream, x.shape, x.dtype, x.device)
+    st = lib().la_recurrence_step(_view("x", x, True), _view("g", g, True), _view("y", y, True), s, code, _ptr(h),
+                                  _stream(stream, x.device))
+    _check(st, "la_recurrence_step")
+    return y
+
+
+def la_recurrence_backward(x, g, out, dout, gate="sigmoid", h0=None, dhN=None, dh0=None, lens=None, dx=None, dg=None,
+                           stream=None):
+    """Gradients (dx, dg) of la_recurrence_forward given its out and dout =
+    dL/dout.  h0, lens: as given to the forward; dhN: gradient of its hN; dh0
+    (fp32, written): gradient of h0, may be dhN.  x is read by the sigmoid
+    gate only and may be None for the others."""
+    s = _rec_shape(g, False)
+    code = _gate_code(gate)
+    _need(x is not None or gate != "sigmoid", "the sigmoid gate needs x")
+    for name, t in (("x", x), ("out", out), ("dout", dout), ("dx", dx), ("dg", dg)):
+        _like(name, t, g.shape, g.dtype)
+    state = g.shape[:-2] + g.shape[-1:]
+    _state("h0", h0, state)
+    _state("dhN", dhN, state)
+    _state("dh0", dh0, state)
+    _lens(lens, g.shape[0])
+    _same_place(g, x=x, out=out, dout=dout, h0=h0, dhN=dhN, dh0=dh0, lens=lens, dx=dx, dg=dg)
+    if dx is None:
+        dx = _empty(stream, g.shape, g.dtype, g.device)
+    if dg is None:
+        dg = _empty(stream, g.shape, g.dtype, g.device)
+    st = lib().la_recurrence_backward(_view("x", x), _view("g", g), _view("out", out), _view("dout", dout),
+                                      _view("dx", dx), _view("dg", dg), _ptr(lens), s, code, _ptr(h0), _ptr(dhN),
+                                      _ptr(dh0), _stream(stream, g.device))
+    _check(st, "la_recurrence_backward")
+    return dx, dg
+
+
+def _rows(name, t) -> la_rows:
+    """All rows (last dimension) of t as one strided list."""
+    if t is None:
+        return la_rows(None, 0)
+    if t.is_contiguous():
+        return la_rows(t.data_ptr(), t.shape[-1])
+    st, sh = t.stride(), t.shape
+    _need(st[-1] == 1 or sh[-1] <= 1, "%s: the last dimension must be contiguous" % name)
+    stride = extent = None
+    for d in range(t.dim() - 2, -1, -1):
+        if sh[d] == 1:
+            continue
+        if stride is None:
+            stride, extent = st[d], st[d] * sh[d]
+        else:
+            _need(st[d] == extent, "%s: the rows must share one stride" % name)
+            extent = st[d] * sh[d]
+    return la_rows(t.data_ptr(), sh[-1] if stride is None else stride)
+
+
+def _row_count(t) -> int:
+    return t.numel() // t.shape[-1]
+
+
+def la_layernorm_forward(x, w=None, b=None, eps=1e-5, res=None, y=None, sum=None, mean=None, rstd=None, stats=True,
+                         stream=None):
+    """Layer norm of the rows of x [..., C], with the residual sum s = x + res
+    in front when res is given.  w, b: fp32 [C] or None.  Returns (y, s, mean,
+    rstd): s is x itself without res; mean and rstd (fp32, for the backward)
+    are None with stats=False.  sum: where s goes (may be x or res)."""
+    _need(x.dim() >= 1 and x.shape[-1] >= 1, "x must have rows of at least one value")
+    code = _dtype_code(x.dtype)
+    C = x.shape[-1]
+    for name, t in (("res", res), ("sum", sum), ("y", y)):
+        _like(name, t, x.shape, x.dtype)
+    for name, t, shape in (("w", w, (C,)), ("b", b, (C,)), ("mean", mean, x.shape[:-1]), ("rstd", rstd, x.shape[:-1])):
+        _state(name, t, shape)
+    _need(sum is None or res is not None, "sum needs res")
+    _same_place(x, res=res, sum=sum, y=y, w=w, b=b, mean=mean, rstd=rstd)
+    if y is None:
+        y = _empty(stream, x.shape, x.dtype, x.device)
+    if res is not None and sum is None:
+        sum = _empty(stream, x.shape, x.dtype, x.device)
+    if stats:
+        mean = _empty(stream, x.shape[:-1], torch.float32, x.device) if mean is None else mean
+        rstd = _empty(stream, x.shape[:-1], torch.float32, x.device) if rstd is None else rstd
+    else:
+        _need(mean is None and rstd is None, "mean and rstd need stats")
+    st = lib().la_layernorm_forward(_rows("x", x), _rows("res", res), _rows("sum", sum), _rows("y", y), _ptr(w),
+                                    _ptr(b), _ptr(mean), _ptr(rstd), _row_count(x), C, code, eps,
+                                    _stream(stream, x.device))
+    _check(st, "la_layernorm_forward")
+    return y, (x if res is None else sum), mean, rstd
+
+
+def la_layernorm_backward(dy, s, w, mean, rstd, dsum=None, ds=None, dw=None, db=None, stream=None):
+    """Gradients (ds, dw, db) of la_layernorm_forward given dy = dL/dy, the s,
+    mean and rstd it returned and, where s went on as the residual stream,
+    dsum = dL/ds.  ds is the gradient of x and of res; w may be None (1)."""
+    _need(dy.dim() >= 1 and dy.shape[-1] >= 1, "dy must have rows of at least one value")
+    code = _dtype_code(dy.dtype)
+    C = dy.shape[-1]
+    for name, t in (("s", s), ("dsum", dsum), ("ds", ds)):
+        _like(name, t, dy.shape, dy.dtype)
+    for name, t, shape in (("w", w, (C,)), ("dw", dw, (C,)), ("db", db, (C,)), ("mean", mean, dy.shape[:-1]),
+                           ("rstd", rstd, dy.shape[:-1])):
+        _state(name, t, shape)
+    _need(mean is not None and rstd is not None, "mean and rstd are required")
+    _same_place(dy, s=s, dsum=dsum, ds=ds, w=w, mean=mean, rstd=rstd, dw=dw, db=db)
+    if ds is None:
+        ds = _empty(stream, dy.shape, dy.dtype, dy.device)
+    if dw is None:
+        dw = _empty(stream, (C,), torch.float32, dy.device)
+    if db is None:
+        db = _empty(stream, (C,), torch.float32, dy.device)
+    rows = _row_count(dy)
+    need = lib().la_layernorm_workspace_bytes(rows, C, code)
+    if need == _SIZE_MAX:
+        raise LAError(LA_ERR_UNSUPPORTED, "la_layernorm_workspace_bytes")
+    ws = _empty(stream, (need,), torch.uint8, dy.device) if need else None
+    st = lib().la_layernorm_backward(_rows("dy", dy), _rows("s", s), _rows("dsum", dsum), _rows("ds", ds), _ptr(w),
+                                     _ptr(mean), _ptr(rstd), _ptr(dw), _ptr(db), rows, C, code, _ptr(ws), need,
+                                     _stream(stream, dy.device))
+    _check(st, "la_layernorm_backward")
+    return ds, dw, db
+
+
+def _grad_list(grads, out):
+    grads = list(grads)
+    _need(len(grads) > 0, "no tensors")
+    out = [None] * len(grads) if out is None else list(out)
+    _need(len(out) == len(grads), "out must have one tensor per gradient")
+    table = (la_tensor * len(grads))()
+    for e, t, d in zip(table, grads, out):
+        _contig(t)
+        e.src, e.n, e.dtype = t.data_ptr(), t.numel(), _dtype_code(t.dtype)
+        if d is not None:
+            _like("out", d, t.shape, t.dtype)
+            _contig(d)
+            e.dst = d.data_ptr()
+    first = grads[0]
+    _same_place(first)
+    for t in grads + [d for d in out if d is not None]:
+        _need(t.device == first.device, "all tensors must be on one device")
+    return table, first.device
+
+
+def la_grad_norm(grads, norm=None, stream=None):
+    """Global norm sqrt(sum of all squares) over a list of tensors, an fp32 scalar on the device."""
+    table, device = _grad_list(grads, None)
+    return _grad_call("la_grad_norm", table, device, norm, stream)
+
+
+def la_grad_clip(grads, max_norm, out=None, norm=None, stream=None):
+    """Scales every tensor by min(1, max_norm / (norm + 1e-6)) with the global
+    norm, in place or into the tensors of out; returns the norm (an fp32
+    scalar on the device)."""
+    grads = list(grads)
+    table, device = _grad_list(grads, grads if out is None else out)
+    return _grad_call("la_grad_clip", table, device, norm, stream, float(max_norm))
+
+
+def _grad_call(name, table, device, norm, stream, *args):
+    _state("norm", norm, ())
+    if norm is None:
+        norm = _empty(stream, (), torch.float32, device)
+    need = lib().la_grad_workspace_bytes(len(table))
+    ws = _empty(stream, (need,), torch.uint8, device)
+    st = getattr(lib(), name)(table, len(table), *args, _ptr(norm), _ptr(ws), need, _stream(stream, device))
+    _check(st, name)
+    return norm
 
 
 def la_get_last_error(stream=None, device=None) -> int:
