@@ -1,41 +1,135 @@
 // la_gate.cuh - the gate of the gated linear recurrence: a and w = du/dx from
-// the value g of a token and channel.
+// the value g of a token and channel, for V neighbouring channels at a time.
 #pragma once
 
 #include "la_common.cuh"
 
 namespace la {
 
-// e^g for the log gate.  A memory of T tokens has a about 1 - 1/T, and a
-// rounding of a that is off to one side moves h by T times as much: fp32 e^g,
-// whose error of an ulp need not be centred, was 6.6e-6 off over 5001 tokens
-// with T up to 1000, where a correctly rounded a gives 4e-7.  Near 0, 1 +
+// Two fp32 operations in one instruction (each half rounds as the single one).
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
+          "l"(reinterpret_cast<unsigned long long &>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long &>(r))
+        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
+    return r;
+}
+
+// V fp32 values, as pairs where V is even.
+template <int V> struct Lanes {
+    static_assert(V % 2 == 0, "");
+    float2 p[V / 2];
+    __device__ __forceinline__ float get(int v) const { return v % 2 ? p[v / 2].y : p[v / 2].x; }
+    __device__ __forceinline__ void set(int v, float x) { (v % 2 ? p[v / 2].y : p[v / 2].x) = x; }
+};
+template <> struct Lanes<1> {
+    float p[1];
+    __device__ __forceinline__ float get(int) const { return p[0]; }
+    __device__ __forceinline__ void set(int, float x) { p[0] = x; }
+};
+
+__device__ __forceinline__ float fma_pair(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float mul_pair(float a, float b) { return a * b; }
+__device__ __forceinline__ float add_pair(float a, float b) { return a + b; }
+
+template <int V> __device__ __forceinline__ Lanes<V> all(float x) {
+    Lanes<V> r;
+#pragma unroll
+    for (int v = 0; v < V; v++) r.set(v, x);
+    return r;
+}
+template <int V> __device__ __forceinline__ Lanes<V> fma(const Lanes<V> &a, const Lanes<V> &b, const Lanes<V> &c) {
+    Lanes<V> r;
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; i++) r.p[i] = fma_pair(a.p[i], b.p[i], c.p[i]);
+    return r;
+}
+template <int V> __device__ __forceinline__ Lanes<V> mul(const Lanes<V> &a, const Lanes<V> &b) {
+    Lanes<V> r;
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; i++) r.p[i] = mul_pair(a.p[i], b.p[i]);
+    return r;
+}
+template <int V> __device__ __forceinline__ Lanes<V> add(const Lanes<V> &a, const Lanes<V> &b) {
+    Lanes<V> r;
+#pragma unroll
+    for (int i = 0; i < (V + 1) / 2; i++) r.p[i] = add_pair(a.p[i], b.p[i]);
+    return r;
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// a = e^g of the log gate.  A memory of T tokens has a about 1 - 1/T, and a
+// rounding of a that is off to one side moves h by T times as much: an fp32
+// e^g, whose error of an ulp need not be centred, was 6.6e-6 off over 5001
+// tokens with T up to 1000, where a correctly rounded a gives 4e-7.  Near 0, 1 +
 // (e^g - 1) with the Taylor series of e^g - 1 up to g^7 / 7! (the next term is
 // below 4e-10 for |g| <= 1/4) rounds once, at the last sum.
-__device__ __forceinline__ float exp_gate(float g) {
-    float p = 1.f / 5040.f;
-    p = fmaf(p, g, 1.f / 720.f);
-    p = fmaf(p, g, 1.f / 120.f);
-    p = fmaf(p, g, 1.f / 24.f);
-    p = fmaf(p, g, 1.f / 6.f);
-    p = fmaf(p, g, 0.5f);
-    p = fmaf(p * g, g, g);
-    return fabsf(g) <= 0.25f ? 1.f + p : expf(g);
+template <int V> __device__ __forceinline__ Lanes<V> exp_gate(const Lanes<V> &g) {
+    Lanes<V> p = all<V>(1.f / 5040.f);
+    p = fma(p, g, all<V>(1.f / 720.f));
+    p = fma(p, g, all<V>(1.f / 120.f));
+    p = fma(p, g, all<V>(1.f / 24.f));
+    p = fma(p, g, all<V>(1.f / 6.f));
+    p = fma(p, g, all<V>(0.5f));
+    p = fma(mul(p, g), g, g);
+    p = add(p, all<V>(1.f));
+    const Lanes<V> t = mul(g, all<V>(kLog2e));
+#pragma unroll
+    for (int v = 0; v < V; v++)
+        if (!(fabsf(g.get(v)) <= 0.25f)) p.set(v, ex2_approx(t.get(v)));
+    return p;
 }
 
 // GATE: a value of la_gate.  w is 1 - a for the sigmoid gate, without
-// cancellation, and 1 for the others.
-template <int GATE> __device__ __forceinline__ void gate_of(float g, float &a, float &w) {
-    if (GATE == 2) {
-        // the smaller of the two from the exponential, the larger as 1 minus it
-        const float e = expf(-fabsf(g));
-        const float lo = __fdividef(e, 1.f + e), hi = 1.f - lo;
-        a = g >= 0.f ? hi : lo;
-        w = g >= 0.f ? lo : hi;
-        if (isnan(g)) a = w = g;
+// cancellation, and 1 for the others.  The sigmoid has to be short: HBM
+// delivers 3.9 values a clock and SM, and an SM issues 4 instructions a clock.
+// w = 1 / (1 + e^g) is within 2^-21 (1 + |g|) of itself; where a is the larger
+// it is 1 - w, rounded once, so that an a next to 1 is not off to one side,
+// where it is the smaller it is e^g w.
+template <int GATE, int V>
+__device__ __forceinline__ void gate_of(const Lanes<V> &g, Lanes<V> &a, Lanes<V> &w) {
+    if constexpr (GATE == 2) {
+        Lanes<V> e = mul(g, all<V>(kLog2e));
+#pragma unroll
+        for (int v = 0; v < V; v++) e.set(v, ex2_approx(e.get(v)));
+        w = add(e, all<V>(1.f));
+#pragma unroll
+        for (int v = 0; v < V; v++) w.set(v, rcp_approx(w.get(v)));
+        a = fma(w, all<V>(-1.f), all<V>(1.f));
+        const Lanes<V> small = mul(e, w);
+#pragma unroll
+        for (int v = 0; v < V; v++)
+            if (g.get(v) < 0.f) a.set(v, small.get(v));
     } else {
-        a = GATE == 1 ? exp_gate(g) : g;
-        w = 1.f;
+        a = GATE == 1 ? exp_gate<V>(g) : g;
+        w = all<V>(1.f);
     }
 }
 
