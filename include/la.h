@@ -336,8 +336,11 @@ typedef struct {
  *   LA_GATE_DECAY    a = g,             u = x
  *   LA_GATE_LOG      a = e^g,           u = x
  *   LA_GATE_SIGMOID  a = 1/(1 + e^-g),  u = (1 - a) x
- * (LA_GATE_LOG and LA_GATE_SIGMOID give a with the relative accuracy of
- * fp32 in both a and 1 - a, so that long memories keep their length.)
+ * LA_GATE_LOG rounds an a next to 1 once, and LA_GATE_SIGMOID has both a and
+ * 1 - a within 2^-21 (1 + |g|) of themselves, so that long memories keep their
+ * length.  Products of gates over runs of tokens are formed in fp32 (held at its
+ * largest value past it): with |a| > 1 throughout, a state that is not 0 can
+ * reach infinity before its own value would.
  */
 typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOG = 1, LA_GATE_SIGMOID = 2 } la_gate;
 
@@ -347,6 +350,7 @@ typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOG = 1, LA_GATE_SIGMOID = 2 } la_gate
  *   h0: [B,H,D] contiguous fp32, the state before the first token (NULL: 0).
  *   hN: [B,H,D] contiguous fp32, receives the state after the last token
  *      (NULL: not wanted); it may be h0 itself.
+ *   workspace: la_recurrence_workspace_bytes(s) bytes.
  *   lens: device pointer to B int32 lengths (clamped to [0, N]; NULL: all N):
  *      rows of sequence b at or past lens[b] are not read, their rows of out
  *      are 0, and hN is the state after lens[b] tokens (h0 for none).
@@ -355,7 +359,15 @@ typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOG = 1, LA_GATE_SIGMOID = 2 } la_gate
  * sequences are LA_ERR_UNSUPPORTED.
  */
 la_status la_recurrence_forward(la_view x, la_view g, la_view out, const int *lens, la_shape s, la_gate gate,
-                                const float *h0, float *hN, la_stream_t stream);
+                                const float *h0, float *hN, void *workspace, size_t ws_bytes,
+                                la_stream_t stream);
+
+/*
+ * Bytes of device workspace la_recurrence_forward and la_recurrence_backward
+ * need for shape `s` (0: none, NULL is accepted): a few long sequences are cut
+ * into segments, whose (A, H) go through it.  (size_t)-1 for an invalid shape.
+ */
+size_t la_recurrence_workspace_bytes(la_shape s);
 
 /*
  * One token of every sequence: x, g, y [B,H,D] (views without the token
@@ -382,7 +394,7 @@ la_status la_recurrence_step(la_view x, la_view g, la_view y, la_shape s, la_gat
  */
 la_status la_recurrence_backward(la_view x, la_view g, la_view out, la_view dout, la_view dx, la_view dg,
                                  const int *lens, la_shape s, la_gate gate, const float *h0, const float *dhN,
-                                 float *dh0, la_stream_t stream);
+                                 float *dh0, void *workspace, size_t ws_bytes, la_stream_t stream);
 
 /*
  * Layer norm of every row, with the residual sum in front of it:

@@ -38,8 +38,8 @@ def _shape(B=2, H=4, N=8, D=16, dt=F32):
 def test_recurrence_forward_refusals(lib):
     f, s = lib.la_recurrence_forward, _shape()
 
-    def call(x=_v(0), g=_v(1), out=_v(2), lens=None, s=s, gate=2, h0=None, hN=None):
-        return f(x, g, out, lens, s, gate, h0, hN, None)
+    def call(x=_v(0), g=_v(1), out=_v(2), lens=None, s=s, gate=2, h0=None, hN=None, ws=None, n=0):
+        return f(x, g, out, lens, s, gate, h0, hN, ws, n, None)
     assert call(s=_shape(B=-1)) == INVALID
     assert call(s=_shape(N=-1)) == INVALID
     assert call(s=_shape(D=0)) == INVALID
@@ -63,6 +63,14 @@ def test_recurrence_forward_refusals(lib):
     # more channel groups than a grid has CTAs
     assert call(s=_shape(B=1 << 20, H=1 << 12, D=64)) == UNSUPPORTED
     assert call(s=_shape(D=0x7fffffff)) == UNSUPPORTED
+    # a few long sequences need workspace
+    long = _shape(B=1, H=1, N=65536)
+    need = lib.la_recurrence_workspace_bytes(long)
+    assert 0 < need < (1 << 22) and lib.la_recurrence_workspace_bytes(_shape(N=128)) == 0
+    assert lib.la_recurrence_workspace_bytes(_shape(N=-1)) == la._SIZE_MAX
+    assert call(s=long) == INVALID
+    assert call(s=long, ws=_p(7), n=need - 1) == INVALID
+    assert call(s=long, ws=_p(7, 8), n=need) == INVALID
     # nothing to do
     assert call(x=_v(None), g=_v(None), out=_v(None), s=_shape(B=0)) == OK
     assert call(x=_v(None), g=_v(None), out=_v(None), s=_shape(N=0)) == OK
@@ -83,8 +91,8 @@ def test_recurrence_backward_refusals(lib):
     f = lib.la_recurrence_backward
 
     def call(x=_v(0), g=_v(1), out=_v(2), dout=_v(3), dx=_v(4), dg=_v(5), lens=None, s=_shape(), gate=2, h0=None,
-             dhN=None, dh0=None):
-        return f(x, g, out, dout, dx, dg, lens, s, gate, h0, dhN, dh0, None)
+             dhN=None, dh0=None, ws=None, n=0):
+        return f(x, g, out, dout, dx, dg, lens, s, gate, h0, dhN, dh0, ws, n, None)
     bad = _v(7, off=1)
     for name in ("x", "g", "out", "dout", "dx", "dg"):
         assert call(**{name: bad}) == INVALID

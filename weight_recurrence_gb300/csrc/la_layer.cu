@@ -62,6 +62,10 @@ bool out_rows_ok(const la_rows &v, la_dtype t, long long rows, int C) {
 }
 bool same(const void *a, const void *b) { return a != nullptr && a == b; }
 
+bool workspace_ok(size_t need, const void *ws, size_t bytes) {
+    return need == 0 || (bytes >= need && aligned(ws, 16));
+}
+
 la_status check_norm(long long rows, int C, la_dtype t) {
     if (rows < 0 || C < 1 || !dtype_ok(t)) return LA_ERR_INVALID_ARG;
     if (C > kNormMaxC || rows > (1LL << 40)) return LA_ERR_UNSUPPORTED;
@@ -75,8 +79,12 @@ using namespace la;
 
 extern "C" {
 
+size_t la_recurrence_workspace_bytes(la_shape s) {
+    return check_rec_shape(s, LA_GATE_DECAY) == LA_OK ? recurrence_ws_bytes(s) : (size_t)-1;
+}
+
 la_status la_recurrence_forward(la_view x, la_view g, la_view out, const int *lens, la_shape s, la_gate gate,
-                                const float *h0, float *hN, la_stream_t stream) {
+                                const float *h0, float *hN, void *workspace, size_t ws_bytes, la_stream_t stream) {
     la_status st = check_rec_shape(s, gate);
     if (st != LA_OK) return st;
     if (s.B == 0 || s.H == 0) return LA_OK;
@@ -87,12 +95,11 @@ la_status la_recurrence_forward(la_view x, la_view g, la_view out, const int *le
     for (const void *i : {(const void *)x.data, (const void *)g.data, (const void *)lens, (const void *)h0})
         if (same(out.data, i)) return LA_ERR_INVALID_ARG;
     if (hN && (same(hN, out.data) || same(hN, x.data) || same(hN, g.data) || same(hN, lens))) return LA_ERR_INVALID_ARG;
-    const DeviceInfo *dev = device_info();
-    if (!dev) return LA_ERR_CUDA;
+    if (!workspace_ok(recurrence_ws_bytes(s), workspace, ws_bytes)) return LA_ERR_INVALID_ARG;
     RecProblem p{};
-    p.x = x, p.g = g, p.out = out, p.lens = lens, p.h0 = h0, p.hN = hN;
+    p.x = x, p.g = g, p.out = out, p.lens = lens, p.h0 = h0, p.hN = hN, p.ws = workspace;
     p.B = s.B, p.H = s.H, p.N = s.N, p.D = s.D, p.dtype = s.dtype, p.gate = gate, p.stream = (cudaStream_t)stream;
-    return from_cuda(recurrence_forward(p, *dev));
+    return from_cuda(recurrence_forward(p));
 }
 
 la_status la_recurrence_step(la_view x, la_view g, la_view y, la_shape s, la_gate gate, float *h,
@@ -100,12 +107,12 @@ la_status la_recurrence_step(la_view x, la_view g, la_view y, la_shape s, la_gat
     s.N = 1;
     x.sn = g.sn = y.sn = 0;
     if (s.B > 0 && s.H > 0 && h == nullptr) return LA_ERR_INVALID_ARG;
-    return la_recurrence_forward(x, g, y, nullptr, s, gate, h, h, stream);
+    return la_recurrence_forward(x, g, y, nullptr, s, gate, h, h, nullptr, 0, stream);
 }
 
 la_status la_recurrence_backward(la_view x, la_view g, la_view out, la_view dout, la_view dx, la_view dg,
                                  const int *lens, la_shape s, la_gate gate, const float *h0, const float *dhN,
-                                 float *dh0, la_stream_t stream) {
+                                 float *dh0, void *workspace, size_t ws_bytes, la_stream_t stream) {
     la_status st = check_rec_shape(s, gate);
     if (st != LA_OK) return st;
     if (s.B == 0 || s.H == 0) return LA_OK;
@@ -123,13 +130,12 @@ la_status la_recurrence_backward(la_view x, la_view g, la_view out, la_view dout
         if (same(dx.data, i) || same(dg.data, i) || same(dh0, i)) return LA_ERR_INVALID_ARG;
     if (dx.data == dg.data || same(dh0, dx.data) || same(dh0, dg.data) || same(dhN, dx.data) || same(dhN, dg.data))
         return LA_ERR_INVALID_ARG;
-    const DeviceInfo *dev = device_info();
-    if (!dev) return LA_ERR_CUDA;
+    if (!workspace_ok(recurrence_ws_bytes(s), workspace, ws_bytes)) return LA_ERR_INVALID_ARG;
     RecProblem p{};
     p.x = x, p.g = g, p.out = out, p.dout = dout, p.dx = dx, p.dg = dg, p.lens = lens, p.h0 = h0, p.dhN = dhN;
-    p.dh0 = dh0;
+    p.dh0 = dh0, p.ws = workspace;
     p.B = s.B, p.H = s.H, p.N = s.N, p.D = s.D, p.dtype = s.dtype, p.gate = gate, p.stream = (cudaStream_t)stream;
-    return from_cuda(recurrence_backward(p, *dev));
+    return from_cuda(recurrence_backward(p));
 }
 
 la_status la_layernorm_forward(la_rows x, la_rows res, la_rows sum, la_rows y, const float *w, const float *b,

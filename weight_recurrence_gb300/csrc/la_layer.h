@@ -18,11 +18,13 @@ struct RecProblem {
     int B, H, N, D;
     la_dtype dtype;
     la_gate gate;
+    void *ws;
     cudaStream_t stream;
 };
 
-cudaError_t recurrence_forward(const RecProblem &p, const DeviceInfo &dev);
-cudaError_t recurrence_backward(const RecProblem &p, const DeviceInfo &dev);
+size_t recurrence_ws_bytes(const la_shape &s);   // s valid
+cudaError_t recurrence_forward(const RecProblem &p);
+cudaError_t recurrence_backward(const RecProblem &p);
 
 struct NormProblem {
     la_rows x, res, sum, y;    // backward: x is s, res is dsum, sum unused, y is dy

@@ -8,13 +8,18 @@
 // product of its gates and H the run started from 0, so runs are walked side
 // by side and joined by their (A, H).
 //
-// A strip of 32 lanes' channels belongs to one CTA, or to a cluster of CTAs
-// where there are few strips.  They walk its tokens in tiles: each warp takes
-// R consecutive rows, first forms (A, H) of them, then learns the state before
-// them (the warps' maps through shared memory, the CTAs' through distributed
-// shared memory) and runs the recurrence proper from it.  Every value is read
-// once and written once, without workspace, flags in global memory or atomics,
-// and the grouping depends on the sizes alone, so equal calls give equal bits.
+// A strip of 32 lanes' channels belongs to one CTA, which walks its tokens in
+// tiles: each warp takes R consecutive rows, first forms (A, H) of them, then
+// learns the state before them (the warps' maps joined through shared memory)
+// and runs the recurrence proper from it.  Every value is read once and written
+// once.  Where the strips alone would leave SMs empty, a sequence is cut into
+// segments, one CTA each, after a first launch that forms each segment's (A, H)
+// alone; that reads x and g (g and dout) a second time.  (Clusters of CTAs that
+// walk one sequence side by side and exchange their maps through distributed
+// shared memory read everything once, but wait for one another at every tile:
+// 1.1 us for 512 rows, 142 us for N = 65536, D = 64.)  No atomics and no flags,
+// and the grouping depends on the sizes alone: equal calls give equal bits.
+#include <algorithm>
 #include <initializer_list>
 #include <type_traits>
 
@@ -30,7 +35,11 @@ struct Dims {
     const int *lens;
     int H, N, D;
     int strips;        // groups of 32 lanes' channels in a sequence
-    int *err;          // device error word
+    int segments;      // CTAs of a strip
+    long long rows;    // tokens of a segment (a multiple of a tile's)
+    long long channels;   // B*H*D
+    float2 *maps;      // [segments - 1][B*H*D] (A, H) of the segments but the last
+    float *start;      // [B*H*D] the state before the first
 };
 
 // V neighbouring channels of one row as they lie in memory.
@@ -72,92 +81,71 @@ template <> struct Raw<__nv_bfloat16, 4> {
     }
 };
 
-__device__ __forceinline__ unsigned cluster_ctas() {
-    unsigned r;
-    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void st_async_v2(uint32_t raddr, float x, float y, uint32_t rbar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(raddr),
-                 "r"(__float_as_uint(x)), "r"(__float_as_uint(y)), "r"(rbar)
-                 : "memory");
-}
-
 // A product of gates past fp32's range would turn an empty state into NaN
 // (inf * 0): it is held at the largest finite value instead.
 __device__ __forceinline__ float finite(float A) {
     return fminf(fmaxf(A, -3.402823466e38f), 3.402823466e38f);
 }
 
-constexpr uint64_t kWaitNs = 2000000000ull;   // limit of a wait on the other CTAs of a cluster
-
 // The joining of a tile's maps (A, H), one per warp and channel.  For that the
 // CTA's threads change sides: G = W / V neighbouring lanes own a channel, each
 // of them the maps of V consecutive warps, so that a map is read once and not
 // by every warp after it (which cost a third of all instructions).  The owners
-// form the CTA's map, carry the channel's state over the tile, and leave the
-// state before each warp's rows in place of its H.  Everything is in two sets,
-// used in turn, so that a set is not written again before all have read it.
-// In a cluster each CTA's map goes to all of its CTAs by st.async, which
-// completes their mbarrier: a cluster barrier per tile waited for the tile's
-// global stores as well (its release) and took 12000 cycles.
+// carry the channel's state over the tile and leave the state before each
+// warp's rows in place of its H.  Everything is in two sets, used in turn, so
+// that a set is not written again before all have read it.
 template <int V, int W> struct Joint {
     static constexpr int G = W / V, C = 32 * V;
     static_assert(G * V == W, "");
     float A[2][W][C + 4], H[2][W][C + 4];   // the 4: owners of a warp read distinct banks
-    uint64_t bar[2];
 };
+
+template <int V> using Vec = std::conditional_t<V == 4, float4, std::conditional_t<V == 2, float2, float>>;
+template <int V> __device__ __forceinline__ void put_lanes(float *to, const Lanes<V> &v) {
+    *reinterpret_cast<Vec<V> *>(to) = *reinterpret_cast<const Vec<V> *>(&v);
+}
+template <int V> __device__ __forceinline__ Lanes<V> get_lanes(const float *from) {
+    const Vec<V> r = *reinterpret_cast<const Vec<V> *>(from);
+    return *reinterpret_cast<const Lanes<V> *>(&r);
+}
+template <int V> __device__ __forceinline__ Lanes<V> finite(const Lanes<V> &A) {
+    Lanes<V> r;
+#pragma unroll
+    for (int v = 0; v < V; v++) r.set(v, finite(A.get(v)));
+    return r;
+}
 
 template <int V, int W> struct Join {
     using J = Joint<V, W>;
-    using Vec = std::conditional_t<V == 4, float4, std::conditional_t<V == 2, float2, float>>;
     J &j;
-    float2 *cta;             // [2][ctas][C]: the cluster's maps
-    unsigned ctas, rank;
     int warp, lane, channel, sub;
     float state;             // of the owned channel
-    int it = 0;
-    bool alive = true;
-    int *err;
+    int set = 0;
 
-    // first: the strip's first channel in the states [B,H,D], of which `left` exist.
-    __device__ __forceinline__ Join(J &j_, unsigned ctas_, unsigned rank_, const float *first, int left, int *err_)
-        : j(j_), cta(reinterpret_cast<float2 *>(&j_ + 1)), ctas(ctas_), rank(rank_), warp(threadIdx.x >> 5),
-          lane(threadIdx.x & 31), channel(threadIdx.x / J::G), sub(threadIdx.x % J::G), err(err_) {
+    // first: the strip's first channel of the state before the CTA's rows.
+    __device__ __forceinline__ Join(J &j_, const float *first, int left)
+        : j(j_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), channel(threadIdx.x / J::G),
+          sub(threadIdx.x % J::G) {
         state = first && channel < left ? first[channel] : 0.f;
-        if (ctas > 1) {
-            if (threadIdx.x == 0) {
-                tc::mbar_init(&j.bar[0], 1);
-                tc::mbar_init(&j.bar[1], 1);
-                tc::fence_mbar_init();
+    }
+    // Over the segments before this one; maps: their strip's first channel, `pitch` apart.
+    __device__ __forceinline__ void skip(const float2 *maps, int segments, long long pitch, int left) {
+        if (channel < left) {
+#pragma unroll 8
+            for (int i = 0; i < segments; i++) {
+                const float2 m = maps[i * pitch + channel];
+                state = fmaf(m.x, state, m.y);
             }
-            tc::cluster_arrive_release();   // the others' barriers are there once they have started
-            tc::cluster_wait_acquire();
         }
     }
-    // Writes the last state; no CTA leaves while another may still store into it.
     __device__ __forceinline__ void end(float *first, int left) {
-        if (first && channel < left && sub == 0 && rank == 0) first[channel] = state;
-        if (ctas > 1) {
-            tc::cluster_arrive_release();
-            tc::cluster_wait_acquire();
-        }
-    }
-
-    static __device__ __forceinline__ void put(float *to, const Lanes<V> &v) { *reinterpret_cast<Vec *>(to) = *reinterpret_cast<const Vec *>(&v); }
-    static __device__ __forceinline__ Lanes<V> get(const float *from) {
-        const Vec r = *reinterpret_cast<const Vec *>(from);
-        return *reinterpret_cast<const Lanes<V> *>(&r);
+        if (first && channel < left && sub == 0) first[channel] = state;
     }
 
     // A, H: this thread's rows; returns the state before them.
     __device__ __forceinline__ Lanes<V> operator()(const Lanes<V> &A, const Lanes<V> &H) {
-        const int set = it & 1;
-        Lanes<V> bounded;
-#pragma unroll
-        for (int v = 0; v < V; v++) bounded.set(v, finite(A.get(v)));
-        put(&j.A[set][warp][lane * V], bounded);
-        put(&j.H[set][warp][lane * V], H);
+        put_lanes(&j.A[set][warp][lane * V], finite(A));
+        put_lanes(&j.H[set][warp][lane * V], H);
         __syncthreads();
         float a[V], h[V], ta = 1.f, th = 0.f;
 #pragma unroll
@@ -178,109 +166,176 @@ template <int V, int W> struct Join {
             ta = __shfl_sync(~0u, ta, J::G - 1, J::G);
             th = __shfl_sync(~0u, th, J::G - 1, J::G);
         }
-        float start = state;
-        if (ctas == 1) {
-            state = fmaf(ta, state, th);
-        } else {
-            float2 *maps = cta + (size_t)set * ctas * J::C;
-            if (threadIdx.x == 0) tc::mbar_arrive_expect_tx(&j.bar[set], ctas * J::C * (unsigned)sizeof(float2));
-            const uint32_t to = tc::smem_u32(&maps[rank * J::C + channel]), bar = tc::smem_u32(&j.bar[set]);
-            for (unsigned r = sub; r < ctas; r += J::G)
-                st_async_v2(tc::mapa_shared(to, r), ta, th, tc::mapa_shared(bar, r));
-            if (alive && !tc::mbar_try_wait(&j.bar[set], (it >> 1) & 1)) {
-                alive = tc::mbar_wait_bounded(&j.bar[set], (it >> 1) & 1, globaltimer_ns() + kWaitNs, nullptr);
-                if (!alive) record_error(err, kErrTimeout);
-            }
-            for (unsigned r = 0; r < ctas; r++) {
-                if (r == rank) start = state;
-                const float2 m = maps[r * J::C + channel];
-                state = fmaf(m.x, state, m.y);
-            }
-        }
-        start = fmaf(ea, start, eh);
+        float before = fmaf(ea, state, eh);
+        state = fmaf(ta, state, th);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            j.H[set][sub * V + i][channel] = start;
-            start = fmaf(a[i], start, h[i]);
+            j.H[set][sub * V + i][channel] = before;
+            before = fmaf(a[i], before, h[i]);
         }
         __syncthreads();
-        it++;
-        return get(&j.H[set][warp][lane * V]);
+        const Lanes<V> r = get_lanes<V>(&j.H[set][warp][lane * V]);
+        set ^= 1;
+        return r;
     }
 };
 
-// A thread's place: its channels, its sequence, its CTA's part of the cluster.
+// A CTA's place: its sequence, its channels, its rows [from, to) in the order
+// of the walk.
 template <int V> struct Place {
-    unsigned ctas, rank;
-    long long b, h, bh;
-    int d0, d, len;          // first channel of the strip, of the thread
-    bool ok;                 // its channels exist (all V or none: D is a multiple of V)
-    __device__ __forceinline__ explicit Place(const Dims &s) {
-        ctas = cluster_ctas();
-        rank = tc::cluster_ctarank();
-        const unsigned strip = blockIdx.x / ctas;
-        bh = strip / s.strips;
+    long long b, h, at;      // at: its first channel in [B,H,D]
+    int d0, left, len, segment;
+    long long from, to;
+    bool ok;                 // the thread's channels exist (all V or none: D is a multiple of V)
+    __device__ __forceinline__ Place(const Dims &s, int segments) {
+        const unsigned strip = blockIdx.x / segments;
+        segment = blockIdx.x % segments;
+        const long long bh = strip / s.strips;
         b = bh / s.H;
         h = bh % s.H;
         d0 = (int)(strip % s.strips) * 32 * V;
-        d = d0 + (threadIdx.x & 31) * V;
-        ok = d < s.D;
+        left = s.D - d0;
+        at = bh * s.D + d0;
+        ok = (int)(threadIdx.x & 31) * V < left;
         len = s.lens ? min(max(s.lens[b], 0), s.N) : s.N;
+        from = min(segment * s.rows, (long long)len);
+        to = min(from + s.rows, (long long)len);
     }
-    template <typename T> __device__ __forceinline__ T *rows(const la_view &v) const {
-        return static_cast<T *>(v.data) + b * v.sb + h * v.sh + (ok ? d : 0);
+    template <typename T> __device__ __forceinline__ T *strip(const la_view &v) const {
+        return static_cast<T *>(v.data) + b * v.sb + h * v.sh + d0;
     }
+    // whether the last token is among its rows (no token at all: the first segment)
+    __device__ __forceinline__ bool last() const { return to == len && (from < to || segment == 0); }
 };
 
-// Rows at or past a sequence's length become 0.
+// Rows at or past a sequence's length become 0, the segments taking turns.
 template <typename T, int V, int W>
-__device__ __forceinline__ void clear_rows(T *p, long long sn, const Place<V> &q, long long N) {
+__device__ __forceinline__ void clear_rows(T *p, long long sn, const Place<V> &q, const Dims &s) {
     using RT = typename Raw<T, V>::type;
     if (!q.ok) return;
-    for (long long t = q.len + q.rank * W + (threadIdx.x >> 5); t < N; t += q.ctas * W)
+    for (long long t = q.len + q.segment * W + (threadIdx.x >> 5); t < s.N; t += s.segments * W)
         *reinterpret_cast<RT *>(p + t * sn) = RT{};
 }
 
-template <typename T, int GATE, int V, int W, int R, int CTAS>
+// A warp's rows of NT tensors on their way through shared memory, S tiles deep.
+// WIDE: every row starts on 16 bytes and its channels fill 16-byte pieces:
+// neighbouring lanes copy neighbouring pieces, two or four rows a request.  Else
+// each lane copies its own V channels: 4 or 8 bytes asynchronously, single bf16
+// values through registers, which reach shared memory a tile later.
+template <typename T, int V, int NT, int R, int S, bool WIDE> struct Ring {
+    using RT = typename Raw<T, V>::type;
+    static constexpr bool kHeld = sizeof(RT) < 4;
+    RT (*slot)[NT][R][32];   // [S], this warp's
+    int lane;
+    RT held[kHeld ? NT : 1][kHeld ? R : 1] = {};
+    int held_stage = -1;
+
+    __device__ __forceinline__ Ring(RT (*slot_)[NT][R][32], int lane_) : slot(slot_), lane(lane_) {}
+
+    // Before the copies of a tile.
+    __device__ __forceinline__ void begin(int stage) {
+        if constexpr (kHeld) {
+            if (held_stage >= 0) {
+#pragma unroll
+                for (int k = 0; k < NT; k++)
+#pragma unroll
+                    for (int r = 0; r < R; r++) slot[held_stage][k][r][lane] = held[k][r];
+            }
+            held_stage = stage;
+        }
+    }
+
+    // Rows 0 .. n - 1 of tensor `k`: row r at p + r * sn (p: the row's first
+    // channel of the strip), `left` channels of it exist.
+    __device__ __forceinline__ void copy(int stage, int k, const T *p, long long sn, int n, int left) {
+        if constexpr (WIDE) {
+            constexpr int kPieces = 32 * V * (int)sizeof(T) / 16, kRows = 32 / kPieces, kPer = 16 / (int)sizeof(T);
+            const int piece = lane % kPieces;
+            p += piece * kPer + (lane / kPieces) * sn;
+            unsigned char *to = reinterpret_cast<unsigned char *>(slot[stage][k][lane / kPieces]) + piece * 16;
+            if (piece * kPer < left) {
+#pragma unroll
+                for (int r = 0; r < R; r += kRows, p += kRows * sn)
+                    if (r + lane / kPieces < n)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         tc::smem_u32(to + r * 32 * (int)sizeof(RT))),
+                                     "l"(p)
+                                     : "memory");
+            }
+        } else {
+            p += lane * V;
+            if (lane * V < left) {
+#pragma unroll
+                for (int r = 0; r < R; r++, p += sn) {
+                    if (r < n) {
+                        if constexpr (sizeof(RT) >= 4)
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                                             tc::smem_u32(&slot[stage][k][r][lane])),
+                                         "l"(p), "n"(sizeof(RT))
+                                         : "memory");
+                        else
+                            held[k][r] = *reinterpret_cast<const RT *>(p);
+                    }
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // All but the LEFT newest commits have landed, for the whole warp.
+    template <int LEFT> __device__ __forceinline__ void wait() const {
+        asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+        __syncwarp();
+    }
+    __device__ __forceinline__ Lanes<V> get(int stage, int k, int r) const { return Raw<T, V>::get(slot[stage][k][r][lane]); }
+};
+
+template <typename T, int V, int W, int NT, int R, int S> struct Tiles {
+    typename Raw<T, V>::type slot[W][S][NT][R][32];
+    Joint<V, W> joint;
+};
+
+template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la_view g, la_view out, Dims s,
                                                                   const float *h0, float *hN) {
     using RT = typename Raw<T, V>::type;
-    using Io = Raw<T, V>;
     extern __shared__ __align__(16) unsigned char smem[];
+    auto &sh = *reinterpret_cast<Tiles<T, V, W, 2, R, S> *>(smem);
     pdl_wait_cta();
-    const Place<V> q(s);
-    const long long at = q.bh * s.D + q.d0;
-    Join<V, W> join(*reinterpret_cast<Joint<V, W> *>(smem), q.ctas, q.rank, h0 ? h0 + at : nullptr, s.D - q.d0, s.err);
-    const T *px = q.template rows<T>(x), *pg = q.template rows<T>(g);
-    T *po = q.template rows<T>(out);
-    const long long step = (long long)q.ctas * W * R;                // rows of a tile
-    const long long first = (long long)(q.rank * W + join.warp) * R; // this warp's rows in it
-    const int tiles = (int)((q.len + step - 1) / step);
-    // rows of this thread in the tile that starts at t0
-    auto rows_at = [&](long long t0) { return q.ok ? (int)min((long long)R, max(q.len - t0, 0LL)) : 0; };
-
-    RT rx[R] = {}, rg[R] = {};   // the next tile's rows, on their way while this one's are used
-    {
-        const int n = rows_at(first);
-        const T *ax = px + (n ? first : 0) * x.sn, *ag = pg + (n ? first : 0) * g.sn;
-#pragma unroll
-        for (int r = 0; r < R; r++, ax += x.sn, ag += g.sn)
-            if (r < n) rx[r] = *reinterpret_cast<const RT *>(ax), rg[r] = *reinterpret_cast<const RT *>(ag);
-    }
+    const Place<V> q(s, s.segments);
+    Join<V, W> join(sh.joint, s.segments > 1 ? s.start + q.at : h0 ? h0 + q.at : nullptr, q.left);
+    Ring<T, V, 2, R, S, WIDE> ring(sh.slot[join.warp], join.lane);
+    const T *px = q.template strip<T>(x), *pg = q.template strip<T>(g);
+    T *po = q.template strip<T>(out) + join.lane * V;
+    const long long first = q.from + join.warp * R;   // this warp's rows in the first tile
+    const int tiles = (int)((q.to - q.from + W * R - 1) / (W * R));
+    auto fetch = [&](int it, int stage) {
+        const long long t = first + (long long)it * (W * R);
+        ring.begin(stage);
+        if (t < q.to) {
+            const int n = (int)min((long long)R, q.to - t);
+            ring.copy(stage, 0, px + t * x.sn, x.sn, n, q.left);
+            ring.copy(stage, 1, pg + t * g.sn, g.sn, n, q.left);
+        }
+        ring.commit();
+    };
+    for (int i = 0; i < S; i++) fetch(i, i);
+    join.skip(s.maps + q.at, q.segment, s.channels, q.left);
+    int stage = 0;
     for (int it = 0; it < tiles; it++) {
-        const long long t0 = it * step + first;
-        const int n = rows_at(t0), next = rows_at(t0 + step);
-        const T *ax = px + (next ? t0 + step : 0) * x.sn, *ag = pg + (next ? t0 + step : 0) * g.sn;
+        ring.template wait<S - 1>();
+        const long long t0 = first + (long long)it * (W * R);
+        const int n = (int)min((long long)R, max(q.to - t0, 0LL));
         Lanes<V> a[R], u[R];
 #pragma unroll
-        for (int r = 0; r < R; r++, ax += x.sn, ag += g.sn) {
+        for (int r = 0; r < R; r++) {
             Lanes<V> w;
-            const Lanes<V> xv = Io::get(rx[r]), gv = Io::get(rg[r]);
-            if (r < next) rx[r] = *reinterpret_cast<const RT *>(ax), rg[r] = *reinterpret_cast<const RT *>(ag);
-            gate_of<GATE, V>(gv, a[r], w);
-            u[r] = GATE == LA_GATE_SIGMOID ? mul(w, xv) : xv;
+            gate_of<GATE, V>(ring.get(stage, 1, r), a[r], w);
+            u[r] = GATE == LA_GATE_SIGMOID ? mul(w, ring.get(stage, 0, r)) : ring.get(stage, 0, r);
         }
-        if (n < R) {   // rows past the end leave the state as it is
+        __syncwarp();   // the stage is free
+        fetch(it + S, stage);
+        stage = stage == S - 1 ? 0 : stage + 1;
+        if (n < R) {    // rows past the end leave the state as it is
 #pragma unroll
             for (int r = 0; r < R; r++)
                 if (r >= n) a[r] = all<V>(1.f), u[r] = all<V>(0.f);
@@ -289,15 +344,77 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
 #pragma unroll
         for (int r = 1; r < R; r++) A = mul(A, a[r]), H = fma(a[r], H, u[r]);
         Lanes<V> h = join(A, H);
-        T *p = po + (n ? t0 : 0) * out.sn;
+        const int rows = q.ok ? n : 0;
+        T *p = po + t0 * out.sn;
 #pragma unroll
         for (int r = 0; r < R; r++, p += out.sn) {
             h = fma(a[r], h, u[r]);
-            if (r < n) *reinterpret_cast<RT *>(p) = Io::put(h);
+            if (r < rows) *reinterpret_cast<RT *>(p) = Raw<T, V>::put(h);
         }
     }
-    clear_rows<T, V, W>(po, out.sn, q, s.N);
-    join.end(hN ? hN + at : nullptr, s.D - q.d0);
+    clear_rows<T, V, W>(po, out.sn, q, s);
+    if (q.last()) join.end(hN ? hN + q.at : nullptr, q.left);
+}
+
+// (A, H) of every segment but the last, and a copy of the state that the walk
+// starts from (a caller's hN may be its h0).  Warps take consecutive eighths of
+// a segment and meet once at its end.  BACK: the backward's maps, of g and dout.
+template <typename T, int GATE, int V, bool WIDE, bool BACK, int W, int R, int S, int CTAS>
+__global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_view x, Dims s, const float *state) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto &sh = *reinterpret_cast<Tiles<T, V, W, 2, R, S> *>(smem);
+    pdl_wait_cta();
+    const Place<V> q(s, s.segments - 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Ring<T, V, 2, R, S, WIDE> ring(sh.slot[warp], lane);
+    const T *px = q.template strip<T>(x), *pg = q.template strip<T>(g);
+    const long long per = s.rows / W, first = min(q.from + warp * per, q.to), last = min(first + per, q.to);
+    const int pieces = (int)((last - first + R - 1) / R);
+    auto fetch = [&](int i, int stage) {
+        const long long t = first + (long long)i * R;
+        ring.begin(stage);
+        if (t < last) {
+            const int n = (int)min((long long)R, last - t);
+            const long long row = BACK ? q.len - 1 - t : t;
+            ring.copy(stage, 0, px + row * x.sn, BACK ? -x.sn : x.sn, n, q.left);
+            ring.copy(stage, 1, pg + row * g.sn, BACK ? -g.sn : g.sn, n, q.left);
+        }
+        ring.commit();
+    };
+    for (int i = 0; i < S; i++) fetch(i, i);
+    Lanes<V> A = all<V>(1.f), H = all<V>(0.f);
+    int stage = 0;
+    for (int i = 0; i < pieces; i++) {
+        ring.template wait<S - 1>();
+        const int n = (int)min((long long)R, last - (first + (long long)i * R));
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            Lanes<V> a, w;
+            gate_of<GATE, V>(ring.get(stage, 1, r), a, w);
+            const Lanes<V> v = ring.get(stage, 0, r);
+            if (r < n) {
+                A = mul(A, a);
+                if (BACK) H = mul(a, add(v, H));
+                else H = fma(a, H, GATE == LA_GATE_SIGMOID ? mul(w, v) : v);
+            }
+        }
+        __syncwarp();
+        fetch(i + S, stage);
+        stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    put_lanes(&sh.joint.A[0][warp][lane * V], finite(A));
+    put_lanes(&sh.joint.H[0][warp][lane * V], H);
+    __syncthreads();
+    for (int c = threadIdx.x; c < 32 * V && c < q.left; c += 32 * W) {
+        float a = 1.f, h = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; w++) {
+            h = fmaf(sh.joint.A[0][w][c], h, sh.joint.H[0][w][c]);
+            a = finite(a * sh.joint.A[0][w][c]);
+        }
+        s.maps[q.segment * s.channels + q.at + c] = make_float2(a, h);
+        if (q.segment == 0) s.start[q.at + c] = state ? state[q.at + c] : 0.f;
+    }
 }
 
 // Up to kShortRows tokens (a decoded token among them) there is nothing to
@@ -349,57 +466,69 @@ __global__ void __launch_bounds__(kShortThreads) rec_short_kernel(la_view x, la_
 }
 
 // The same walk from the last token to the first: the state is mu_t = a_t l_t,
-// which the token before adds to its own gradient.
-template <typename T, int GATE, int V, int W, int R, int CTAS>
+// which the token before adds to its own gradient.  The rows of g and dout are
+// free once they have become a, w and d, those of h_{t-1} and x only after the
+// join, so they go through two rings.
+template <typename T, int V, int W, int NL, int R, int S> struct BackTiles {
+    typename Raw<T, V>::type early[W][S][2][R][32], late[W][S][NL][R][32];
+    Joint<V, W> joint;
+};
+
+template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, la_view g, la_view out, la_view dout,
                                                                    la_view dx, la_view dg, Dims s, const float *h0,
                                                                    const float *dhN, float *dh0) {
     using RT = typename Raw<T, V>::type;
-    using Io = Raw<T, V>;
     constexpr bool kSigmoid = GATE == LA_GATE_SIGMOID;
+    constexpr int NL = kSigmoid ? 2 : 1;
     extern __shared__ __align__(16) unsigned char smem[];
+    auto &sh = *reinterpret_cast<BackTiles<T, V, W, NL, R, S> *>(smem);
     pdl_wait_cta();
-    const Place<V> q(s);
-    const long long at = q.bh * s.D + q.d0;
-    Join<V, W> join(*reinterpret_cast<Joint<V, W> *>(smem), q.ctas, q.rank, dhN ? dhN + at : nullptr, s.D - q.d0,
-                    s.err);
-    const T *px = kSigmoid ? q.template rows<T>(x) : nullptr, *pg = q.template rows<T>(g);
-    const T *po = q.template rows<T>(out), *pd = q.template rows<T>(dout);
-    T *pdx = q.template rows<T>(dx), *pdg = q.template rows<T>(dg);
-    const long long step = (long long)q.ctas * W * R;
-    const long long first = (long long)(q.rank * W + join.warp) * R;
-    const int tiles = (int)((q.len + step - 1) / step);
-    // rows t, t - 1, ... of this thread in the tile whose row `first` is t
-    auto rows_at = [&](long long t) { return q.ok ? (int)min((long long)R, max(t + 1, 0LL)) : 0; };
-
-    // the next tile's rows on their way: g and dout from where this tile's are
-    // turned into a, w and d, h_{t-1} and x from where they are used
-    RT rg[R] = {}, rd[R] = {}, rb[R] = {}, rx[R] = {};
-    {
-        const long long t = q.len - 1 - first;
-        const int n = rows_at(t);
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            if (r < n) {
-                rg[r] = *reinterpret_cast<const RT *>(pg + (t - r) * g.sn);
-                rd[r] = *reinterpret_cast<const RT *>(pd + (t - r) * dout.sn);
-                if (t - r > 0) rb[r] = *reinterpret_cast<const RT *>(po + (t - r - 1) * out.sn);
-                if constexpr (kSigmoid) rx[r] = *reinterpret_cast<const RT *>(px + (t - r) * x.sn);
-            }
+    const Place<V> q(s, s.segments);
+    Join<V, W> join(sh.joint, s.segments > 1 ? s.start + q.at : dhN ? dhN + q.at : nullptr, q.left);
+    Ring<T, V, 2, R, S, WIDE> early(sh.early[join.warp], join.lane);
+    Ring<T, V, NL, R, S, WIDE> late(sh.late[join.warp], join.lane);
+    const T *px = kSigmoid ? q.template strip<T>(x) : nullptr, *pg = q.template strip<T>(g);
+    const T *po = q.template strip<T>(out), *pd = q.template strip<T>(dout);
+    T *pdx = q.template strip<T>(dx) + join.lane * V, *pdg = q.template strip<T>(dg) + join.lane * V;
+    const long long first = q.len - 1 - (q.from + join.warp * R);   // this warp's first row, and the CTA's last
+    const long long end = q.len - q.to;
+    const int tiles = (int)((q.to - q.from + W * R - 1) / (W * R));
+    auto fetch_early = [&](int it, int stage) {   // rows t, t - 1, ...
+        const long long t = first - (long long)it * (W * R);
+        early.begin(stage);
+        if (t >= end) {
+            const int n = (int)min((long long)R, t - end + 1);
+            early.copy(stage, 0, pg + t * g.sn, -g.sn, n, q.left);
+            early.copy(stage, 1, pd + t * dout.sn, -dout.sn, n, q.left);
         }
-    }
+        early.commit();
+    };
+    auto fetch_late = [&](int it, int stage) {
+        const long long t = first - (long long)it * (W * R);
+        late.begin(stage);
+        if (t >= end) {
+            const int n = (int)min((long long)R, t - end + 1);
+            late.copy(stage, 0, po + (t - 1) * out.sn, -out.sn, (int)min((long long)n, t), q.left);
+            if constexpr (kSigmoid) late.copy(stage, 1, px + t * x.sn, -x.sn, n, q.left);
+        }
+        late.commit();
+    };
+    for (int i = 0; i < S; i++) fetch_early(i, i), fetch_late(i, i);
+    join.skip(s.maps + q.at, q.segment, s.channels, q.left);
+    int stage = 0;
     for (int it = 0; it < tiles; it++) {
-        const long long t0 = q.len - 1 - (it * step + first), t1 = t0 - step;
-        const int n = rows_at(t0), next = rows_at(t1);
-        const T *ag = pg + (next ? t1 : 0) * g.sn, *ad = pd + (next ? t1 : 0) * dout.sn;
+        early.template wait<2 * S - 1>();   // commits in turn: early, late, early, ...
+        const long long t0 = first - (long long)it * (W * R);
+        const int n = (int)min((long long)R, max(t0 - end + 1, 0LL));
         Lanes<V> a[R], w[R], d[R];
 #pragma unroll
-        for (int r = 0; r < R; r++, ag -= g.sn, ad -= dout.sn) {
-            const Lanes<V> gv = Io::get(rg[r]);
-            d[r] = Io::get(rd[r]);
-            if (r < next) rg[r] = *reinterpret_cast<const RT *>(ag), rd[r] = *reinterpret_cast<const RT *>(ad);
-            gate_of<GATE, V>(gv, a[r], w[r]);
+        for (int r = 0; r < R; r++) {
+            d[r] = early.get(stage, 1, r);
+            gate_of<GATE, V>(early.get(stage, 0, r), a[r], w[r]);
         }
+        __syncwarp();
+        fetch_early(it + S, stage);
         if (n < R) {   // rows before the first leave the state as it is
 #pragma unroll
             for (int r = 0; r < R; r++)
@@ -409,160 +538,181 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
 #pragma unroll
         for (int r = 1; r < R; r++) A = mul(A, a[r]), H = mul(a[r], add(d[r], H));
         Lanes<V> mu = join(A, H);
-        T *to_x = pdx + (n ? t0 : 0) * dx.sn, *to_g = pdg + (n ? t0 : 0) * dg.sn;
-        const T *ab = po + (next ? t1 - 1 : 0) * out.sn;
-        const T *ax = kSigmoid ? px + (next ? t1 : 0) * x.sn : nullptr;
-        const int next_b = next && t1 - next < 0 ? next - 1 : next;   // row 0 has no row before it
+        late.template wait<2 * S - 1>();
+        const int rows = q.ok ? n : 0;
+        T *to_x = pdx + t0 * dx.sn, *to_g = pdg + t0 * dg.sn;
 #pragma unroll
         for (int r = 0; r < R; r++, to_x -= dx.sn, to_g -= dg.sn) {
-            Lanes<V> before = Io::get(rb[r]), xv;
-            if (r < next_b) rb[r] = *reinterpret_cast<const RT *>(ab);
-            ab -= out.sn;
-            if constexpr (kSigmoid) {
-                xv = Io::get(rx[r]);
-                if (r < next) rx[r] = *reinterpret_cast<const RT *>(ax);
-                ax -= x.sn;
-            }
+            Lanes<V> before = late.get(stage, 0, r);
             if (t0 == r && q.ok) {   // the first token: the state that the forward started from
 #pragma unroll
-                for (int v = 0; v < V; v++) before.set(v, h0 ? h0[q.bh * s.D + q.d + v] : 0.f);
+                for (int v = 0; v < V; v++) before.set(v, h0 ? h0[q.at + join.lane * V + v] : 0.f);
             }
             const Lanes<V> l = add(d[r], mu);
             mu = mul(a[r], l);
-            const Lanes<V> ox = kSigmoid ? mul(l, w[r]) : l;
-            const Lanes<V> og = kSigmoid ? mul(mul(mu, w[r]), fma(xv, all<V>(-1.f), before))
-                                         : mul(GATE == LA_GATE_LOG ? mu : l, before);
-            if (r < n) {
-                *reinterpret_cast<RT *>(to_x) = Io::put(ox);
-                *reinterpret_cast<RT *>(to_g) = Io::put(og);
+            Lanes<V> ox = l, og;
+            if constexpr (kSigmoid) {
+                ox = mul(l, w[r]);
+                og = mul(mul(mu, w[r]), fma(late.get(stage, NL - 1, r), all<V>(-1.f), before));
+            } else {
+                og = mul(GATE == LA_GATE_LOG ? mu : l, before);
+            }
+            if (r < rows) {
+                *reinterpret_cast<RT *>(to_x) = Raw<T, V>::put(ox);
+                *reinterpret_cast<RT *>(to_g) = Raw<T, V>::put(og);
             }
         }
+        __syncwarp();
+        fetch_late(it + S, stage);
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
-    clear_rows<T, V, W>(pdx, dx.sn, q, s.N);
-    clear_rows<T, V, W>(pdg, dg.sn, q, s.N);
-    join.end(dh0 ? dh0 + at : nullptr, s.D - q.d0);
+    clear_rows<T, V, W>(pdx, dx.sn, q, s);
+    clear_rows<T, V, W>(pdg, dg.sn, q, s);
+    if (q.last()) join.end(dh0 ? dh0 + q.at : nullptr, q.left);
 }
 
-// Tiles: W warps of R rows a CTA, CTAS of them a SM.
-#ifndef FWD_CFG
-#define FWD_CFG 8, 8, 2
-#endif
-#ifndef BWD_CFG
-#define BWD_CFG 8, 8, 1
-#endif
-#ifndef MAXK
-#define MAXK 8
-#endif
-#ifndef FILL
-#define FILL 2
-#endif
-template <int W_, int R_, int C_> struct Tile {
-    static constexpr int W = W_, R = R_, CTAS = C_;
+// Tiles: W warps of R rows a CTA, S of them on their way, CTAS CTAs a SM.
+template <int W_, int R_, int S_, int C_> struct Tile {
+    static constexpr int W = W_, R = R_, S = S_, CTAS = C_;
 };
-using Fwd = Tile<FWD_CFG>;
-using Bwd = Tile<BWD_CFG>;
+// Many CTAs: two a SM hide each other's joins.  No more CTAs than SMs: twice the
+// rows a tile for the same number of joins (128 strips of 4096 tokens, bf16:
+// forward 63 us, backward 126 us, against 71 and 141 us with the small tiles; 256
+// strips of 2048: 69 and 109 us against 63 and 109 us).
+using Fwd = Tile<8, 8, 2, 2>;
+using FwdFew = Tile<8, 16, 3, 1>;
+using Bwd = Tile<8, 4, 2, 2>;
+using BwdFew = Tile<8, 8, 3, 1>;
+using Pre = Tile<8, 8, 3, 2>;
+constexpr int kSms = 152;
+constexpr int kSegmentRows = 128;   // a multiple of every tile's rows
 
-// CTAs per strip: enough that every SM has as many as it can hold, as far as
-// the tokens fill their tiles.
-int cluster_of(long long strips, int N, int rows, int ctas, const DeviceInfo &dev) {
-    int k = 1;
-    while (k < MAXK && strips * k * FILL < (long long)ctas * dev.sm_count * 2 && (long long)N > (long long)k * rows) k *= 2;
-    return k;
+// Segments of a strip: none of it (1) where the strips fill half of the SMs, else
+// as many as give every SM two CTAs, of at least kSegmentRows tokens.
+int segments_of(long long strips, int N, long long *rows) {
+    long long n = strips * 2 <= kSms ? 2 * kSms / strips : 1;
+    n = std::min(n, ((long long)N + kSegmentRows - 1) / kSegmentRows);
+    *rows = (((long long)N + n - 1) / n + kSegmentRows - 1) / kSegmentRows * kSegmentRows;
+    return (int)(((long long)N + *rows - 1) / *rows);
 }
 
-template <int V, typename Tile, typename Kernel, typename... Args>
-cudaError_t launch_tiles(Kernel kernel, const RecProblem &p, Dims s, const DeviceInfo &dev, Args... args) {
-    const long long strips = (long long)p.B * p.H * s.strips;
-    const int k = cluster_of(strips, p.N, Tile::W * Tile::R, Tile::CTAS, dev);
-    const size_t smem = sizeof(Joint<V, Tile::W>) + (k > 1 ? 2 * k * 32 * V * sizeof(float2) : 0);
+template <int V> Dims dims_of(const RecProblem &p) {
+    Dims s{p.lens, p.H, p.N, p.D, (p.D + 32 * V - 1) / (32 * V), 1, 0, (long long)p.B * p.H * p.D, nullptr, nullptr};
+    s.segments = segments_of((long long)p.B * p.H * s.strips, p.N, &s.rows);
+    s.maps = static_cast<float2 *>(p.ws);
+    s.start = reinterpret_cast<float *>(s.maps + (s.segments - 1) * s.channels);
+    return s;
+}
+
+template <typename Tile, typename Kernel, typename... Args>
+cudaError_t launch_tiles(Kernel kernel, size_t smem, const RecProblem &p, const Dims &s, int segments, Args... args) {
+    const long long ctas = (long long)p.B * p.H * s.strips * segments;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && k > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kernel, dim3((unsigned)(strips * k)), dim3(32 * Tile::W), smem, p.stream, (unsigned)k, args...);
+    e = launch_pdl(kernel, dim3((unsigned)ctas), dim3(32 * Tile::W), smem, p.stream, 0u, args...);
     count_launches(1);
     return e;
 }
 
-// Channels a lane takes: 8 bytes of a row, or as many as its alignment and the
-// strides allow; half of that where the last strip would be less than half full.
-template <typename T> int lane_channels(int D, std::initializer_list<la_view> views) {
-    const int most = 8 / (int)sizeof(T);
-    unsigned long long bits = (unsigned)D;
-    for (const la_view &v : views)
-        bits |= (unsigned long long)(reinterpret_cast<uintptr_t>(v.data) / sizeof(T)) | v.sb | v.sh | v.sn;
-#ifdef MAXV
-    int V = MAXV / (int)(sizeof(T) / 2);
-#else
-    int V = most;
-#endif
-    while (V > 1 && (bits & (V - 1))) V /= 2;
-    if (V == most && D % (32 * V) != 0 && D % (32 * V) <= 16 * V && D < 256 * V) V /= 2;
-    return V;
+template <typename T, int GATE, int V, bool WIDE, bool BACK>
+cudaError_t segment_maps(const RecProblem &p, const Dims &s) {
+    if (s.segments == 1) return cudaSuccess;
+    return launch_tiles<Pre>(rec_maps_kernel<T, GATE, V, WIDE, BACK, Pre::W, Pre::R, Pre::S, Pre::CTAS>,
+                                sizeof(Tiles<T, V, Pre::W, 2, Pre::R, Pre::S>), p, s, s.segments - 1, p.g,
+                                BACK ? p.dout : p.x, s, BACK ? p.dhN : p.h0);
 }
 
-template <typename T, int GATE, int V> cudaError_t forward_v(const RecProblem &p, const DeviceInfo &dev) {
-    Dims s{p.lens, p.H, p.N, p.D, (p.D + 32 * V - 1) / (32 * V)};
-    if (p.N <= kShortRows) {
-        const long long groups = (long long)p.B * p.H * (p.D / V);
-        const cudaError_t e = launch_pdl(rec_short_kernel<T, GATE, V>,
-                                         dim3((unsigned)((groups + kShortThreads - 1) / kShortThreads)),
-                                         dim3(kShortThreads), 0, p.stream, 0u, p.x, p.g, p.out, s, groups, p.h0, p.hN);
-        count_launches(1);
-        return e;
+template <typename T, int GATE, int V> cudaError_t short_v(const RecProblem &p) {
+    const long long groups = (long long)p.B * p.H * (p.D / V);
+    const cudaError_t e =
+        launch_pdl(rec_short_kernel<T, GATE, V>, dim3((unsigned)((groups + kShortThreads - 1) / kShortThreads)),
+                   dim3(kShortThreads), 0, p.stream, 0u, p.x, p.g, p.out, dims_of<V>(p), groups, p.h0, p.hN);
+    count_launches(1);
+    return e;
+}
+
+bool few_ctas(const RecProblem &p, const Dims &s) {
+    return (long long)p.B * p.H * s.strips * s.segments <= kSms;
+}
+
+struct Forward {
+    template <typename T, int GATE, int V, bool WIDE> static cudaError_t run(const RecProblem &p) {
+        if (p.N <= kShortRows) return short_v<T, GATE, V>(p);
+        const Dims s = dims_of<V>(p);
+        const cudaError_t e = segment_maps<T, GATE, V, WIDE, false>(p, s);
+        if (e != cudaSuccess) return e;
+        return few_ctas(p, s) ? tiles<T, GATE, V, WIDE, FwdFew>(p, s) : tiles<T, GATE, V, WIDE, Fwd>(p, s);
     }
-    s.err = dev.err_word;
-    return launch_tiles<V, Fwd>(rec_forward_kernel<T, GATE, V, Fwd::W, Fwd::R, Fwd::CTAS>, p, s, dev, p.x, p.g, p.out,
-                                s, p.h0, p.hN);
-}
-
-template <typename T, int GATE, int V> cudaError_t backward_v(const RecProblem &p, const DeviceInfo &dev) {
-    Dims s{p.lens, p.H, p.N, p.D, (p.D + 32 * V - 1) / (32 * V)};
-    s.err = dev.err_word;
-    return launch_tiles<V, Bwd>(rec_backward_kernel<T, GATE, V, Bwd::W, Bwd::R, Bwd::CTAS>, p, s, dev, p.x, p.g, p.out,
-                                p.dout, p.dx, p.dg, s, p.h0, p.dhN, p.dh0);
-}
-
-template <int GATE> cudaError_t forward_g(const RecProblem &p, const DeviceInfo &dev) {
-    if (p.dtype == LA_DTYPE_F32)
-        return lane_channels<float>(p.D, {p.x, p.g, p.out}) == 2 ? forward_v<float, GATE, 2>(p, dev)
-                                                                 : forward_v<float, GATE, 1>(p, dev);
-    switch (lane_channels<__nv_bfloat16>(p.D, {p.x, p.g, p.out})) {
-        case 4: return forward_v<__nv_bfloat16, GATE, 4>(p, dev);
-        case 2: return forward_v<__nv_bfloat16, GATE, 2>(p, dev);
-        default: return forward_v<__nv_bfloat16, GATE, 1>(p, dev);
+    template <typename T, int GATE, int V, bool WIDE, typename C>
+    static cudaError_t tiles(const RecProblem &p, const Dims &s) {
+        return launch_tiles<C>(rec_forward_kernel<T, GATE, V, WIDE, C::W, C::R, C::S, C::CTAS>,
+                               sizeof(Tiles<T, V, C::W, 2, C::R, C::S>), p, s, s.segments, p.x, p.g, p.out, s, p.h0,
+                               p.hN);
     }
+};
+
+struct Backward {
+    template <typename T, int GATE, int V, bool WIDE> static cudaError_t run(const RecProblem &p) {
+        const Dims s = dims_of<V>(p);
+        const cudaError_t e = segment_maps<T, GATE, V, WIDE, true>(p, s);
+        if (e != cudaSuccess) return e;
+        return few_ctas(p, s) ? tiles<T, GATE, V, WIDE, BwdFew>(p, s) : tiles<T, GATE, V, WIDE, Bwd>(p, s);
+    }
+    template <typename T, int GATE, int V, bool WIDE, typename C>
+    static cudaError_t tiles(const RecProblem &p, const Dims &s) {
+        return launch_tiles<C>(rec_backward_kernel<T, GATE, V, WIDE, C::W, C::R, C::S, C::CTAS>,
+                               sizeof(BackTiles<T, V, C::W, GATE == LA_GATE_SIGMOID ? 2 : 1, C::R, C::S>), p, s,
+                               s.segments, p.x, p.g, p.out, p.dout, p.dx, p.dg, s, p.h0, p.dhN, p.dh0);
+    }
+};
+
+// Largest power of two that divides every row's first address, in bytes (at most 16).
+int row_alignment(const RecProblem &p, int size) {
+    unsigned long long bits = 16 | (unsigned long long)p.D * size;
+    for (const la_view &v : {p.x, p.g, p.out, p.dout, p.dx, p.dg})   // those that a call lacks are 0
+        bits |= reinterpret_cast<uintptr_t>(v.data) | (unsigned long long)(v.sb | v.sh | v.sn) * size;
+    return (int)(bits & (~bits + 1));
 }
 
-template <int GATE> cudaError_t backward_g(const RecProblem &p, const DeviceInfo &dev) {
-    if (p.dtype == LA_DTYPE_F32)
-        return lane_channels<float>(p.D, {p.x, p.g, p.out, p.dout, p.dx, p.dg}) == 2
-                   ? backward_v<float, GATE, 2>(p, dev)
-                   : backward_v<float, GATE, 1>(p, dev);
-    switch (lane_channels<__nv_bfloat16>(p.D, {p.x, p.g, p.out, p.dout, p.dx, p.dg})) {
-        case 4: return backward_v<__nv_bfloat16, GATE, 4>(p, dev);
-        case 2: return backward_v<__nv_bfloat16, GATE, 2>(p, dev);
-        default: return backward_v<__nv_bfloat16, GATE, 1>(p, dev);
+// Channels a lane takes: 8 bytes of a row where rows start on 16 bytes (half of
+// that where the last strip would be less than half full), else 4, or one value.
+template <typename Call, int GATE> cudaError_t choose(const RecProblem &p) {
+    const bool f32 = p.dtype == LA_DTYPE_F32;
+    const int align = row_alignment(p, f32 ? 4 : 2), wide = f32 ? 64 : 128;
+    if (align == 16) {
+        const bool half = p.D % wide != 0 && p.D % wide <= wide / 2 && p.D < 8 * wide;
+        if (f32) return half ? Call::template run<float, GATE, 1, true>(p) : Call::template run<float, GATE, 2, true>(p);
+        return half ? Call::template run<__nv_bfloat16, GATE, 2, true>(p)
+                    : Call::template run<__nv_bfloat16, GATE, 4, true>(p);
     }
+    if (f32) return Call::template run<float, GATE, 1, false>(p);
+    return align >= 4 ? Call::template run<__nv_bfloat16, GATE, 2, false>(p)
+                      : Call::template run<__nv_bfloat16, GATE, 1, false>(p);
+}
+
+template <typename Call> cudaError_t choose_gate(const RecProblem &p) {
+    switch (p.gate) {
+        case LA_GATE_DECAY: return choose<Call, LA_GATE_DECAY>(p);
+        case LA_GATE_LOG: return choose<Call, LA_GATE_LOG>(p);
+        case LA_GATE_SIGMOID: return choose<Call, LA_GATE_SIGMOID>(p);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t recurrence_forward(const RecProblem &p, const DeviceInfo &dev) {
-    switch (p.gate) {
-        case LA_GATE_DECAY: return forward_g<LA_GATE_DECAY>(p, dev);
-        case LA_GATE_LOG: return forward_g<LA_GATE_LOG>(p, dev);
-        case LA_GATE_SIGMOID: return forward_g<LA_GATE_SIGMOID>(p, dev);
-    }
-    return cudaErrorInvalidValue;
+// Segments times channels is at most 304 strips' worth (of 128 channels) where
+// there is more than one segment.
+size_t recurrence_ws_bytes(const la_shape &s) {
+    const long long channels = (long long)s.B * s.H * s.D;
+    if (s.N <= kSegmentRows || channels == 0) return 0;
+    const long long strips = (long long)s.B * s.H * ((s.D + 127) / 128);   // the fewest that any lane width gives
+    if (strips * 2 > kSms) return 0;
+    const long long most = std::min(2LL * kSms / strips, ((long long)s.N + kSegmentRows - 1) / kSegmentRows);
+    return (size_t)most * channels * sizeof(float2);
 }
 
-cudaError_t recurrence_backward(const RecProblem &p, const DeviceInfo &dev) {
-    switch (p.gate) {
-        case LA_GATE_DECAY: return backward_g<LA_GATE_DECAY>(p, dev);
-        case LA_GATE_LOG: return backward_g<LA_GATE_LOG>(p, dev);
-        case LA_GATE_SIGMOID: return backward_g<LA_GATE_SIGMOID>(p, dev);
-    }
-    return cudaErrorInvalidValue;
-}
+cudaError_t recurrence_forward(const RecProblem &p) { return choose_gate<Forward>(p); }
+cudaError_t recurrence_backward(const RecProblem &p) { return choose_gate<Backward>(p); }
 
 }  // namespace la

@@ -33,7 +33,8 @@ EXPORTED = ("la_workspace_bytes", "la_forward_noncausal", "la_forward_causal", "
             "la_backward_noncausal", "la_forward_causal_varlen", "la_decode_steps",
             "la_feature_dim", "la_variant_workspace_bytes", "la_forward_causal_variant",
             "la_forward_noncausal_variant", "la_decode_step_variant", "la_checked_build",
-            "la_debug_inject_bounds", "la_recurrence_forward", "la_recurrence_step",
+            "la_debug_inject_bounds", "la_recurrence_workspace_bytes",
+            "la_recurrence_forward", "la_recurrence_step",
             "la_recurrence_backward", "la_layernorm_forward", "la_layernorm_workspace_bytes",
             "la_layernorm_backward", "la_grad_workspace_bytes", "la_grad_norm", "la_grad_clip")
 
@@ -150,11 +151,13 @@ def _load(path: str) -> ctypes.CDLL:
         L.la_debug_inject_bounds.argtypes = [i]
         ll, f = ctypes.c_longlong, ctypes.c_float
         L.la_recurrence_forward.restype = i
-        L.la_recurrence_forward.argtypes = [la_view, la_view, la_view, vp, la_shape, i, vp, vp, vp]
+        L.la_recurrence_forward.argtypes = [la_view, la_view, la_view, vp, la_shape, i, vp, vp, vp, sz, vp]
+        L.la_recurrence_workspace_bytes.restype = sz
+        L.la_recurrence_workspace_bytes.argtypes = [la_shape]
         L.la_recurrence_step.restype = i
         L.la_recurrence_step.argtypes = [la_view, la_view, la_view, la_shape, i, vp, vp]
         L.la_recurrence_backward.restype = i
-        L.la_recurrence_backward.argtypes = [la_view] * 6 + [vp, la_shape, i, vp, vp, vp, vp]
+        L.la_recurrence_backward.argtypes = [la_view] * 6 + [vp, la_shape, i, vp, vp, vp, vp, sz, vp]
         L.la_layernorm_forward.restype = i
         L.la_layernorm_forward.argtypes = [la_rows] * 4 + [vp, vp, vp, vp, ll, i, i, f, vp]
         L.la_layernorm_workspace_bytes.restype = sz
@@ -505,6 +508,13 @@ def _lens(lens, B):
         _contig(lens)
 
 
+def _recurrence_ws(s, stream, device):
+    need = lib().la_recurrence_workspace_bytes(s)
+    if need == _SIZE_MAX:   # the call itself says what is wrong
+        need = 0
+    return need, _empty(stream, (need,), torch.uint8, device) if need else None
+
+
 def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens=None, stream=None):
     """Gated linear recurrence h_t = a_t h_{t-1} + u_t of every channel, out_t = h_t.
 
@@ -524,8 +534,9 @@ def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens
     _same_place(x, g=g, out=out, h0=h0, hN=hN, lens=lens)
     if out is None:
         out = _empty(stream, x.shape, x.dtype, x.device)
+    need, ws = _recurrence_ws(s, stream, x.device)
     st = lib().la_recurrence_forward(_view("x", x), _view("g", g), _view("out", out), _ptr(lens), s, code, _ptr(h0),
-                                     _ptr(hN), _stream(stream, x.device))
+                                     _ptr(hN), _ptr(ws), need, _stream(stream, x.device))
     _check(st, "la_recurrence_forward")
     return out
 
@@ -569,9 +580,10 @@ def la_recurrence_backward(x, g, out, dout, gate="sigmoid", h0=None, dhN=None, d
         dx = _empty(stream, g.shape, g.dtype, g.device)
     if dg is None:
         dg = _empty(stream, g.shape, g.dtype, g.device)
+    need, ws = _recurrence_ws(s, stream, g.device)
     st = lib().la_recurrence_backward(_view("x", x), _view("g", g), _view("out", out), _view("dout", dout),
                                       _view("dx", dx), _view("dg", dg), _ptr(lens), s, code, _ptr(h0), _ptr(dhN),
-                                      _ptr(dh0), _stream(stream, g.device))
+                                      _ptr(dh0), _ptr(ws), need, _stream(stream, g.device))
     _check(st, "la_recurrence_backward")
     return dx, dg
 
