@@ -156,12 +156,10 @@ la_status la_layernorm_forward(la_rows x, la_rows res, la_rows sum, la_rows y, c
     if ((same(sum.data, x.data) && sum.stride != x.stride) || (same(sum.data, res.data) && sum.stride != res.stride))
         return LA_ERR_INVALID_ARG;
     if (same(mean, rstd)) return LA_ERR_INVALID_ARG;
-    const DeviceInfo *dev = device_info();
-    if (!dev) return LA_ERR_CUDA;
     NormProblem p{};
     p.x = x, p.res = res, p.sum = sum, p.y = y, p.w = w, p.b = b, p.mean = mean, p.rstd = rstd;
     p.rows = rows, p.C = C, p.dtype = dtype, p.eps = eps, p.stream = (cudaStream_t)stream;
-    return from_cuda(layernorm_forward(p, *dev));
+    return from_cuda(layernorm_forward(p));
 }
 
 size_t la_layernorm_workspace_bytes(long long rows, int C, la_dtype dtype) {
@@ -191,13 +189,11 @@ la_status la_layernorm_backward(la_rows dy, la_rows s, la_rows dsum, la_rows ds,
         if (same(ds.data, i)) return LA_ERR_INVALID_ARG;
     const size_t need = layernorm_ws_bytes(rows, C);
     if ((dw || db) && (ws_bytes < need || !aligned(workspace, 16))) return LA_ERR_INVALID_ARG;
-    const DeviceInfo *dev = device_info();
-    if (!dev) return LA_ERR_CUDA;
     NormProblem p{};
     p.x = s, p.res = dsum, p.y = dy, p.ds = ds, p.w = w, p.mean = const_cast<float *>(mean);
     p.rstd = const_cast<float *>(rstd), p.dw = dw, p.db = db;
     p.rows = rows, p.C = C, p.dtype = dtype, p.ws = workspace, p.stream = (cudaStream_t)stream;
-    return from_cuda(layernorm_backward(p, *dev));
+    return from_cuda(layernorm_backward(p));
 }
 
 size_t la_grad_workspace_bytes(int count) { return count < 0 ? (size_t)-1 : grad_ws_bytes(count); }

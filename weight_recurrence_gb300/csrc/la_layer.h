@@ -42,8 +42,8 @@ struct NormProblem {
 
 constexpr int kNormMaxC = 16384;
 size_t layernorm_ws_bytes(long long rows, int C);
-cudaError_t layernorm_forward(const NormProblem &p, const DeviceInfo &dev);
-cudaError_t layernorm_backward(const NormProblem &p, const DeviceInfo &dev);
+cudaError_t layernorm_forward(const NormProblem &p);
+cudaError_t layernorm_backward(const NormProblem &p);
 
 size_t grad_ws_bytes(int count);
 // max_norm < 0: the norm alone

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -440,34 +441,51 @@ def la_decode_step_variant(q, k, v, S, var: la_variant, z=None, beta=None, y=Non
 # ------------------------------------------- the layer around the attention
 # These calls check shapes, types and devices here (the library sees pointers,
 # sizes and strides only), take views, and allocate what they return or need
-# as workspace on the stream that they launch on.
+# as workspace on the stream that they launch on.  A decoded token's call is a
+# few microseconds of GPU time, so the checks are kept short.
 
 def _need(ok, what: str):
     if not ok:
         raise ValueError(what)
 
 
-def _same_place(ref, **ts):
-    """Every tensor is on ref's CUDA device, which is the current one."""
-    _need(ref.is_cuda, "tensors must be on a CUDA device")
-    _need(ref.device.index == torch.cuda.current_device(), "tensors must be on the current CUDA device")
-    for name, t in ts.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, ref.device))
-
-
-def _empty(stream, shape, dtype, device):
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):   # memory of the stream that uses it
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _like(name, t, shape, dtype):
+def _like(name, t, shape, dtype, dev: int):
+    """t (or None) has this shape, type and device."""
     if t is not None:
-        _need(tuple(t.shape) == tuple(shape), "%s must have shape %s" % (name, tuple(shape)))
-        if t.dtype != dtype:
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s" % (name, tuple(shape)))
+        if t.dtype is not dtype:
             raise TypeError("%s must be %s" % (name, dtype))
+        if t.get_device() != dev:
+            raise ValueError("%s must be on the same device as the rest" % name)
+
+
+def _state(name, t, shape, dev: int):
+    """_like for what the library takes as a plain fp32 array."""
+    if t is not None:
+        _like(name, t, shape, torch.float32, dev)
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _launch_stream(stream, dev: int) -> int:
+    """The stream's handle; dev has to be the current CUDA device."""
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _empty(stream, like, shape, dtype):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):   # memory of the stream that uses it
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _view(name, t, step: bool = False) -> la_view:
@@ -475,44 +493,44 @@ def _view(name, t, step: bool = False) -> la_view:
     if t is None:
         return la_view(None, 0, 0, 0)
     st = t.stride()
-    _need(st[-1] == 1 or t.shape[-1] <= 1, "%s: the channels must be contiguous" % name)
-    sn = 0 if step else st[-2]
-    lead = len(st) - (1 if step else 2)
-    return la_view(t.data_ptr(), st[0], st[1] if lead == 2 else 0, sn)
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError("%s: the channels must be contiguous" % name)
+    if step:
+        return la_view(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0, 0)
+    return la_view(t.data_ptr(), st[0], st[1] if len(st) == 4 else 0, st[-2])
 
 
 def _rec_shape(x, step: bool) -> la_shape:
-    lead = x.dim() - (1 if step else 2)
-    _need(lead in (1, 2), "x must be [B,D] or [B,H,D]" if step else "x must be [B,N,D] or [B,H,N,D]")
-    _need(x.shape[-1] >= 1, "x must have a channel")
-    B, H = x.shape[0], (x.shape[1] if lead == 2 else 1)
-    return la_shape(B, H, 1 if step else x.shape[-2], x.shape[-1], 0, _dtype_code(x.dtype))
+    sh = x.shape
+    lead = len(sh) - (1 if step else 2)
+    if lead not in (1, 2):
+        raise ValueError("x must be [B,D] or [B,H,D]" if step else "x must be [B,N,D] or [B,H,N,D]")
+    if sh[-1] < 1:
+        raise ValueError("x must have a channel")
+    return la_shape(sh[0], sh[1] if lead == 2 else 1, 1 if step else sh[-2], sh[-1], 0, _dtype_code(x.dtype))
 
 
 def _gate_code(gate: str) -> int:
-    _need(gate in LA_GATE, "gate must be one of %s" % ", ".join(LA_GATE))
-    return LA_GATE[gate]
+    code = LA_GATE.get(gate)
+    if code is None:
+        raise ValueError("gate must be one of %s" % ", ".join(LA_GATE))
+    return code
 
 
-def _state(name, t, shape):
-    if t is not None:
-        _like(name, t, shape, torch.float32)
-        _contig(t)
-
-
-def _lens(lens, B):
+def _lens(lens, B: int, dev: int):
     if lens is not None:
         if lens.dtype != torch.int32:
             raise TypeError("lens must be torch.int32")
-        _need(tuple(lens.shape) == (B,), "lens must have shape (%d,)" % B)
-        _contig(lens)
+        _need(lens.shape == (B,), "lens must have shape (%d,)" % B)
+        _need(lens.is_contiguous(), "lens must be contiguous")
+        _need(lens.get_device() == dev, "lens must be on the same device as the rest")
 
 
-def _recurrence_ws(s, stream, device):
+def _recurrence_ws(s, stream, like):
     need = lib().la_recurrence_workspace_bytes(s)
     if need == _SIZE_MAX:   # the call itself says what is wrong
         need = 0
-    return need, _empty(stream, (need,), torch.uint8, device) if need else None
+    return need, _empty(stream, like, (need,), torch.uint8) if need else None
 
 
 def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens=None, stream=None):
@@ -525,18 +543,19 @@ def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens
     rows past a length are 0.  Returns out."""
     s = _rec_shape(x, False)
     code = _gate_code(gate)
-    _like("g", g, x.shape, x.dtype)
-    _like("out", out, x.shape, x.dtype)
+    dev = x.get_device()
+    _like("g", g, x.shape, x.dtype, dev)
+    _like("out", out, x.shape, x.dtype, dev)
     state = x.shape[:-2] + x.shape[-1:]
-    _state("h0", h0, state)
-    _state("hN", hN, state)
-    _lens(lens, x.shape[0])
-    _same_place(x, g=g, out=out, h0=h0, hN=hN, lens=lens)
+    _state("h0", h0, state, dev)
+    _state("hN", hN, state, dev)
+    _lens(lens, s.B, dev)
+    sp = _launch_stream(stream, dev)
     if out is None:
-        out = _empty(stream, x.shape, x.dtype, x.device)
-    need, ws = _recurrence_ws(s, stream, x.device)
-    st = lib().la_recurrence_forward(_view("x", x), _view("g", g), _view("out", out), _ptr(lens), s, code, _ptr(h0),
-                                     _ptr(hN), _ptr(ws), need, _stream(stream, x.device))
+        out = _empty(stream, x, x.shape, x.dtype)
+    need, ws = _recurrence_ws(s, stream, x)
+    st = lib().la_recurrence_forward(_view("x", x), _view("g", g), _view("out", out), _addr(lens), s, code, _addr(h0),
+                                     _addr(hN), _addr(ws), need, sp)
     _check(st, "la_recurrence_forward")
     return out
 
@@ -546,15 +565,16 @@ def la_recurrence_step(x, g, h, gate="sigmoid", y=None, stream=None):
     the same shape, updated in place.  Returns y = h in x's type."""
     s = _rec_shape(x, True)
     code = _gate_code(gate)
-    _like("g", g, x.shape, x.dtype)
-    _like("y", y, x.shape, x.dtype)
+    dev = x.get_device()
     _need(h is not None, "h is required")
-    _state("h", h, x.shape)
-    _same_place(x, g=g, y=y, h=h)
+    _like("g", g, x.shape, x.dtype, dev)
+    _like("y", y, x.shape, x.dtype, dev)
+    _state("h", h, x.shape, dev)
+    sp = _launch_stream(stream, dev)
     if y is None:
-        y = _empty(stream, x.shape, x.dtype, x.device)
-    st = lib().la_recurrence_step(_view("x", x, True), _view("g", g, True), _view("y", y, True), s, code, _ptr(h),
-                                  _stream(stream, x.device))
+        y = _empty(stream, x, x.shape, x.dtype)
+    st = lib().la_recurrence_step(_view("x", x, True), _view("g", g, True), _view("y", y, True), s, code,
+                                  h.data_ptr(), sp)
     _check(st, "la_recurrence_step")
     return y
 
@@ -568,22 +588,23 @@ def la_recurrence_backward(x, g, out, dout, gate="sigmoid", h0=None, dhN=None, d
     s = _rec_shape(g, False)
     code = _gate_code(gate)
     _need(x is not None or gate != "sigmoid", "the sigmoid gate needs x")
+    dev = g.get_device()
     for name, t in (("x", x), ("out", out), ("dout", dout), ("dx", dx), ("dg", dg)):
-        _like(name, t, g.shape, g.dtype)
+        _like(name, t, g.shape, g.dtype, dev)
     state = g.shape[:-2] + g.shape[-1:]
-    _state("h0", h0, state)
-    _state("dhN", dhN, state)
-    _state("dh0", dh0, state)
-    _lens(lens, g.shape[0])
-    _same_place(g, x=x, out=out, dout=dout, h0=h0, dhN=dhN, dh0=dh0, lens=lens, dx=dx, dg=dg)
+    _state("h0", h0, state, dev)
+    _state("dhN", dhN, state, dev)
+    _state("dh0", dh0, state, dev)
+    _lens(lens, s.B, dev)
+    sp = _launch_stream(stream, dev)
     if dx is None:
-        dx = _empty(stream, g.shape, g.dtype, g.device)
+        dx = _empty(stream, g, g.shape, g.dtype)
     if dg is None:
-        dg = _empty(stream, g.shape, g.dtype, g.device)
-    need, ws = _recurrence_ws(s, stream, g.device)
+        dg = _empty(stream, g, g.shape, g.dtype)
+    need, ws = _recurrence_ws(s, stream, g)
     st = lib().la_recurrence_backward(_view("x", x), _view("g", g), _view("out", out), _view("dout", dout),
-                                      _view("dx", dx), _view("dg", dg), _ptr(lens), s, code, _ptr(h0), _ptr(dhN),
-                                      _ptr(dh0), _ptr(ws), need, _stream(stream, g.device))
+                                      _view("dx", dx), _view("dg", dg), _addr(lens), s, code, _addr(h0), _addr(dhN),
+                                      _addr(dh0), _addr(ws), need, sp)
     _check(st, "la_recurrence_backward")
     return dx, dg
 
@@ -608,37 +629,35 @@ def _rows(name, t) -> la_rows:
     return la_rows(t.data_ptr(), sh[-1] if stride is None else stride)
 
 
-def _row_count(t) -> int:
-    return t.numel() // t.shape[-1]
-
-
 def la_layernorm_forward(x, w=None, b=None, eps=1e-5, res=None, y=None, sum=None, mean=None, rstd=None, stats=True,
                          stream=None):
     """Layer norm of the rows of x [..., C], with the residual sum s = x + res
     in front when res is given.  w, b: fp32 [C] or None.  Returns (y, s, mean,
     rstd): s is x itself without res; mean and rstd (fp32, for the backward)
     are None with stats=False.  sum: where s goes (may be x or res)."""
-    _need(x.dim() >= 1 and x.shape[-1] >= 1, "x must have rows of at least one value")
-    code = _dtype_code(x.dtype)
-    C = x.shape[-1]
-    for name, t in (("res", res), ("sum", sum), ("y", y)):
-        _like(name, t, x.shape, x.dtype)
-    for name, t, shape in (("w", w, (C,)), ("b", b, (C,)), ("mean", mean, x.shape[:-1]), ("rstd", rstd, x.shape[:-1])):
-        _state(name, t, shape)
+    sh, dtype, dev = x.shape, x.dtype, x.get_device()
+    _need(len(sh) >= 1 and sh[-1] >= 1, "x must have rows of at least one value")
+    code = _dtype_code(dtype)
+    C, lead = sh[-1], sh[:-1]
     _need(sum is None or res is not None, "sum needs res")
-    _same_place(x, res=res, sum=sum, y=y, w=w, b=b, mean=mean, rstd=rstd)
+    _need(stats or (mean is None and rstd is None), "mean and rstd need stats")
+    _like("res", res, sh, dtype, dev)
+    _like("sum", sum, sh, dtype, dev)
+    _like("y", y, sh, dtype, dev)
+    _state("w", w, (C,), dev)
+    _state("b", b, (C,), dev)
+    _state("mean", mean, lead, dev)
+    _state("rstd", rstd, lead, dev)
+    sp = _launch_stream(stream, dev)
     if y is None:
-        y = _empty(stream, x.shape, x.dtype, x.device)
+        y = _empty(stream, x, sh, dtype)
     if res is not None and sum is None:
-        sum = _empty(stream, x.shape, x.dtype, x.device)
+        sum = _empty(stream, x, sh, dtype)
     if stats:
-        mean = _empty(stream, x.shape[:-1], torch.float32, x.device) if mean is None else mean
-        rstd = _empty(stream, x.shape[:-1], torch.float32, x.device) if rstd is None else rstd
-    else:
-        _need(mean is None and rstd is None, "mean and rstd need stats")
-    st = lib().la_layernorm_forward(_rows("x", x), _rows("res", res), _rows("sum", sum), _rows("y", y), _ptr(w),
-                                    _ptr(b), _ptr(mean), _ptr(rstd), _row_count(x), C, code, eps,
-                                    _stream(stream, x.device))
+        mean = _empty(stream, x, lead, torch.float32) if mean is None else mean
+        rstd = _empty(stream, x, lead, torch.float32) if rstd is None else rstd
+    st = lib().la_layernorm_forward(_rows("x", x), _rows("res", res), _rows("sum", sum), _rows("y", y), _addr(w),
+                                    _addr(b), _addr(mean), _addr(rstd), x.numel() // C, C, code, eps, sp)
     _check(st, "la_layernorm_forward")
     return y, (x if res is None else sum), mean, rstd
 
@@ -647,58 +666,79 @@ def la_layernorm_backward(dy, s, w, mean, rstd, dsum=None, ds=None, dw=None, db=
     """Gradients (ds, dw, db) of la_layernorm_forward given dy = dL/dy, the s,
     mean and rstd it returned and, where s went on as the residual stream,
     dsum = dL/ds.  ds is the gradient of x and of res; w may be None (1)."""
-    _need(dy.dim() >= 1 and dy.shape[-1] >= 1, "dy must have rows of at least one value")
-    code = _dtype_code(dy.dtype)
-    C = dy.shape[-1]
-    for name, t in (("s", s), ("dsum", dsum), ("ds", ds)):
-        _like(name, t, dy.shape, dy.dtype)
-    for name, t, shape in (("w", w, (C,)), ("dw", dw, (C,)), ("db", db, (C,)), ("mean", mean, dy.shape[:-1]),
-                           ("rstd", rstd, dy.shape[:-1])):
-        _state(name, t, shape)
+    sh, dtype, dev = dy.shape, dy.dtype, dy.get_device()
+    _need(len(sh) >= 1 and sh[-1] >= 1, "dy must have rows of at least one value")
+    code = _dtype_code(dtype)
+    C, lead = sh[-1], sh[:-1]
     _need(mean is not None and rstd is not None, "mean and rstd are required")
-    _same_place(dy, s=s, dsum=dsum, ds=ds, w=w, mean=mean, rstd=rstd, dw=dw, db=db)
+    _like("s", s, sh, dtype, dev)
+    _like("dsum", dsum, sh, dtype, dev)
+    _like("ds", ds, sh, dtype, dev)
+    _state("w", w, (C,), dev)
+    _state("mean", mean, lead, dev)
+    _state("rstd", rstd, lead, dev)
+    _state("dw", dw, (C,), dev)
+    _state("db", db, (C,), dev)
+    sp = _launch_stream(stream, dev)
     if ds is None:
-        ds = _empty(stream, dy.shape, dy.dtype, dy.device)
+        ds = _empty(stream, dy, sh, dtype)
     if dw is None:
-        dw = _empty(stream, (C,), torch.float32, dy.device)
+        dw = _empty(stream, dy, (C,), torch.float32)
     if db is None:
-        db = _empty(stream, (C,), torch.float32, dy.device)
-    rows = _row_count(dy)
+        db = _empty(stream, dy, (C,), torch.float32)
+    rows = dy.numel() // C
     need = lib().la_layernorm_workspace_bytes(rows, C, code)
     if need == _SIZE_MAX:
         raise LAError(LA_ERR_UNSUPPORTED, "la_layernorm_workspace_bytes")
-    ws = _empty(stream, (need,), torch.uint8, dy.device) if need else None
-    st = lib().la_layernorm_backward(_rows("dy", dy), _rows("s", s), _rows("dsum", dsum), _rows("ds", ds), _ptr(w),
-                                     _ptr(mean), _ptr(rstd), _ptr(dw), _ptr(db), rows, C, code, _ptr(ws), need,
-                                     _stream(stream, dy.device))
+    ws = _empty(stream, dy, (need,), torch.uint8) if need else None
+    st = lib().la_layernorm_backward(_rows("dy", dy), _rows("s", s), _rows("dsum", dsum), _rows("ds", ds), _addr(w),
+                                     mean.data_ptr(), rstd.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, C, code,
+                                     _addr(ws), need, sp)
     _check(st, "la_layernorm_backward")
     return ds, dw, db
 
 
-def _grad_list(grads, out):
-    grads = list(grads)
+_tensor_code = {torch.float32: LA_DTYPE_F32, torch.bfloat16: LA_DTYPE_BF16}
+
+
+def _grad_call(name, grads, out, norm, stream, *args):
+    """Packs the la_tensor table (one struct.pack for all of it) and calls."""
     _need(len(grads) > 0, "no tensors")
-    out = [None] * len(grads) if out is None else list(out)
-    _need(len(out) == len(grads), "out must have one tensor per gradient")
-    table = (la_tensor * len(grads))()
-    for e, t, d in zip(table, grads, out):
-        _contig(t)
-        e.src, e.n, e.dtype = t.data_ptr(), t.numel(), _dtype_code(t.dtype)
-        if d is not None:
-            _like("out", d, t.shape, t.dtype)
-            _contig(d)
-            e.dst = d.data_ptr()
-    first = grads[0]
-    _same_place(first)
-    for t in grads + [d for d in out if d is not None]:
-        _need(t.device == first.device, "all tensors must be on one device")
-    return table, first.device
+    dev = grads[0].get_device()
+    for t in grads:
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        if t.dtype not in _tensor_code:
+            raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
+        if t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    if out is None:
+        dst = [0] * len(grads)
+    elif out is grads:
+        dst = [t.data_ptr() for t in grads]
+    else:
+        _need(len(out) == len(grads), "out must have one tensor per gradient")
+        for t, d in zip(grads, out):
+            _like("out", d, t.shape, t.dtype, dev)
+            if not d.is_contiguous():
+                raise ValueError("out must be contiguous")
+        dst = [t.data_ptr() for t in out]
+    _state("norm", norm, (), dev)
+    sp = _launch_stream(stream, dev)
+    if norm is None:
+        norm = _empty(stream, grads[0], (), torch.float32)
+    table = struct.pack("PPqi4x" * len(grads), *[v for t, d in zip(grads, dst)
+                                                 for v in (t.data_ptr(), d, t.numel(), _tensor_code[t.dtype])])
+    need = lib().la_grad_workspace_bytes(len(grads))
+    ws = _empty(stream, grads[0], (need,), torch.uint8)
+    st = getattr(lib(), name)(table, len(grads), *args, norm.data_ptr(), ws.data_ptr(), need, sp)
+    _check(st, name)
+    return norm
 
 
 def la_grad_norm(grads, norm=None, stream=None):
     """Global norm sqrt(sum of all squares) over a list of tensors, an fp32 scalar on the device."""
-    table, device = _grad_list(grads, None)
-    return _grad_call("la_grad_norm", table, device, norm, stream)
+    return _grad_call("la_grad_norm", list(grads), None, norm, stream)
 
 
 def la_grad_clip(grads, max_norm, out=None, norm=None, stream=None):
@@ -706,19 +746,7 @@ def la_grad_clip(grads, max_norm, out=None, norm=None, stream=None):
     norm, in place or into the tensors of out; returns the norm (an fp32
     scalar on the device)."""
     grads = list(grads)
-    table, device = _grad_list(grads, grads if out is None else out)
-    return _grad_call("la_grad_clip", table, device, norm, stream, float(max_norm))
-
-
-def _grad_call(name, table, device, norm, stream, *args):
-    _state("norm", norm, ())
-    if norm is None:
-        norm = _empty(stream, (), torch.float32, device)
-    need = lib().la_grad_workspace_bytes(len(table))
-    ws = _empty(stream, (need,), torch.uint8, device)
-    st = getattr(lib(), name)(table, len(table), *args, _ptr(norm), _ptr(ws), need, _stream(stream, device))
-    _check(st, name)
-    return norm
+    return _grad_call("la_grad_clip", grads, grads if out is None else list(out), norm, stream, float(max_norm))
 
 
 def la_get_last_error(stream=None, device=None) -> int:
