@@ -2,33 +2,9 @@
 // the value g of a token and channel, for V neighbouring channels at a time.
 #pragma once
 
-#include "la_common.cuh"
+#include "la_pair.cuh"
 
 namespace la {
-
-// Two fp32 operations in one instruction (each half rounds as the single one).
-__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<unsigned long long &>(r))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)),
-          "l"(reinterpret_cast<unsigned long long &>(c)));
-    return r;
-}
-__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) {
-    float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<unsigned long long &>(r))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return r;
-}
-__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
-    float2 r;
-    asm("add.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<unsigned long long &>(r))
-        : "l"(reinterpret_cast<unsigned long long &>(a)), "l"(reinterpret_cast<unsigned long long &>(b)));
-    return r;
-}
 
 // V fp32 values, as pairs where V is even.
 template <int V> struct Lanes {

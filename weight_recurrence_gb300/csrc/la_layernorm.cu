@@ -9,8 +9,9 @@
 // registers; the sums of all groups are added in a fixed order.
 #include <algorithm>
 
-#include "la_common.cuh"
 #include "la_layer.h"
+#include "la_pair.cuh"
+#include "tc_ptx.cuh"
 
 namespace la {
 namespace {
@@ -59,41 +60,92 @@ template <typename T, int TPR, int K, bool WIDE> struct Share {
             }
         }
     }
-    __device__ __forceinline__ float get(int i) const {
-        if constexpr (WIDE) {
-            const unsigned w = (&piece[i / VEC].x)[(i % VEC) * sizeof(T) / 4];
-            if constexpr (sizeof(T) == 4) return __uint_as_float(w);
-            else return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
+    // elements 2i and 2i + 1
+    __device__ __forceinline__ float2 get(int i) const {
+        if constexpr (WIDE && sizeof(T) == 4)
+            return i % 2 ? make_float2(__uint_as_float(piece[i / 2].z), __uint_as_float(piece[i / 2].w))
+                         : make_float2(__uint_as_float(piece[i / 2].x), __uint_as_float(piece[i / 2].y));
+        else if constexpr (WIDE)
+            return get_pair((&piece[i / 4].x)[i % 4]);
+        else if constexpr (sizeof(T) == 4)
+            return make_float2(__uint_as_float(one[2 * i]), __uint_as_float(one[2 * i + 1]));
+        else
+            return make_float2(__uint_as_float((unsigned)one[2 * i] << 16),
+                               __uint_as_float((unsigned)one[2 * i + 1] << 16));
+    }
+    __device__ __forceinline__ void set(int i, float2 v) {
+        if constexpr (WIDE && sizeof(T) == 4) {
+            (&piece[i / 2].x)[i % 2 * 2] = __float_as_uint(v.x);
+            (&piece[i / 2].x)[i % 2 * 2 + 1] = __float_as_uint(v.y);
+        } else if constexpr (WIDE) {
+            (&piece[i / 4].x)[i % 4] = put_pair(v);
+        } else if constexpr (sizeof(T) == 4) {
+            one[2 * i] = __float_as_uint(v.x);
+            one[2 * i + 1] = __float_as_uint(v.y);
         } else {
-            if constexpr (sizeof(T) == 4) return __uint_as_float(one[i]);
-            else return __uint_as_float((unsigned)one[i] << 16);
+            const unsigned w = put_pair(v);
+            one[2 * i] = (unsigned short)w;
+            one[2 * i + 1] = (unsigned short)(w >> 16);
         }
     }
-    __device__ __forceinline__ void set(const float (&v)[E]) {
-        if constexpr (sizeof(T) == 4) {
+};
+
+// A thread's shares of NT tensors on their way, S rows deep: 16-byte pieces
+// through its own places in shared memory (no other thread touches them, so no
+// barrier), single values through registers, one row ahead.  S = 0: loaded when
+// they are taken (the widest rows, whose threads have no room for more).
+template <typename T, int TPR, int K, bool WIDE, int NT, int S> struct Feed {
+    using Sh = Share<T, TPR, K, WIDE>;
+    static constexpr bool kShared = WIDE && S > 0, kHeld = !WIDE && S > 0;
+    static constexpr int DEPTH = kShared ? S : 1;
+    static constexpr size_t bytes(int threads) { return kShared ? (size_t)S * NT * K * 16 * threads : 0; }
+    uint4 *slot;
+    int threads, lane, C;
+    Sh held[kHeld ? NT : 1];
+
+    __device__ __forceinline__ void fetch(int stage, int k, const T *row) {
+        if constexpr (kShared) {
 #pragma unroll
-            for (int i = 0; i < E; i++) {
-                if constexpr (WIDE) (&piece[i / VEC].x)[i % VEC] = __float_as_uint(v[i]);
-                else one[i] = __float_as_uint(v[i]);
+            for (int i = 0; i < K; i++) {
+                const int c = (i * TPR + lane) * Sh::VEC;
+                if (c < C)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     tc::smem_u32(&slot[((stage * NT + k) * K + i) * threads])),
+                                 "l"(row + c)
+                                 : "memory");
             }
-        } else if constexpr (WIDE) {
-#pragma unroll
-            for (int i = 0; i < E; i += 2) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(v[i], v[i + 1]);
-                (&piece[i / VEC].x)[(i % VEC) / 2] = *reinterpret_cast<const unsigned *>(&p);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; i++) one[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+        } else if constexpr (kHeld) {
+            held[k].load(row, lane, C);
         }
+    }
+    __device__ __forceinline__ void commit() {
+        if constexpr (kShared) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void wait() {
+        if constexpr (kShared) asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    }
+    // columns past C are 0; row: the one that was fetched into the stage
+    __device__ __forceinline__ Sh take(int stage, int k, const T *row) {
+        Sh r;
+        if constexpr (kShared) {
+#pragma unroll
+            for (int i = 0; i < K; i++)
+                r.piece[i] = (i * TPR + lane) * Sh::VEC < C ? slot[((stage * NT + k) * K + i) * threads]
+                                                            : make_uint4(0, 0, 0, 0);
+        } else if constexpr (kHeld) {
+            r = held[k];
+        } else {
+            r.load(row, lane, C);
+        }
+        return r;
     }
 };
 
 // fp32 parameters of the thread's columns; a null pointer gives `none`.
 template <int TPR, int K, int VEC, bool WIDE>
-__device__ __forceinline__ void load_columns(float (&v)[K * VEC], const float *p, int lane, int C, float none) {
+__device__ __forceinline__ void load_columns(float2 (&v)[K * VEC / 2], const float *p, int lane, int C, float none) {
 #pragma unroll
-    for (int i = 0; i < K * VEC; i++) v[i] = none;
+    for (int i = 0; i < K * VEC / 2; i++) v[i] = make_float2(none, none);
     if (p == nullptr) return;
     if constexpr (WIDE) {
 #pragma unroll
@@ -101,13 +153,13 @@ __device__ __forceinline__ void load_columns(float (&v)[K * VEC], const float *p
             const int c = ((i / VEC) * TPR + lane) * VEC + i % VEC;
             if (c < C) {
                 const float4 q = *reinterpret_cast<const float4 *>(p + c);
-                v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+                v[i / 2] = make_float2(q.x, q.y), v[i / 2 + 1] = make_float2(q.z, q.w);
             }
         }
     } else {
 #pragma unroll
         for (int i = 0; i < K * VEC; i++)
-            if (i * TPR + lane < C) v[i] = p[i * TPR + lane];
+            if (i * TPR + lane < C) (i % 2 ? v[i / 2].y : v[i / 2].x) = p[i * TPR + lane];
     }
 }
 
@@ -147,161 +199,191 @@ template <typename T> __device__ __forceinline__ T *row_at(const la_rows &v, lon
 
 template <int TPR> constexpr int threads_of() { return TPR > 256 ? TPR : TPR > 32 ? TPR : 256; }
 
-// ROWS rows of a group are on their way together where a row is short.
-template <typename T, int TPR, int K, bool WIDE, int ROWS>
-__global__ void __launch_bounds__(threads_of<TPR>()) ln_forward_kernel(NormProblem p) {
-    using S = Share<T, TPR, K, WIDE>;
-    constexpr int E = S::E, GROUPS = threads_of<TPR>() / TPR;
+// Groups walk over rows gridDim * GROUPS apart.
+template <typename T, int TPR, int K, bool WIDE, int S, int CTAS>
+__global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_forward_kernel(NormProblem p) {
+    using F = Feed<T, TPR, K, WIDE, 2, S>;
+    using Sh = typename F::Sh;
+    constexpr int E2 = Sh::E / 2, GROUPS = threads_of<TPR>() / TPR;
     __shared__ float sh[2][1][TPR / 32 > 0 ? TPR / 32 : 1];
+    extern __shared__ __align__(16) uint4 smem[];
     Sums<TPR, 1> sum{sh};
     pdl_wait_cta();
-    const int lane = threadIdx.x % TPR;
-    const long long r0 = ((long long)blockIdx.x * GROUPS + threadIdx.x / TPR) * ROWS;
-    float v[ROWS][E];
-    {
-        S a[ROWS], b[ROWS];
-#pragma unroll
-        for (int j = 0; j < ROWS; j++)
-            if (r0 + j < p.rows) {
-                a[j].load(row_at<T>(p.x, r0 + j), lane, p.C);
-                if (p.res.data) b[j].load(row_at<T>(p.res, r0 + j), lane, p.C);
-            }
-#pragma unroll
-        for (int j = 0; j < ROWS; j++) {
-#pragma unroll
-            for (int i = 0; i < E; i++) v[j][i] = a[j].get(i);
-            if (p.res.data) {
-#pragma unroll
-                for (int i = 0; i < E; i++) v[j][i] += b[j].get(i);
-                a[j].set(v[j]);   // the stream as it is kept, and normalised
-                if (p.sum.data && r0 + j < p.rows) a[j].store(row_at<T>(p.sum, r0 + j), lane, p.C);
-#pragma unroll
-                for (int i = 0; i < E; i++) v[j][i] = a[j].get(i);
-            }
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    F feed{smem + threadIdx.x, threads_of<TPR>(), lane, p.C};
+    const long long step = (long long)gridDim.x * GROUPS;
+    auto fetch = [&](long long r, int stage) {
+        if (r < p.rows) {
+            feed.fetch(stage, 0, row_at<T>(p.x, r));
+            if (p.res.data) feed.fetch(stage, 1, row_at<T>(p.res, r));
         }
-    }
-    float w[E], b[E];
-    load_columns<TPR, K, S::VEC, WIDE>(w, p.w, lane, p.C, 1.f);
-    load_columns<TPR, K, S::VEC, WIDE>(b, p.b, lane, p.C, 0.f);
+        feed.commit();
+    };
 #pragma unroll
-    for (int j = 0; j < ROWS; j++) {
-        float s[1] = {0.f};
+    for (int i = 0; i < F::DEPTH; i++) fetch((long long)blockIdx.x * GROUPS + group + i * step, i);
+    float2 w[E2], b[E2];
+    load_columns<TPR, K, Sh::VEC, WIDE>(w, p.w, lane, p.C, 1.f);
+    load_columns<TPR, K, Sh::VEC, WIDE>(b, p.b, lane, p.C, 0.f);
+    int stage = 0;
+    // a CTA's groups run the same number of rounds (their barriers and shuffles meet)
+    for (long long base = (long long)blockIdx.x * GROUPS; base < p.rows; base += step) {
+        const long long r = base + group;
+        const long long at = min(r, p.rows - 1);   // a group without a row takes along
+        feed.wait();
+        Sh a = feed.take(stage, 0, row_at<T>(p.x, at));
+        float2 v[E2];
 #pragma unroll
-        for (int i = 0; i < E; i++) s[0] += v[j][i];   // columns past C are 0
+        for (int i = 0; i < E2; i++) v[i] = a.get(i);
+        if (p.res.data) {
+            const Sh c = feed.take(stage, 1, row_at<T>(p.res, at));
+#pragma unroll
+            for (int i = 0; i < E2; i++) {   // the stream as it is kept, and normalised
+                a.set(i, add_pair(v[i], c.get(i)));
+                v[i] = a.get(i);
+            }
+            if (p.sum.data && r < p.rows) a.store(row_at<T>(p.sum, r), lane, p.C);
+        }
+        fetch(r + F::DEPTH * step, stage);
+        stage = stage == F::DEPTH - 1 ? 0 : stage + 1;
+        float2 s2 = v[0];
+#pragma unroll
+        for (int i = 1; i < E2; i++) s2 = add_pair(s2, v[i]);
+        float s[1] = {s2.x + s2.y};
         sum(s);
         const float mean = s[0] / p.C;
         s[0] = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; i++) {
-            v[j][i] -= mean;
-            if (S::column(i, lane) < p.C) s[0] = fmaf(v[j][i], v[j][i], s[0]);
+        for (int k = 0; k < K; k++) {
+            float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = k * Sh::VEC / 2; i < (k + 1) * Sh::VEC / 2; i++) {
+                v[i] = add_pair(v[i], make_float2(-mean, -mean));
+                if (!WIDE) {   // columns past C do not count
+                    if (Sh::column(2 * i, lane) >= p.C) v[i].x = 0.f;
+                    if (Sh::column(2 * i + 1, lane) >= p.C) v[i].y = 0.f;
+                }
+                q = fma_pair(v[i], v[i], q);
+            }
+            if (!WIDE || (k * TPR + lane) * Sh::VEC < p.C) s[0] += q.x + q.y;
         }
         sum(s);
-        const float rstd = 1.f / sqrtf(s[0] / p.C + p.eps);
-        if (r0 + j < p.rows) {
-            S y;
-            float out[E];
+        const float rstd = rsqrtf(s[0] / p.C + p.eps);
+        if (r < p.rows) {
+            Sh y;
 #pragma unroll
-            for (int i = 0; i < E; i++) out[i] = fmaf(v[j][i] * rstd, w[i], b[i]);
-            y.set(out);
-            y.store(row_at<T>(p.y, r0 + j), lane, p.C);
-            if (p.mean && lane == 0) p.mean[r0 + j] = mean, p.rstd[r0 + j] = rstd;
+            for (int i = 0; i < E2; i++) y.set(i, fma_pair(mul_pair(v[i], make_float2(rstd, rstd)), w[i], b[i]));
+            y.store(row_at<T>(p.y, r), lane, p.C);
+            if (p.mean && lane == 0) p.mean[r] = mean, p.rstd[r] = rstd;
         }
     }
 }
 
-// Groups walk over rows gridDim * GROUPS apart; the next row is on its way
-// while one is worked on.
-template <typename T, int TPR, int K, bool WIDE>
-__global__ void __launch_bounds__(threads_of<TPR>()) ln_backward_kernel(NormProblem p) {
-    using S = Share<T, TPR, K, WIDE>;
-    constexpr int E = S::E, GROUPS = threads_of<TPR>() / TPR;
+template <typename T, int TPR, int K, bool WIDE, int S, int CTAS>
+__global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_backward_kernel(NormProblem p) {
+    using F = Feed<T, TPR, K, WIDE, 3, S>;
+    using Sh = typename F::Sh;
+    constexpr int E = Sh::E, E2 = E / 2, GROUPS = threads_of<TPR>() / TPR;
     __shared__ float sh[2][2][TPR / 32 > 0 ? TPR / 32 : 1];
-    // [GROUPS][2][C] where a CTA has several groups; the sums themselves, [2][E]
-    // [threads], where a CTA of 1024 threads leaves 64 registers to each
+    extern __shared__ __align__(16) uint4 smem[];
+    // After the feed, and over it once the walk is done, [GROUPS][2][C] where a
+    // CTA has several groups; the sums themselves, [2][E][threads], where a CTA of
+    // 1024 threads leaves 64 registers to each.
     constexpr bool kOutside = TPR == 1024;
-    extern __shared__ float columns[];
+    float *columns = reinterpret_cast<float *>(smem) + (kOutside ? F::bytes(TPR) / sizeof(float) : 0);
     Sums<TPR, 2> sum{sh};
     pdl_wait_cta();
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    F feed{smem + threadIdx.x, threads_of<TPR>(), lane, p.C};
     const long long step = (long long)gridDim.x * GROUPS;
-    float w[kOutside ? 1 : E], dw[kOutside ? 1 : E], db[kOutside ? 1 : E];
+    float mean = 0.f, rstd = 0.f;
+    auto fetch = [&](long long r, int stage) {
+        if (r < p.rows) {
+            feed.fetch(stage, 0, row_at<T>(p.y, r));
+            feed.fetch(stage, 1, row_at<T>(p.x, r));
+            if (p.res.data) feed.fetch(stage, 2, row_at<T>(p.res, r));
+        }
+        feed.commit();
+    };
+    auto next_stats = [&](long long r) {
+        if (r < p.rows) mean = p.mean[r], rstd = p.rstd[r];
+    };
+#pragma unroll
+    for (int i = 0; i < F::DEPTH; i++) fetch((long long)blockIdx.x * GROUPS + group + i * step, i);
+    next_stats((long long)blockIdx.x * GROUPS + group);
+    float2 w[kOutside ? 1 : E2], dw[kOutside ? 1 : E2], db[kOutside ? 1 : E2];
     if constexpr (kOutside) {
 #pragma unroll
         for (int i = 0; i < 2 * E; i++) columns[i * TPR + lane] = 0.f;
     } else {
-        load_columns<TPR, K, S::VEC, WIDE>(w, p.w, lane, p.C, 1.f);
+        load_columns<TPR, K, Sh::VEC, WIDE>(w, p.w, lane, p.C, 1.f);
 #pragma unroll
-        for (int i = 0; i < E; i++) dw[i] = db[i] = 0.f;
+        for (int i = 0; i < E2; i++) dw[i] = db[i] = make_float2(0.f, 0.f);
     }
-    S dy, s, extra;
-    float mean = 0.f, rstd = 0.f;
-    auto fetch = [&](long long r) {
-        if (r < p.rows) {
-            dy.load(row_at<T>(p.y, r), lane, p.C);
-            s.load(row_at<T>(p.x, r), lane, p.C);
-            if (p.res.data) extra.load(row_at<T>(p.res, r), lane, p.C);
-            mean = p.mean[r], rstd = p.rstd[r];
-        }
-    };
-    if constexpr (!kOutside) fetch((long long)blockIdx.x * GROUPS + group);
-    // a CTA's groups run the same number of rounds (their barriers and shuffles meet)
+    int stage = 0;
     for (long long base = (long long)blockIdx.x * GROUPS; base < p.rows; base += step) {
         const long long r = base + group;
-        float g[E], xh[E], t[2] = {0.f, 0.f};
-        if constexpr (kOutside) fetch(r);
-        const float rs = rstd;
-#pragma unroll
-        for (int i = 0; i < E; i++) {
-            g[i] = dy.get(i);
-            xh[i] = (s.get(i) - mean) * rs;
-        }
-        const S here = extra;
-        if constexpr (!kOutside) fetch(r + step);
+        const long long at = min(r, p.rows - 1);
+        feed.wait();
+        const Sh dy = feed.take(stage, 0, row_at<T>(p.y, at)), s = feed.take(stage, 1, row_at<T>(p.x, at));
+        Sh extra;
+        if (p.res.data) extra = feed.take(stage, 2, row_at<T>(p.res, at));
+        const float2 m = make_float2(-mean, -mean), rs = make_float2(rstd, rstd);
+        fetch(r + F::DEPTH * step, stage);
+        next_stats(r + step);
+        stage = stage == F::DEPTH - 1 ? 0 : stage + 1;
+        float2 g[E2], xh[E2], t1 = make_float2(0.f, 0.f), t2 = t1;
         if (r < p.rows) {
 #pragma unroll
-            for (int i = 0; i < E; i++) {   // g is 0 in the columns past C
+            for (int i = 0; i < E2; i++) {   // g is 0 in the columns past C
+                g[i] = dy.get(i);
+                xh[i] = mul_pair(add_pair(s.get(i), m), rs);
                 if constexpr (kOutside) {
-                    const int c = S::column(i, lane);
-                    columns[i * TPR + lane] = fmaf(g[i], xh[i], columns[i * TPR + lane]);
-                    columns[(E + i) * TPR + lane] += g[i];
-                    g[i] *= p.w && c < p.C ? p.w[c] : 1.f;
+                    const int c0 = Sh::column(2 * i, lane), c1 = Sh::column(2 * i + 1, lane);
+                    float *at = columns + 2 * i * TPR + lane;
+                    at[0] = fmaf(g[i].x, xh[i].x, at[0]), at[TPR] = fmaf(g[i].y, xh[i].y, at[TPR]);
+                    at[E * TPR] += g[i].x, at[(E + 1) * TPR] += g[i].y;
+                    if (p.w) g[i] = mul_pair(g[i], make_float2(c0 < p.C ? p.w[c0] : 0.f, c1 < p.C ? p.w[c1] : 0.f));
                 } else {
-                    dw[i] = fmaf(g[i], xh[i], dw[i]);
-                    db[i] += g[i];
-                    g[i] *= w[i];
+                    dw[i] = fma_pair(g[i], xh[i], dw[i]);
+                    db[i] = add_pair(db[i], g[i]);
+                    g[i] = mul_pair(g[i], w[i]);
                 }
-                t[0] += g[i];
-                t[1] = fmaf(g[i], xh[i], t[1]);
+                t1 = add_pair(t1, g[i]);
+                t2 = fma_pair(g[i], xh[i], t2);
             }
         }
+        float t[2] = {t1.x + t1.y, t2.x + t2.y};
         sum(t);
         if (r < p.rows) {
-            const float a = t[0] / p.C, b = t[1] / p.C;
-            float out[E];
+            const float2 a = make_float2(-t[0] / p.C, -t[0] / p.C), b = make_float2(-t[1] / p.C, -t[1] / p.C);
+            Sh ds;
 #pragma unroll
-            for (int i = 0; i < E; i++)
-                out[i] = fmaf(rs, g[i] - a - xh[i] * b, p.res.data ? here.get(i) : 0.f);
-            S ds;
-            ds.set(out);
+            for (int i = 0; i < E2; i++) {
+                const float2 d = fma_pair(xh[i], b, add_pair(g[i], a));
+                ds.set(i, p.res.data ? fma_pair(rs, d, extra.get(i)) : mul_pair(rs, d));
+            }
             ds.store(row_at<T>(p.ds, r), lane, p.C);
         }
     }
+    if constexpr (GROUPS > 1) __syncthreads();   // every thread has taken its last rows
     if (p.ws == nullptr) return;
     float *part = static_cast<float *>(p.ws) + (long long)blockIdx.x * 2 * p.C;
     if constexpr (GROUPS == 1) {
 #pragma unroll
         for (int i = 0; i < E; i++) {
-            const int c = S::column(i, lane);
+            const int c = Sh::column(i, lane);
             if (c >= p.C) continue;
             if constexpr (kOutside) part[c] = columns[i * TPR + lane], part[p.C + c] = columns[(E + i) * TPR + lane];
-            else part[c] = dw[i], part[p.C + c] = db[i];
+            else part[c] = i % 2 ? dw[i / 2].y : dw[i / 2].x, part[p.C + c] = i % 2 ? db[i / 2].y : db[i / 2].x;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < E; i++) {
-            const int c = S::column(i, lane);
-            if (c < p.C) columns[group * 2 * p.C + c] = dw[i], columns[group * 2 * p.C + p.C + c] = db[i];
+            const int c = Sh::column(i, lane);
+            if (c < p.C) {
+                columns[group * 2 * p.C + c] = i % 2 ? dw[i / 2].y : dw[i / 2].x;
+                columns[group * 2 * p.C + p.C + c] = i % 2 ? db[i / 2].y : db[i / 2].x;
+            }
         }
         __syncthreads();
         for (int c = threadIdx.x; c < 2 * p.C; c += threads_of<TPR>()) {
@@ -339,21 +421,39 @@ __global__ void __launch_bounds__(32 * kFinishWarps) ln_finish_kernel(const floa
     }
 }
 
-// CTAs of the backward: enough to fill the SMs twice over (four times with
-// CTAs of 256 threads and less), no more than there are rows for.
-int parts_of(long long rows, int groups, int threads) {
-    const long long most = kSms * (threads > 512 ? 2 : threads > 256 ? 3 : 4), need = (rows + groups - 1) / groups;
-    return (int)std::min(most, need);
+// CTAs that walk over the rows: as many as the SMs hold, no more than there are
+// rows for.
+int ctas_of(long long rows, int groups, int per_sm) {
+    return (int)std::min((long long)kSms * per_sm, (rows + groups - 1) / groups);
 }
+
+// Rows on their way (S) and CTAs a SM, within the registers and shared memory
+// that the widths leave.  Measured (bf16, forward | backward): rows of 64 13.3 |
+// 26.3 us for 262144 with 4 CTAs and 4 rows | 3 and 3 (5 and 3: 17.0; 4 and 2:
+// 32.2); rows of 2048 92.6 | 96.5 us for 32768 with 6 and 2 | 3 and 3 (4 and 4:
+// 98.1; 4 and 2: 111).
+template <typename T, int TPR, int K, bool WIDE> struct Shape {
+    static constexpr int THREADS = threads_of<TPR>(), PER = 256;   // CTAs counted for 256 threads
+    static constexpr bool kLean = WIDE || sizeof(T) == 4;          // single bf16 values take more registers
+    static constexpr int FWD_S = K == 1 ? (TPR <= 32 ? 4 : 2) : K == 4 ? 1 : THREADS == 1024 ? 2 : 3;
+    static constexpr int FWD_CTAS = THREADS == 1024  ? 1
+                                    : THREADS == 512 ? (kLean ? 2 : 1)
+                                    : K == 1         ? (!kLean ? 2 : TPR <= 32 ? 4 : 6) * PER / THREADS
+                                                     : (kLean ? 4 : 2);
+    static constexpr int BWD_S = K == 1 ? 3 : THREADS < 1024 ? 2 : K == 2 && WIDE ? 1 : 0;
+    static constexpr int BWD_CTAS = THREADS >= 512 ? 1 : K == 1 ? (kLean ? 3 : 2) * PER / THREADS : kLean ? 2 : 1;
+};
 
 struct Forward {
     template <typename T, int TPR, int K, bool WIDE> static cudaError_t run(const NormProblem &p) {
-        constexpr int E = Share<T, TPR, K, WIDE>::E, ROWS = TPR > 32 ? 1 : E <= 8 ? 4 : E <= 16 ? 2 : 1;
-        constexpr int per = threads_of<TPR>() / TPR * ROWS;
-        const long long ctas = (p.rows + per - 1) / per;
-        if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-        const cudaError_t e = launch_pdl(ln_forward_kernel<T, TPR, K, WIDE, ROWS>, dim3((unsigned)ctas),
-                                         dim3(threads_of<TPR>()), 0, p.stream, 0u, p);
+        constexpr int THREADS = threads_of<TPR>(), GROUPS = THREADS / TPR;
+        using C = Shape<T, TPR, K, WIDE>;
+        const auto kernel = ln_forward_kernel<T, TPR, K, WIDE, C::FWD_S, C::FWD_CTAS>;
+        const size_t smem = Feed<T, TPR, K, WIDE, 2, C::FWD_S>::bytes(THREADS);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(kernel, dim3((unsigned)ctas_of(p.rows, GROUPS, C::FWD_CTAS)), dim3(THREADS), smem, p.stream, 0u,
+                       p);
         count_launches(1);
         return e;
     }
@@ -362,15 +462,16 @@ struct Forward {
 struct Backward {
     template <typename T, int TPR, int K, bool WIDE> static cudaError_t run(NormProblem p) {
         constexpr int THREADS = threads_of<TPR>(), GROUPS = THREADS / TPR;
-        const int parts = parts_of(p.rows, GROUPS, THREADS);
+        using C = Shape<T, TPR, K, WIDE>;
+        const auto kernel = ln_backward_kernel<T, TPR, K, WIDE, C::BWD_S, C::BWD_CTAS>;
+        const int parts = ctas_of(p.rows, GROUPS, C::BWD_CTAS);
         if (!p.dw && !p.db) p.ws = nullptr;
-        size_t smem = GROUPS > 1 ? (size_t)GROUPS * 2 * p.C * sizeof(float) : 0;
-        if (TPR == 1024) smem = 2 * Share<T, TPR, K, WIDE>::E * TPR * sizeof(float);
-        cudaError_t e = cudaFuncSetAttribute(ln_backward_kernel<T, TPR, K, WIDE>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        size_t smem = Feed<T, TPR, K, WIDE, 3, C::BWD_S>::bytes(THREADS);
+        if (GROUPS > 1) smem = std::max(smem, (size_t)GROUPS * 2 * p.C * sizeof(float));
+        if (TPR == 1024) smem += 2 * Share<T, TPR, K, WIDE>::E * TPR * sizeof(float);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(ln_backward_kernel<T, TPR, K, WIDE>, dim3((unsigned)parts), dim3(THREADS), smem, p.stream, 0u,
-                       p);
+        e = launch_pdl(kernel, dim3((unsigned)parts), dim3(THREADS), smem, p.stream, 0u, p);
         count_launches(1);
         if (e != cudaSuccess || !p.ws) return e;
         e = launch_pdl(ln_finish_kernel, dim3((unsigned)((2 * p.C + 31) / 32)), dim3(32 * kFinishWarps), 0, p.stream,
@@ -410,9 +511,9 @@ template <typename Call> cudaError_t by_type(const NormProblem &p) {
 
 }  // namespace
 
-// A part per CTA of the backward: at most 4 a SM, at most one per row.
+// A part per CTA of the backward: at most 8 a SM, at most one per row.
 size_t layernorm_ws_bytes(long long rows, int C) {
-    return (size_t)std::min(rows, 4LL * kSms) * 2 * C * sizeof(float);
+    return (size_t)std::min(rows, 8LL * kSms) * 2 * C * sizeof(float);
 }
 
 cudaError_t layernorm_forward(const NormProblem &p) { return by_type<Forward>(p); }

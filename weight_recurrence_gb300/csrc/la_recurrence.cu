@@ -43,13 +43,6 @@ struct Dims {
 };
 
 // V neighbouring channels of one row as they lie in memory.
-__device__ __forceinline__ float2 get_pair(unsigned r) {
-    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
-}
-__device__ __forceinline__ unsigned put_pair(float2 v) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
-    return *reinterpret_cast<const unsigned *>(&p);
-}
 template <typename T, int V> struct Raw;
 template <> struct Raw<float, 1> {
     using type = float;
