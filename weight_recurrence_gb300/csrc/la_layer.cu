@@ -215,9 +215,7 @@ la_status la_grad_norm(const la_tensor *tensors, int count, float *norm, void *w
                        la_stream_t stream) {
     const la_status st = check_grads(tensors, count, norm, workspace, ws_bytes, false);
     if (st != LA_OK) return st;
-    const DeviceInfo *dev = device_info();
-    if (!dev) return LA_ERR_CUDA;
-    return from_cuda(grad_norm_clip(tensors, count, -1.f, norm, workspace, (cudaStream_t)stream, *dev));
+    return from_cuda(grad_norm_clip(tensors, count, -1.f, norm, workspace, (cudaStream_t)stream));
 }
 
 la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
@@ -225,9 +223,7 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
     if (!(max_norm >= 0.f)) return LA_ERR_INVALID_ARG;
     const la_status st = check_grads(tensors, count, norm, workspace, ws_bytes, true);
     if (st != LA_OK) return st;
-    const DeviceInfo *dev = device_info();
-    if (!dev) return LA_ERR_CUDA;
-    return from_cuda(grad_norm_clip(tensors, count, max_norm, norm, workspace, (cudaStream_t)stream, *dev));
+    return from_cuda(grad_norm_clip(tensors, count, max_norm, norm, workspace, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -47,7 +47,6 @@ cudaError_t layernorm_backward(const NormProblem &p);
 
 size_t grad_ws_bytes(int count);
 // max_norm < 0: the norm alone
-cudaError_t grad_norm_clip(const la_tensor *t, int count, float max_norm, float *norm, void *ws,
-                           cudaStream_t stream, const DeviceInfo &dev);
+cudaError_t grad_norm_clip(const la_tensor *t, int count, float max_norm, float *norm, void *ws, cudaStream_t stream);
 
 }  // namespace la

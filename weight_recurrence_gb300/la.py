@@ -703,35 +703,36 @@ _tensor_code = {torch.float32: LA_DTYPE_F32, torch.bfloat16: LA_DTYPE_BF16}
 
 def _grad_call(name, grads, out, norm, stream, *args):
     """Packs the la_tensor table (one struct.pack for all of it) and calls."""
-    _need(len(grads) > 0, "no tensors")
+    n, T = len(grads), torch.Tensor
+    _need(n > 0, "no tensors")
     dev = grads[0].get_device()
-    for t in grads:
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        if t.dtype not in _tensor_code:
-            raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
-        if t.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
-    if out is None:
-        dst = [0] * len(grads)
-    elif out is grads:
-        dst = [t.data_ptr() for t in grads]
-    else:
-        _need(len(out) == len(grads), "out must have one tensor per gradient")
+    if not all(map(T.is_contiguous, grads)):
+        raise ValueError("tensors must be contiguous")
+    codes = [_tensor_code.get(t.dtype) for t in grads]
+    if None in codes:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % grads[codes.index(None)].dtype)
+    _need(set(map(T.get_device, grads)) == {dev}, "all tensors must be on one device")
+    table = [0] * (4 * n)   # src, dst, n, dtype of every tensor in turn
+    table[0::4] = map(T.data_ptr, grads)
+    table[2::4] = map(T.numel, grads)
+    table[3::4] = codes
+    if out is grads:
+        table[1::4] = table[0::4]
+    elif out is not None:
+        _need(len(out) == n, "out must have one tensor per gradient")
         for t, d in zip(grads, out):
-            _like("out", d, t.shape, t.dtype, dev)
-            if not d.is_contiguous():
-                raise ValueError("out must be contiguous")
-        dst = [t.data_ptr() for t in out]
+            if d.shape != t.shape or d.dtype is not t.dtype:
+                raise ValueError("out must have the gradients' shapes and types")
+        _need(all(map(T.is_contiguous, out)), "out must be contiguous")
+        _need(set(map(T.get_device, out)) == {dev}, "all tensors must be on one device")
+        table[1::4] = map(T.data_ptr, out)
     _state("norm", norm, (), dev)
     sp = _launch_stream(stream, dev)
     if norm is None:
         norm = _empty(stream, grads[0], (), torch.float32)
-    table = struct.pack("PPqi4x" * len(grads), *[v for t, d in zip(grads, dst)
-                                                 for v in (t.data_ptr(), d, t.numel(), _tensor_code[t.dtype])])
-    need = lib().la_grad_workspace_bytes(len(grads))
+    need = lib().la_grad_workspace_bytes(n)
     ws = _empty(stream, grads[0], (need,), torch.uint8)
-    st = getattr(lib(), name)(table, len(grads), *args, norm.data_ptr(), ws.data_ptr(), need, sp)
+    st = getattr(lib(), name)(struct.pack("PPqi4x" * n, *table), n, *args, norm.data_ptr(), ws.data_ptr(), need, sp)
     _check(st, name)
     return norm
 
