@@ -121,15 +121,23 @@ template <int V, int W> struct Join {
           sub(threadIdx.x % J::G) {
         state = first && channel < left ? first[channel] : 0.f;
     }
-    // Over the segments before this one; maps: their strip's first channel, `pitch` apart.
+    // Over the segments before this one; maps: their strip's first channel,
+    // `pitch` apart.  The owners of a channel take equal runs of them.
     __device__ __forceinline__ void skip(const float2 *maps, int segments, long long pitch, int left) {
+        if (segments == 0) return;
+        float a = 1.f, h = 0.f;
         if (channel < left) {
-#pragma unroll 8
-            for (int i = 0; i < segments; i++) {
+            const int to = (sub + 1) * segments / J::G;
+#pragma unroll 16
+            for (int i = sub * segments / J::G; i < to; i++) {
                 const float2 m = maps[i * pitch + channel];
-                state = fmaf(m.x, state, m.y);
+                h = fmaf(m.x, h, m.y);
+                a = finite(m.x * a);
             }
         }
+#pragma unroll
+        for (int i = 0; i < J::G; i++)
+            state = fmaf(__shfl_sync(~0u, a, i, J::G), state, __shfl_sync(~0u, h, i, J::G));
     }
     __device__ __forceinline__ void end(float *first, int left) {
         if (first && channel < left && sub == 0) first[channel] = state;
@@ -352,10 +360,14 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
 // (A, H) of every segment but the last, and a copy of the state that the walk
 // starts from (a caller's hN may be its h0).  Warps take consecutive eighths of
 // a segment and meet once at its end.  BACK: the backward's maps, of g and dout.
+template <typename T, int V, int W, int R, int S> struct MapTiles {
+    typename Raw<T, V>::type slot[W][S][2][R][32];
+    float A[W][32 * V], H[W][32 * V];
+};
 template <typename T, int GATE, int V, bool WIDE, bool BACK, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_view x, Dims s, const float *state) {
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &sh = *reinterpret_cast<Tiles<T, V, W, 2, R, S> *>(smem);
+    auto &sh = *reinterpret_cast<MapTiles<T, V, W, R, S> *>(smem);
     pdl_wait_cta();
     const Place<V> q(s, s.segments - 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -380,30 +392,33 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_vi
     for (int i = 0; i < pieces; i++) {
         ring.template wait<S - 1>();
         const int n = (int)min((long long)R, last - (first + (long long)i * R));
-#pragma unroll
-        for (int r = 0; r < R; r++) {
+        auto step = [&](int r) {
             Lanes<V> a, w;
             gate_of<GATE, V>(ring.get(stage, 1, r), a, w);
             const Lanes<V> v = ring.get(stage, 0, r);
-            if (r < n) {
-                A = mul(A, a);
-                if (BACK) H = mul(a, add(v, H));
-                else H = fma(a, H, GATE == LA_GATE_SIGMOID ? mul(w, v) : v);
-            }
+            A = mul(A, a);
+            if (BACK) H = mul(a, add(v, H));
+            else H = fma(a, H, GATE == LA_GATE_SIGMOID ? mul(w, v) : v);
+        };
+        if (n >= R) {
+#pragma unroll
+            for (int r = 0; r < R; r++) step(r);
+        } else {
+            for (int r = 0; r < n; r++) step(r);
         }
         __syncwarp();
         fetch(i + S, stage);
         stage = stage == S - 1 ? 0 : stage + 1;
     }
-    put_lanes(&sh.joint.A[0][warp][lane * V], finite(A));
-    put_lanes(&sh.joint.H[0][warp][lane * V], H);
+    put_lanes(&sh.A[warp][lane * V], finite(A));
+    put_lanes(&sh.H[warp][lane * V], H);
     __syncthreads();
     for (int c = threadIdx.x; c < 32 * V && c < q.left; c += 32 * W) {
         float a = 1.f, h = 0.f;
 #pragma unroll
         for (int w = 0; w < W; w++) {
-            h = fmaf(sh.joint.A[0][w][c], h, sh.joint.H[0][w][c]);
-            a = finite(a * sh.joint.A[0][w][c]);
+            h = fmaf(sh.A[w][c], h, sh.H[w][c]);
+            a = finite(a * sh.A[w][c]);
         }
         s.maps[q.segment * s.channels + q.at + c] = make_float2(a, h);
         if (q.segment == 0) s.start[q.at + c] = state ? state[q.at + c] : 0.f;
@@ -564,21 +579,23 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
     if (q.last()) join.end(dh0 ? dh0 + q.at : nullptr, q.left);
 }
 
-// Tiles: W warps of R rows a CTA, S of them on their way, CTAS CTAs a SM.
-template <int W_, int R_, int S_, int C_> struct Tile {
-    static constexpr int W = W_, R = R_, S = S_, CTAS = C_;
+// Tiles: W warps of R rows a CTA, S of them on their way, CTAS CTAs a SM.  ROW:
+// bytes of a strip's row; rows of 256 bytes come by ROWS a warp, narrower ones by
+// as many more (at most ROWS * 2 where they are 64).
+template <int ROW, int ROWS, int S_, int C_> struct Tile {
+    static constexpr int W = 8, R = ROW == 256 ? ROWS : ROWS * 2, S = S_, CTAS = C_;
 };
 // Many CTAs: two a SM hide each other's joins.  No more CTAs than SMs: twice the
 // rows a tile for the same number of joins (128 strips of 4096 tokens, bf16:
 // forward 63 us, backward 126 us, against 71 and 141 us with the small tiles; 256
 // strips of 2048: 69 and 109 us against 63 and 109 us).
-using Fwd = Tile<8, 8, 2, 2>;
-using FwdFew = Tile<8, 16, 3, 1>;
-using Bwd = Tile<8, 4, 2, 2>;
-using BwdFew = Tile<8, 8, 3, 1>;
-using Pre = Tile<8, 8, 3, 2>;
+template <int ROW> using Fwd = Tile<ROW, 8, 2, 2>;
+template <int ROW> using FwdFew = Tile<ROW, 16, 3, 1>;
+template <int ROW> using Bwd = Tile<ROW, 4, 2, 2>;
+template <int ROW> using BwdFew = Tile<ROW, 8, 3, 1>;
+template <int ROW> using Pre = Tile<ROW, 8, 2, 3>;
 constexpr int kSms = 152;
-constexpr int kSegmentRows = 128;   // a multiple of every tile's rows
+constexpr int kSegmentRows = 64;   // a multiple of the warps, and of the tiles' rows (their half for narrow rows)
 
 // Segments of a strip: none of it (1) where the strips fill half of the SMs, else
 // as many as give every SM two CTAs, of at least kSegmentRows tokens.
@@ -610,9 +627,10 @@ cudaError_t launch_tiles(Kernel kernel, size_t smem, const RecProblem &p, const 
 template <typename T, int GATE, int V, bool WIDE, bool BACK>
 cudaError_t segment_maps(const RecProblem &p, const Dims &s) {
     if (s.segments == 1) return cudaSuccess;
-    return launch_tiles<Pre>(rec_maps_kernel<T, GATE, V, WIDE, BACK, Pre::W, Pre::R, Pre::S, Pre::CTAS>,
-                                sizeof(Tiles<T, V, Pre::W, 2, Pre::R, Pre::S>), p, s, s.segments - 1, p.g,
-                                BACK ? p.dout : p.x, s, BACK ? p.dhN : p.h0);
+    using C = Pre<32 * V * (int)sizeof(T)>;
+    return launch_tiles<C>(rec_maps_kernel<T, GATE, V, WIDE, BACK, C::W, C::R, C::S, C::CTAS>,
+                           sizeof(MapTiles<T, V, C::W, C::R, C::S>), p, s, s.segments - 1, p.g, BACK ? p.dout : p.x, s,
+                           BACK ? p.dhN : p.h0);
 }
 
 template <typename T, int GATE, int V> cudaError_t short_v(const RecProblem &p) {
@@ -634,7 +652,8 @@ struct Forward {
         const Dims s = dims_of<V>(p);
         const cudaError_t e = segment_maps<T, GATE, V, WIDE, false>(p, s);
         if (e != cudaSuccess) return e;
-        return few_ctas(p, s) ? tiles<T, GATE, V, WIDE, FwdFew>(p, s) : tiles<T, GATE, V, WIDE, Fwd>(p, s);
+        constexpr int ROW = 32 * V * (int)sizeof(T);
+        return few_ctas(p, s) ? tiles<T, GATE, V, WIDE, FwdFew<ROW>>(p, s) : tiles<T, GATE, V, WIDE, Fwd<ROW>>(p, s);
     }
     template <typename T, int GATE, int V, bool WIDE, typename C>
     static cudaError_t tiles(const RecProblem &p, const Dims &s) {
@@ -649,7 +668,8 @@ struct Backward {
         const Dims s = dims_of<V>(p);
         const cudaError_t e = segment_maps<T, GATE, V, WIDE, true>(p, s);
         if (e != cudaSuccess) return e;
-        return few_ctas(p, s) ? tiles<T, GATE, V, WIDE, BwdFew>(p, s) : tiles<T, GATE, V, WIDE, Bwd>(p, s);
+        constexpr int ROW = 32 * V * (int)sizeof(T);
+        return few_ctas(p, s) ? tiles<T, GATE, V, WIDE, BwdFew<ROW>>(p, s) : tiles<T, GATE, V, WIDE, Bwd<ROW>>(p, s);
     }
     template <typename T, int GATE, int V, bool WIDE, typename C>
     static cudaError_t tiles(const RecProblem &p, const Dims &s) {
