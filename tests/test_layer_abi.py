@@ -66,7 +66,7 @@ def test_recurrence_forward_refusals(lib):
     # a few long sequences need workspace
     long = _shape(B=1, H=1, N=65536)
     need = lib.la_recurrence_workspace_bytes(long)
-    assert 0 < need < (1 << 22) and lib.la_recurrence_workspace_bytes(_shape(N=128)) == 0
+    assert 0 < need < (1 << 22) and lib.la_recurrence_workspace_bytes(_shape(N=64)) == 0
     assert lib.la_recurrence_workspace_bytes(_shape(N=-1)) == la._SIZE_MAX
     assert call(s=long) == INVALID
     assert call(s=long, ws=_p(7), n=need - 1) == INVALID

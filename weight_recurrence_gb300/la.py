@@ -484,6 +484,13 @@ def _empty(stream, like, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _out_like(stream, t):
+    """A contiguous tensor of t's shape and type (empty_like parses less than empty)."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(stream, t, t.shape, t.dtype)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -552,7 +559,7 @@ def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens
     _lens(lens, s.B, dev)
     sp = _launch_stream(stream, dev)
     if out is None:
-        out = _empty(stream, x, x.shape, x.dtype)
+        out = _out_like(stream, x)
     need, ws = _recurrence_ws(s, stream, x)
     st = lib().la_recurrence_forward(_view("x", x), _view("g", g), _view("out", out), _addr(lens), s, code, _addr(h0),
                                      _addr(hN), _addr(ws), need, sp)
@@ -572,7 +579,7 @@ def la_recurrence_step(x, g, h, gate="sigmoid", y=None, stream=None):
     _state("h", h, x.shape, dev)
     sp = _launch_stream(stream, dev)
     if y is None:
-        y = _empty(stream, x, x.shape, x.dtype)
+        y = _out_like(stream, x)
     st = lib().la_recurrence_step(_view("x", x, True), _view("g", g, True), _view("y", y, True), s, code,
                                   h.data_ptr(), sp)
     _check(st, "la_recurrence_step")
@@ -598,9 +605,9 @@ def la_recurrence_backward(x, g, out, dout, gate="sigmoid", h0=None, dhN=None, d
     _lens(lens, s.B, dev)
     sp = _launch_stream(stream, dev)
     if dx is None:
-        dx = _empty(stream, g, g.shape, g.dtype)
+        dx = _out_like(stream, g)
     if dg is None:
-        dg = _empty(stream, g, g.shape, g.dtype)
+        dg = _out_like(stream, g)
     need, ws = _recurrence_ws(s, stream, g)
     st = lib().la_recurrence_backward(_view("x", x), _view("g", g), _view("out", out), _view("dout", dout),
                                       _view("dx", dx), _view("dg", dg), _addr(lens), s, code, _addr(h0), _addr(dhN),
@@ -650,12 +657,12 @@ def la_layernorm_forward(x, w=None, b=None, eps=1e-5, res=None, y=None, sum=None
     _state("rstd", rstd, lead, dev)
     sp = _launch_stream(stream, dev)
     if y is None:
-        y = _empty(stream, x, sh, dtype)
+        y = _out_like(stream, x)
     if res is not None and sum is None:
-        sum = _empty(stream, x, sh, dtype)
+        sum = _out_like(stream, x)
     if stats:
         mean = _empty(stream, x, lead, torch.float32) if mean is None else mean
-        rstd = _empty(stream, x, lead, torch.float32) if rstd is None else rstd
+        rstd = _out_like(stream, mean) if rstd is None else rstd
     st = lib().la_layernorm_forward(_rows("x", x), _rows("res", res), _rows("sum", sum), _rows("y", y), _addr(w),
                                     _addr(b), _addr(mean), _addr(rstd), x.numel() // C, C, code, eps, sp)
     _check(st, "la_layernorm_forward")
@@ -681,11 +688,11 @@ def la_layernorm_backward(dy, s, w, mean, rstd, dsum=None, ds=None, dw=None, db=
     _state("db", db, (C,), dev)
     sp = _launch_stream(stream, dev)
     if ds is None:
-        ds = _empty(stream, dy, sh, dtype)
+        ds = _out_like(stream, dy)
     if dw is None:
         dw = _empty(stream, dy, (C,), torch.float32)
     if db is None:
-        db = _empty(stream, dy, (C,), torch.float32)
+        db = _out_like(stream, dw)
     rows = dy.numel() // C
     need = lib().la_layernorm_workspace_bytes(rows, C, code)
     if need == _SIZE_MAX:
@@ -720,9 +727,8 @@ def _grad_call(name, grads, out, norm, stream, *args):
         table[1::4] = table[0::4]
     elif out is not None:
         _need(len(out) == n, "out must have one tensor per gradient")
-        for t, d in zip(grads, out):
-            if d.shape != t.shape or d.dtype is not t.dtype:
-                raise ValueError("out must have the gradients' shapes and types")
+        if list(map(T.numel, out)) != table[2::4] or [_tensor_code.get(t.dtype) for t in out] != codes:
+            raise ValueError("out must have the gradients' sizes and types")
         _need(all(map(T.is_contiguous, out)), "out must be contiguous")
         _need(set(map(T.get_device, out)) == {dev}, "all tensors must be on one device")
         table[1::4] = map(T.data_ptr, out)
