@@ -187,7 +187,6 @@ template <int V> struct Place {
     long long b, h, at;      // at: its first channel in [B,H,D]
     int d0, left, len, segment;
     long long from, to;
-    bool ok;                 // the thread's channels exist (all V or none: D is a multiple of V)
     __device__ __forceinline__ Place(const Dims &s, int segments) {
         const unsigned strip = blockIdx.x / segments;
         segment = blockIdx.x % segments;
@@ -197,7 +196,6 @@ template <int V> struct Place {
         d0 = (int)(strip % s.strips) * 32 * V;
         left = s.D - d0;
         at = bh * s.D + d0;
-        ok = (int)(threadIdx.x & 31) * V < left;
         len = s.lens ? min(max(s.lens[b], 0), s.N) : s.N;
         from = min(segment * s.rows, (long long)len);
         to = min(from + s.rows, (long long)len);
@@ -209,13 +207,17 @@ template <int V> struct Place {
     __device__ __forceinline__ bool last() const { return to == len && (from < to || segment == 0); }
 };
 
+// Stores a lane's channels of a row (p: the row's first channel of the strip, of
+// which `left` exist; a lane has all V or none: D is a multiple of V).
+template <typename T, int V> __device__ __forceinline__ void store_row(T *p, int lane, int left, const Lanes<V> &x) {
+    if (lane * V < left) *reinterpret_cast<typename Raw<T, V>::type *>(p + lane * V) = Raw<T, V>::put(x);
+}
+
 // Rows at or past a sequence's length become 0, the segments taking turns.
 template <typename T, int V, int W>
 __device__ __forceinline__ void clear_rows(T *p, long long sn, const Place<V> &q, const Dims &s) {
-    using RT = typename Raw<T, V>::type;
-    if (!q.ok) return;
     for (long long t = q.len + q.segment * W + (threadIdx.x >> 5); t < s.N; t += s.segments * W)
-        *reinterpret_cast<RT *>(p + t * sn) = RT{};
+        store_row<T, V>(p + t * sn, threadIdx.x & 31, q.left, all<V>(0.f));
 }
 
 // A warp's rows of NT tensors on their way through shared memory, S tiles deep.
@@ -298,7 +300,6 @@ template <typename T, int V, int W, int NT, int R, int S> struct Tiles {
 template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la_view g, la_view out, Dims s,
                                                                   const float *h0, float *hN) {
-    using RT = typename Raw<T, V>::type;
     extern __shared__ __align__(16) unsigned char smem[];
     auto &sh = *reinterpret_cast<Tiles<T, V, W, 2, R, S> *>(smem);
     pdl_wait_cta();
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
     Join<V, W> join(sh.joint, s.segments > 1 ? s.start + q.at : h0 ? h0 + q.at : nullptr, q.left);
     Ring<T, V, 2, R, S, WIDE> ring(sh.slot[join.warp], join.lane);
     const T *px = q.template strip<T>(x), *pg = q.template strip<T>(g);
-    T *po = q.template strip<T>(out) + join.lane * V;
+    T *po = q.template strip<T>(out);
     const long long first = q.from + join.warp * R;   // this warp's rows in the first tile
     const int tiles = (int)((q.to - q.from + W * R - 1) / (W * R));
     auto fetch = [&](int it, int stage) {
@@ -345,12 +346,11 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
 #pragma unroll
         for (int r = 1; r < R; r++) A = mul(A, a[r]), H = fma(a[r], H, u[r]);
         Lanes<V> h = join(A, H);
-        const int rows = q.ok ? n : 0;
         T *p = po + t0 * out.sn;
 #pragma unroll
         for (int r = 0; r < R; r++, p += out.sn) {
             h = fma(a[r], h, u[r]);
-            if (r < rows) *reinterpret_cast<RT *>(p) = Raw<T, V>::put(h);
+            if (r < n) store_row<T, V>(p, join.lane, q.left, h);
         }
     }
     clear_rows<T, V, W>(po, out.sn, q, s);
@@ -486,7 +486,6 @@ template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, la_view g, la_view out, la_view dout,
                                                                    la_view dx, la_view dg, Dims s, const float *h0,
                                                                    const float *dhN, float *dh0) {
-    using RT = typename Raw<T, V>::type;
     constexpr bool kSigmoid = GATE == LA_GATE_SIGMOID;
     constexpr int NL = kSigmoid ? 2 : 1;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
     Ring<T, V, NL, R, S, WIDE> late(sh.late[join.warp], join.lane);
     const T *px = kSigmoid ? q.template strip<T>(x) : nullptr, *pg = q.template strip<T>(g);
     const T *po = q.template strip<T>(out), *pd = q.template strip<T>(dout);
-    T *pdx = q.template strip<T>(dx) + join.lane * V, *pdg = q.template strip<T>(dg) + join.lane * V;
+    T *pdx = q.template strip<T>(dx), *pdg = q.template strip<T>(dg);
     const long long first = q.len - 1 - (q.from + join.warp * R);   // this warp's first row, and the CTA's last
     const long long end = q.len - q.to;
     const int tiles = (int)((q.to - q.from + W * R - 1) / (W * R));
@@ -547,14 +546,16 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
         for (int r = 1; r < R; r++) A = mul(A, a[r]), H = mul(a[r], add(d[r], H));
         Lanes<V> mu = join(A, H);
         late.template wait<2 * S - 1>();
-        const int rows = q.ok ? n : 0;
         T *to_x = pdx + t0 * dx.sn, *to_g = pdg + t0 * dg.sn;
 #pragma unroll
         for (int r = 0; r < R; r++, to_x -= dx.sn, to_g -= dg.sn) {
             Lanes<V> before = late.get(stage, 0, r);
-            if (t0 == r && q.ok) {   // the first token: the state that the forward started from
+            if (t0 == r) {   // the first token: the state that the forward started from
 #pragma unroll
-                for (int v = 0; v < V; v++) before.set(v, h0 ? h0[q.at + join.lane * V + v] : 0.f);
+                for (int v = 0; v < V; v++) {
+                    const int c = join.lane * V + v;
+                    before.set(v, h0 && c < q.left ? h0[q.at + c] : 0.f);
+                }
             }
             const Lanes<V> l = add(d[r], mu);
             mu = mul(a[r], l);
@@ -565,9 +566,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
             } else {
                 og = mul(GATE == LA_GATE_LOG ? mu : l, before);
             }
-            if (r < rows) {
-                *reinterpret_cast<RT *>(to_x) = Raw<T, V>::put(ox);
-                *reinterpret_cast<RT *>(to_g) = Raw<T, V>::put(og);
+            if (r < n) {
+                store_row<T, V>(to_x, join.lane, q.left, ox);
+                store_row<T, V>(to_g, join.lane, q.left, og);
             }
         }
         __syncwarp();
