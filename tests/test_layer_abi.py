@@ -189,7 +189,7 @@ def test_grad_refusals(lib):
     assert call(mx=float("nan")) == INVALID
 
 
-def test_binding_refusals():
+def test_binding_refusals(lib):
     x = torch.zeros(2, 5, 8)
     g = torch.zeros(2, 5, 8)
     with pytest.raises(ValueError, match="CUDA"):
@@ -241,17 +241,31 @@ def test_binding_refusals():
         la.la_grad_clip([x, g], 1.0, out=[x])
     with pytest.raises(ValueError, match="CUDA"):
         la.la_grad_clip([x], 1.0)
+    for call in (lambda: la.la_recurrence_forward(None, g), lambda: la.la_layernorm_forward(None),
+                 lambda: la.la_recurrence_step(x[:, 0], g[:, 0], None), lambda: la.la_grad_norm([None])):
+        with pytest.raises(ValueError, match="required"):
+            call()
+    with pytest.raises(TypeError, match="tensor"):
+        la.la_recurrence_forward(x, [g])
+    with pytest.raises(TypeError):
+        la.la_grad_clip(3, 1.0)
+    with pytest.raises(TypeError):
+        la.la_layernorm_forward(x, w, eps="small")
 
 
-def test_strided_views_reach_the_library_as_they_are():
+def test_strided_views_reach_the_library_as_they_are(lib):
+    b = la._bound()
     t = torch.zeros(2, 6, 3, 16)                    # [B, N, H, 2D]
-    v = la._view("x", t[..., 8:].transpose(1, 2))   # [B, H, N, D]
-    assert (v.sb, v.sh, v.sn) == (6 * 3 * 16, 16, 48) and v.data == t.data_ptr() + 8 * 4
-    v = la._view("x", torch.zeros(1, 5, 8).expand(4, 5, 8))
-    assert (v.sb, v.sn) == (0, 8)
+    assert b.view(t[..., 8:].transpose(1, 2), False) == (t.data_ptr() + 8 * 4, 6 * 3 * 16, 16, 48)   # [B, H, N, D]
+    assert b.view(torch.zeros(1, 5, 8).expand(4, 5, 8), False)[1:] == (0, 0, 8)
+    assert b.view(t[:, 2, :, :8], True)[1:] == (6 * 3 * 16, 16, 0)
     with pytest.raises(ValueError, match="contiguous"):
-        la._view("x", torch.zeros(2, 8, 5).transpose(1, 2))
-    assert la._rows("x", t[:, :, 1, :8]).stride == 48
-    assert la._rows("x", t[0, 0, 0]).stride == 16
+        b.view(torch.zeros(2, 8, 5).transpose(1, 2), False)
+    assert b.rows(t[:, :, 1, :8]) == (t.data_ptr() + 16 * 4, 48)
+    assert b.rows(t[0, 0, 0])[1] == 16
     with pytest.raises(ValueError, match="one stride"):
-        la._rows("x", t[:, :4, 1])
+        b.rows(t[:, :4, 1])
+    with pytest.raises(TypeError, match="tensor"):
+        b.rows([1.0])
+    with pytest.raises(TypeError, match="arguments"):
+        b.rows(t, t)

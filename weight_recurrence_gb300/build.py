@@ -5,17 +5,21 @@ Each .cu translation unit compiles in parallel to an object under
 ``weight_recurrence_gb300/lib/liblinattn.so`` with the CUDA runtime linked
 statically, so the library depends on nothing but the driver.  The checked
 variant (``--checked``) compiles the same sources with ``-DLA_CHECKED`` into
-``_build_checked/`` and ``lib/liblinattn_checked.so``.
+``_build_checked/`` and ``lib/liblinattn_checked.so``.  ``csrc/la_torch.cpp``,
+the Python binding of part of the calls, compiles with g++ against the installed
+PyTorch's headers into ``lib/_la_torch.so`` (it finds the library at run time).
 
     python -m weight_recurrence_gb300.build [--force] [--verbose] [--checked]
 """
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -32,6 +36,8 @@ VARIANTS = {
 BUILD = os.path.join(PKG, VARIANTS["release"][0])
 LIB = os.path.join(LIBDIR, VARIANTS["release"][1])
 LIB_CHECKED = os.path.join(LIBDIR, VARIANTS["checked"][1])
+BINDING_SRC = os.path.join(CSRC, "la_torch.cpp")
+BINDING = os.path.join(LIBDIR, "_la_torch.so")
 
 
 def nvcc() -> str:
@@ -59,13 +65,28 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_command(out: str):
+    """g++ command line that makes the binding (torch is located, not imported)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", *("-I" + i for i in inc), BINDING_SRC, "-o", out,
+            "-L" + os.path.join(torch, "lib"), "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ltorch_python", "-ldl"]
+
+
 def build_variants(variants=("release",), force: bool = False, verbose: bool = False, extra_flags=()):
-    """Compile (incrementally) every translation unit of the given variants at
-    once, in parallel, then link each library; returns the library paths."""
+    """Compile (incrementally) every translation unit of the given variants and the
+    binding at once, in parallel, then link each library; returns the library paths."""
     os.makedirs(LIBDIR, exist_ok=True)
     cc = nvcc()
     hdrs = headers()
     plan, procs = [], []
+    bound = None
+    if force or _stale(BINDING, [BINDING_SRC, os.path.join(os.path.dirname(PKG), "include", "la.h")]):
+        bound = BINDING + ".tmp%d" % os.getpid()
+        procs.append((BINDING_SRC, subprocess.Popen(binding_command(bound), stdout=subprocess.PIPE,
+                                                    stderr=subprocess.STDOUT)))
     for name in variants:
         bdir, libname, vflags = VARIANTS[name]
         bdir = os.path.join(PKG, bdir)
@@ -89,7 +110,9 @@ def build_variants(variants=("release",), force: bool = False, verbose: bool = F
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+        raise RuntimeError("compilation failed for: " + ", ".join(failed))
+    if bound:
+        os.replace(bound, BINDING)
     for lib, objs, started in plan:
         if force or started or _stale(lib, objs):
             tmp = lib + ".tmp%d" % os.getpid()

@@ -15,14 +15,16 @@ select_library(checked=True) makes every call below go to the checked build.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "liblinattn.so")
 LIB_CHECKED_PATH = os.path.join(_PKG, "lib", "liblinattn_checked.so")
+BINDING_PATH = os.path.join(_PKG, "lib", "_la_torch.so")
 
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT, LA_ERR_BOUNDS = range(6)
 LA_DTYPE_F32, LA_DTYPE_BF16 = 0, 1
@@ -439,82 +441,35 @@ def la_decode_step_variant(q, k, v, S, var: la_variant, z=None, beta=None, y=Non
 
 
 # ------------------------------------------- the layer around the attention
-# These calls check shapes, types and devices here (the library sees pointers,
-# sizes and strides only), take views, and allocate what they return or need
-# as workspace on the stream that they launch on.  A decoded token's call is a
-# few microseconds of GPU time, so the checks are kept short.
+# Their binding is compiled (csrc/la_torch.cpp): it checks shapes, types and
+# devices, takes views, allocates what a call returns or needs as workspace on
+# the stream that it launches on, and calls the library in use.  Raises
+# ValueError or TypeError for arguments it refuses, LAError for what the library
+# answers.
 
-def _need(ok, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
-def _like(name, t, shape, dtype, dev: int):
-    """t (or None) has this shape, type and device."""
-    if t is not None:
-        if t.shape != shape:
-            raise ValueError("%s must have shape %s" % (name, tuple(shape)))
-        if t.dtype is not dtype:
-            raise TypeError("%s must be %s" % (name, dtype))
-        if t.get_device() != dev:
-            raise ValueError("%s must be on the same device as the rest" % name)
+_binding = None
+_binding_for = None
 
 
-def _state(name, t, shape, dev: int):
-    """_like for what the library takes as a plain fp32 array."""
-    if t is not None:
-        _like(name, t, shape, torch.float32, dev)
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
+def _bound():
+    """The compiled binding, calling the library in use."""
+    global _binding, _binding_for
+    L = lib()
+    if _binding_for is not L:
+        if _binding is None:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError("%s is not built; run `python -m weight_recurrence_gb300.build`" % BINDING_PATH)
+            loader = importlib.machinery.ExtensionFileLoader("_la_torch", BINDING_PATH)
+            spec = importlib.util.spec_from_file_location("_la_torch", BINDING_PATH, loader=loader)
+            _binding = importlib.util.module_from_spec(spec)
+            loader.exec_module(_binding)
+        _binding.use(L._name)
+        _binding_for = L
+    return _binding
 
 
-def _launch_stream(stream, dev: int) -> int:
-    """The stream's handle; dev has to be the current CUDA device."""
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    if dev != torch.cuda.current_device():
-        raise ValueError("tensors must be on the current CUDA device")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _empty(stream, like, shape, dtype):
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):   # memory of the stream that uses it
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _out_like(stream, t):
-    """A contiguous tensor of t's shape and type (empty_like parses less than empty)."""
-    if stream is None and t.is_contiguous():
-        return torch.empty_like(t)
-    return _empty(stream, t, t.shape, t.dtype)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _view(name, t, step: bool = False) -> la_view:
-    """Rows of [B,N,D] or [B,H,N,D] ([B,D] or [B,H,D] for a step) as a la_view."""
-    if t is None:
-        return la_view(None, 0, 0, 0)
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError("%s: the channels must be contiguous" % name)
-    if step:
-        return la_view(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0, 0)
-    return la_view(t.data_ptr(), st[0], st[1] if len(st) == 4 else 0, st[-2])
-
-
-def _rec_shape(x, step: bool) -> la_shape:
-    sh = x.shape
-    lead = len(sh) - (1 if step else 2)
-    if lead not in (1, 2):
-        raise ValueError("x must be [B,D] or [B,H,D]" if step else "x must be [B,N,D] or [B,H,N,D]")
-    if sh[-1] < 1:
-        raise ValueError("x must have a channel")
-    return la_shape(sh[0], sh[1] if lead == 2 else 1, 1 if step else sh[-2], sh[-1], 0, _dtype_code(x.dtype))
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def _gate_code(gate: str) -> int:
@@ -522,22 +477,6 @@ def _gate_code(gate: str) -> int:
     if code is None:
         raise ValueError("gate must be one of %s" % ", ".join(LA_GATE))
     return code
-
-
-def _lens(lens, B: int, dev: int):
-    if lens is not None:
-        if lens.dtype != torch.int32:
-            raise TypeError("lens must be torch.int32")
-        _need(lens.shape == (B,), "lens must have shape (%d,)" % B)
-        _need(lens.is_contiguous(), "lens must be contiguous")
-        _need(lens.get_device() == dev, "lens must be on the same device as the rest")
-
-
-def _recurrence_ws(s, stream, like):
-    need = lib().la_recurrence_workspace_bytes(s)
-    if need == _SIZE_MAX:   # the call itself says what is wrong
-        need = 0
-    return need, _empty(stream, like, (need,), torch.uint8) if need else None
 
 
 def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens=None, stream=None):
@@ -548,21 +487,7 @@ def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens
     u = (1 - a) x).  h0, hN: fp32 states [B,D] or [B,H,D], read before the
     first token and written after the last; hN may be h0.  lens: int32 [B];
     rows past a length are 0.  Returns out."""
-    s = _rec_shape(x, False)
-    code = _gate_code(gate)
-    dev = x.get_device()
-    _like("g", g, x.shape, x.dtype, dev)
-    _like("out", out, x.shape, x.dtype, dev)
-    state = x.shape[:-2] + x.shape[-1:]
-    _state("h0", h0, state, dev)
-    _state("hN", hN, state, dev)
-    _lens(lens, s.B, dev)
-    sp = _launch_stream(stream, dev)
-    if out is None:
-        out = _out_like(stream, x)
-    need, ws = _recurrence_ws(s, stream, x)
-    st = lib().la_recurrence_forward(_view("x", x), _view("g", g), _view("out", out), _addr(lens), s, code, _addr(h0),
-                                     _addr(hN), _addr(ws), need, sp)
+    st, out = _bound().recurrence_forward(x, g, _gate_code(gate), out, h0, hN, lens, _handle(stream))
     _check(st, "la_recurrence_forward")
     return out
 
@@ -570,18 +495,7 @@ def la_recurrence_forward(x, g, gate="sigmoid", out=None, h0=None, hN=None, lens
 def la_recurrence_step(x, g, h, gate="sigmoid", y=None, stream=None):
     """One token of the recurrence: x, g [B,D] or [B,H,D]; h the fp32 state of
     the same shape, updated in place.  Returns y = h in x's type."""
-    s = _rec_shape(x, True)
-    code = _gate_code(gate)
-    dev = x.get_device()
-    _need(h is not None, "h is required")
-    _like("g", g, x.shape, x.dtype, dev)
-    _like("y", y, x.shape, x.dtype, dev)
-    _state("h", h, x.shape, dev)
-    sp = _launch_stream(stream, dev)
-    if y is None:
-        y = _out_like(stream, x)
-    st = lib().la_recurrence_step(_view("x", x, True), _view("g", g, True), _view("y", y, True), s, code,
-                                  h.data_ptr(), sp)
+    st, y = _bound().recurrence_step(x, g, h, _gate_code(gate), y, _handle(stream))
     _check(st, "la_recurrence_step")
     return y
 
@@ -592,48 +506,10 @@ def la_recurrence_backward(x, g, out, dout, gate="sigmoid", h0=None, dhN=None, d
     dL/dout.  h0, lens: as given to the forward; dhN: gradient of its hN; dh0
     (fp32, written): gradient of h0, may be dhN.  x is read by the sigmoid
     gate only and may be None for the others."""
-    s = _rec_shape(g, False)
-    code = _gate_code(gate)
-    _need(x is not None or gate != "sigmoid", "the sigmoid gate needs x")
-    dev = g.get_device()
-    for name, t in (("x", x), ("out", out), ("dout", dout), ("dx", dx), ("dg", dg)):
-        _like(name, t, g.shape, g.dtype, dev)
-    state = g.shape[:-2] + g.shape[-1:]
-    _state("h0", h0, state, dev)
-    _state("dhN", dhN, state, dev)
-    _state("dh0", dh0, state, dev)
-    _lens(lens, s.B, dev)
-    sp = _launch_stream(stream, dev)
-    if dx is None:
-        dx = _out_like(stream, g)
-    if dg is None:
-        dg = _out_like(stream, g)
-    need, ws = _recurrence_ws(s, stream, g)
-    st = lib().la_recurrence_backward(_view("x", x), _view("g", g), _view("out", out), _view("dout", dout),
-                                      _view("dx", dx), _view("dg", dg), _addr(lens), s, code, _addr(h0), _addr(dhN),
-                                      _addr(dh0), _addr(ws), need, sp)
+    st, dx, dg = _bound().recurrence_backward(x, g, out, dout, _gate_code(gate), h0, dhN, dh0, lens, dx, dg,
+                                              _handle(stream))
     _check(st, "la_recurrence_backward")
     return dx, dg
-
-
-def _rows(name, t) -> la_rows:
-    """All rows (last dimension) of t as one strided list."""
-    if t is None:
-        return la_rows(None, 0)
-    if t.is_contiguous():
-        return la_rows(t.data_ptr(), t.shape[-1])
-    st, sh = t.stride(), t.shape
-    _need(st[-1] == 1 or sh[-1] <= 1, "%s: the last dimension must be contiguous" % name)
-    stride = extent = None
-    for d in range(t.dim() - 2, -1, -1):
-        if sh[d] == 1:
-            continue
-        if stride is None:
-            stride, extent = st[d], st[d] * sh[d]
-        else:
-            _need(st[d] == extent, "%s: the rows must share one stride" % name)
-            extent = st[d] * sh[d]
-    return la_rows(t.data_ptr(), sh[-1] if stride is None else stride)
 
 
 def la_layernorm_forward(x, w=None, b=None, eps=1e-5, res=None, y=None, sum=None, mean=None, rstd=None, stats=True,
@@ -642,118 +518,35 @@ def la_layernorm_forward(x, w=None, b=None, eps=1e-5, res=None, y=None, sum=None
     in front when res is given.  w, b: fp32 [C] or None.  Returns (y, s, mean,
     rstd): s is x itself without res; mean and rstd (fp32, for the backward)
     are None with stats=False.  sum: where s goes (may be x or res)."""
-    sh, dtype, dev = x.shape, x.dtype, x.get_device()
-    _need(len(sh) >= 1 and sh[-1] >= 1, "x must have rows of at least one value")
-    code = _dtype_code(dtype)
-    C, lead = sh[-1], sh[:-1]
-    _need(sum is None or res is not None, "sum needs res")
-    _need(stats or (mean is None and rstd is None), "mean and rstd need stats")
-    _like("res", res, sh, dtype, dev)
-    _like("sum", sum, sh, dtype, dev)
-    _like("y", y, sh, dtype, dev)
-    _state("w", w, (C,), dev)
-    _state("b", b, (C,), dev)
-    _state("mean", mean, lead, dev)
-    _state("rstd", rstd, lead, dev)
-    sp = _launch_stream(stream, dev)
-    if y is None:
-        y = _out_like(stream, x)
-    if res is not None and sum is None:
-        sum = _out_like(stream, x)
-    if stats:
-        mean = _empty(stream, x, lead, torch.float32) if mean is None else mean
-        rstd = _out_like(stream, mean) if rstd is None else rstd
-    st = lib().la_layernorm_forward(_rows("x", x), _rows("res", res), _rows("sum", sum), _rows("y", y), _addr(w),
-                                    _addr(b), _addr(mean), _addr(rstd), x.numel() // C, C, code, eps, sp)
+    st, y, s, mean, rstd = _bound().layernorm_forward(x, w, b, eps, res, y, sum, mean, rstd, stats, _handle(stream))
     _check(st, "la_layernorm_forward")
-    return y, (x if res is None else sum), mean, rstd
+    return y, s, mean, rstd
 
 
 def la_layernorm_backward(dy, s, w, mean, rstd, dsum=None, ds=None, dw=None, db=None, stream=None):
     """Gradients (ds, dw, db) of la_layernorm_forward given dy = dL/dy, the s,
     mean and rstd it returned and, where s went on as the residual stream,
     dsum = dL/ds.  ds is the gradient of x and of res; w may be None (1)."""
-    sh, dtype, dev = dy.shape, dy.dtype, dy.get_device()
-    _need(len(sh) >= 1 and sh[-1] >= 1, "dy must have rows of at least one value")
-    code = _dtype_code(dtype)
-    C, lead = sh[-1], sh[:-1]
-    _need(mean is not None and rstd is not None, "mean and rstd are required")
-    _like("s", s, sh, dtype, dev)
-    _like("dsum", dsum, sh, dtype, dev)
-    _like("ds", ds, sh, dtype, dev)
-    _state("w", w, (C,), dev)
-    _state("mean", mean, lead, dev)
-    _state("rstd", rstd, lead, dev)
-    _state("dw", dw, (C,), dev)
-    _state("db", db, (C,), dev)
-    sp = _launch_stream(stream, dev)
-    if ds is None:
-        ds = _out_like(stream, dy)
-    if dw is None:
-        dw = _empty(stream, dy, (C,), torch.float32)
-    if db is None:
-        db = _out_like(stream, dw)
-    rows = dy.numel() // C
-    need = lib().la_layernorm_workspace_bytes(rows, C, code)
-    if need == _SIZE_MAX:
-        raise LAError(LA_ERR_UNSUPPORTED, "la_layernorm_workspace_bytes")
-    ws = _empty(stream, dy, (need,), torch.uint8) if need else None
-    st = lib().la_layernorm_backward(_rows("dy", dy), _rows("s", s), _rows("dsum", dsum), _rows("ds", ds), _addr(w),
-                                     mean.data_ptr(), rstd.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, C, code,
-                                     _addr(ws), need, sp)
+    st, ds, dw, db = _bound().layernorm_backward(dy, s, w, mean, rstd, dsum, ds, dw, db, _handle(stream))
     _check(st, "la_layernorm_backward")
     return ds, dw, db
 
 
-_tensor_code = {torch.float32: LA_DTYPE_F32, torch.bfloat16: LA_DTYPE_BF16}
-
-
-def _grad_call(name, grads, out, norm, stream, *args):
-    """Packs the la_tensor table (one struct.pack for all of it) and calls."""
-    n, T = len(grads), torch.Tensor
-    _need(n > 0, "no tensors")
-    dev = grads[0].get_device()
-    if not all(map(T.is_contiguous, grads)):
-        raise ValueError("tensors must be contiguous")
-    codes = [_tensor_code.get(t.dtype) for t in grads]
-    if None in codes:
-        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % grads[codes.index(None)].dtype)
-    _need(set(map(T.get_device, grads)) == {dev}, "all tensors must be on one device")
-    table = [0] * (4 * n)   # src, dst, n, dtype of every tensor in turn
-    table[0::4] = map(T.data_ptr, grads)
-    table[2::4] = map(T.numel, grads)
-    table[3::4] = codes
-    if out is grads:
-        table[1::4] = table[0::4]
-    elif out is not None:
-        _need(len(out) == n, "out must have one tensor per gradient")
-        if list(map(T.numel, out)) != table[2::4] or [_tensor_code.get(t.dtype) for t in out] != codes:
-            raise ValueError("out must have the gradients' sizes and types")
-        _need(all(map(T.is_contiguous, out)), "out must be contiguous")
-        _need(set(map(T.get_device, out)) == {dev}, "all tensors must be on one device")
-        table[1::4] = map(T.data_ptr, out)
-    _state("norm", norm, (), dev)
-    sp = _launch_stream(stream, dev)
-    if norm is None:
-        norm = _empty(stream, grads[0], (), torch.float32)
-    need = lib().la_grad_workspace_bytes(n)
-    ws = _empty(stream, grads[0], (need,), torch.uint8)
-    st = getattr(lib(), name)(struct.pack("PPqi4x" * n, *table), n, *args, norm.data_ptr(), ws.data_ptr(), need, sp)
-    _check(st, name)
+def la_grad_norm(grads, norm=None, stream=None):
+    """Global norm sqrt(sum of all squares) over a list of contiguous tensors,
+    an fp32 scalar on the device."""
+    st, norm = _bound().grad(grads, None, None, norm, _handle(stream))
+    _check(st, "la_grad_norm")
     return norm
 
 
-def la_grad_norm(grads, norm=None, stream=None):
-    """Global norm sqrt(sum of all squares) over a list of tensors, an fp32 scalar on the device."""
-    return _grad_call("la_grad_norm", list(grads), None, norm, stream)
-
-
 def la_grad_clip(grads, max_norm, out=None, norm=None, stream=None):
-    """Scales every tensor by min(1, max_norm / (norm + 1e-6)) with the global
-    norm, in place or into the tensors of out; returns the norm (an fp32
-    scalar on the device)."""
-    grads = list(grads)
-    return _grad_call("la_grad_clip", grads, grads if out is None else list(out), norm, stream, float(max_norm))
+    """Scales every tensor of a list by min(1, max_norm / (norm + 1e-6)) with
+    the global norm, in place or into the tensors of out; returns the norm (an
+    fp32 scalar on the device)."""
+    st, norm = _bound().grad(grads, float(max_norm), out, norm, _handle(stream))
+    _check(st, "la_grad_clip")
+    return norm
 
 
 def la_get_last_error(stream=None, device=None) -> int:
