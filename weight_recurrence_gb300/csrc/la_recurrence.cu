@@ -74,6 +74,25 @@ template <> struct Raw<__nv_bfloat16, 4> {
     }
 };
 
+// A strip's row as the lanes share it.  WIDE (every row starts on 16 bytes and D
+// fills 16-byte pieces): V neighbouring channels each.  Else V channels 32 apart,
+// loaded and stored one by one, the lanes' next to one another.
+template <typename T, int V, bool WIDE> struct Row {
+    static __device__ __forceinline__ int channel(int lane, int v) { return WIDE ? lane * V + v : v * 32 + lane; }
+    // channel of position `at` among the lanes' values in order
+    static __device__ __forceinline__ int channel_at(int at) { return WIDE ? at : at % V * 32 + at / V; }
+    // p: the row's first channel of the strip, of which `left` exist
+    static __device__ __forceinline__ void store(T *p, int lane, int left, const Lanes<V> &x) {
+        if constexpr (WIDE) {
+            if (lane * V < left) *reinterpret_cast<typename Raw<T, V>::type *>(p + lane * V) = Raw<T, V>::put(x);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                if (channel(lane, v) < left) p[channel(lane, v)] = from_f32<T>(x.get(v));
+        }
+    }
+};
+
 // A product of gates past fp32's range would turn an empty state into NaN
 // (inf * 0): it is held at the largest finite value instead.
 __device__ __forceinline__ float finite(float A) {
@@ -108,17 +127,18 @@ template <int V> __device__ __forceinline__ Lanes<V> finite(const Lanes<V> &A) {
     return r;
 }
 
-template <int V, int W> struct Join {
+template <typename Row, int V, int W> struct Join {
     using J = Joint<V, W>;
     J &j;
-    int warp, lane, channel, sub;
+    int warp, lane, at, sub; // at: position of the owned channel, sub: which of its owners
+    int channel;
     float state;             // of the owned channel
     int set = 0;
 
     // first: the strip's first channel of the state before the CTA's rows.
     __device__ __forceinline__ Join(J &j_, const float *first, int left)
-        : j(j_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), channel(threadIdx.x / J::G),
-          sub(threadIdx.x % J::G) {
+        : j(j_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), at(threadIdx.x / J::G), sub(threadIdx.x % J::G),
+          channel(Row::channel_at(threadIdx.x / J::G)) {
         state = first && channel < left ? first[channel] : 0.f;
     }
     // Over the segments before this one; maps: their strip's first channel,
@@ -150,7 +170,7 @@ template <int V, int W> struct Join {
         __syncthreads();
         float a[V], h[V], ta = 1.f, th = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; i++) a[i] = j.A[set][sub * V + i][channel], h[i] = j.H[set][sub * V + i][channel];
+        for (int i = 0; i < V; i++) a[i] = j.A[set][sub * V + i][at], h[i] = j.H[set][sub * V + i][at];
 #pragma unroll
         for (int i = 0; i < V; i++) ta *= a[i], th = fmaf(a[i], th, h[i]);
         ta = finite(ta);
@@ -171,7 +191,7 @@ template <int V, int W> struct Join {
         state = fmaf(ta, state, th);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            j.H[set][sub * V + i][channel] = before;
+            j.H[set][sub * V + i][at] = before;
             before = fmaf(a[i], before, h[i]);
         }
         __syncthreads();
@@ -207,80 +227,58 @@ template <int V> struct Place {
     __device__ __forceinline__ bool last() const { return to == len && (from < to || segment == 0); }
 };
 
-// Stores a lane's channels of a row (p: the row's first channel of the strip, of
-// which `left` exist; a lane has all V or none: D is a multiple of V).
-template <typename T, int V> __device__ __forceinline__ void store_row(T *p, int lane, int left, const Lanes<V> &x) {
-    if (lane * V < left) *reinterpret_cast<typename Raw<T, V>::type *>(p + lane * V) = Raw<T, V>::put(x);
-}
-
 // Rows at or past a sequence's length become 0, the segments taking turns.
-template <typename T, int V, int W>
+template <typename Row, typename T, int V, int W>
 __device__ __forceinline__ void clear_rows(T *p, long long sn, const Place<V> &q, const Dims &s) {
     for (long long t = q.len + q.segment * W + (threadIdx.x >> 5); t < s.N; t += s.segments * W)
-        store_row<T, V>(p + t * sn, threadIdx.x & 31, q.left, all<V>(0.f));
+        Row::store(p + t * sn, threadIdx.x & 31, q.left, all<V>(0.f));
 }
 
-// A warp's rows of NT tensors on their way through shared memory, S tiles deep.
-// WIDE: every row starts on 16 bytes and its channels fill 16-byte pieces:
-// neighbouring lanes copy neighbouring pieces, two or four rows a request.  Else
-// each lane copies its own V channels: 4 or 8 bytes asynchronously, single bf16
-// values through registers, which reach shared memory a tile later.
+// A warp's rows of NT tensors on their way through shared memory, S tiles deep,
+// in 16-byte pieces: neighbouring lanes copy neighbouring pieces, two or four rows
+// a request.  A row that does not start on 16 bytes is copied from the boundary
+// before it (so a copy begins up to 15 bytes before the row, in a piece that holds
+// some of it, and never ends past it) and is read from where it starts in the
+// first piece; copies of single values held the memory pipe up.
 template <typename T, int V, int NT, int R, int S, bool WIDE> struct Ring {
-    using RT = typename Raw<T, V>::type;
-    static constexpr bool kHeld = sizeof(RT) < 4;
-    RT (*slot)[NT][R][32];   // [S], this warp's
+    static constexpr int kRow = 32 * V * (int)sizeof(T), kPieces = kRow / 16, kRows = 32 / kPieces;
+    static constexpr int kPitch = kRow + (WIDE ? 0 : 16);
+    using Slot = unsigned char (*)[NT][R][kPitch];
+    Slot slot;               // [S], this warp's
     int lane;
-    RT held[kHeld ? NT : 1][kHeld ? R : 1] = {};
-    int held_stage = -1;
 
-    __device__ __forceinline__ Ring(RT (*slot_)[NT][R][32], int lane_) : slot(slot_), lane(lane_) {}
-
-    // Before the copies of a tile.
-    __device__ __forceinline__ void begin(int stage) {
-        if constexpr (kHeld) {
-            if (held_stage >= 0) {
-#pragma unroll
-                for (int k = 0; k < NT; k++)
-#pragma unroll
-                    for (int r = 0; r < R; r++) slot[held_stage][k][r][lane] = held[k][r];
-            }
-            held_stage = stage;
-        }
+    static __device__ __forceinline__ void copy16(unsigned char *to, const unsigned char *from, int bytes) {
+        if constexpr (WIDE)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
+        else
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)), "l"(from),
+                         "r"(min(bytes, 16))
+                         : "memory");
     }
-
     // Rows 0 .. n - 1 of tensor `k`: row r at p + r * sn (p: the row's first
     // channel of the strip), `left` channels of it exist.
-    __device__ __forceinline__ void copy(int stage, int k, const T *p, long long sn, int n, int left) {
+    __device__ __forceinline__ void copy(int stage, int k, const T *p, long long sn, int n, int left) const {
+        const int piece = lane % kPieces, row = lane / kPieces, bytes = min(left * (int)sizeof(T), kRow);
+        const long long step = sn * (long long)sizeof(T);
+        const unsigned char *from = reinterpret_cast<const unsigned char *>(p) + row * step;
+        unsigned char *to = slot[stage][k][row] + piece * 16;
         if constexpr (WIDE) {
-            constexpr int kPieces = 32 * V * (int)sizeof(T) / 16, kRows = 32 / kPieces, kPer = 16 / (int)sizeof(T);
-            const int piece = lane % kPieces;
-            p += piece * kPer + (lane / kPieces) * sn;
-            unsigned char *to = reinterpret_cast<unsigned char *>(slot[stage][k][lane / kPieces]) + piece * 16;
-            if (piece * kPer < left) {
+            if (piece * 16 < bytes) {
+                from += piece * 16;
 #pragma unroll
-                for (int r = 0; r < R; r += kRows, p += kRows * sn)
-                    if (r + lane / kPieces < n)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                         tc::smem_u32(to + r * 32 * (int)sizeof(RT))),
-                                     "l"(p)
-                                     : "memory");
+                for (int r = 0; r < R; r += kRows, from += kRows * step)
+                    if (r + row < n) copy16(to + r * kPitch, from, 16);
             }
         } else {
-            p += lane * V;
-            if (lane * V < left) {
 #pragma unroll
-                for (int r = 0; r < R; r++, p += sn) {
-                    if (r < n) {
-                        if constexpr (sizeof(RT) >= 4)
-                            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
-                                             tc::smem_u32(&slot[stage][k][r][lane])),
-                                         "l"(p), "n"(sizeof(RT))
-                                         : "memory");
-                        else
-                            held[k][r] = *reinterpret_cast<const RT *>(p);
-                    }
-                }
+            for (int r = 0; r < R; r += kRows, from += kRows * step) {
+                const int shift = (int)(reinterpret_cast<uintptr_t>(from) & 15), have = shift + bytes - piece * 16;
+                if (r + row < n && have > 0) copy16(to + r * kPitch, from - shift + piece * 16, have);
             }
+            // the piece that a shifted row has more, of every row
+            from = reinterpret_cast<const unsigned char *>(p) + lane * step;
+            const int shift = (int)(reinterpret_cast<uintptr_t>(from) & 15), have = shift + bytes - kRow;
+            if (lane < R && lane < n && have > 0) copy16(slot[stage][k][lane] + kRow, from - shift + kRow, have);
         }
     }
     __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -289,30 +287,48 @@ template <typename T, int V, int NT, int R, int S, bool WIDE> struct Ring {
         asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
         __syncwarp();
     }
-    __device__ __forceinline__ Lanes<V> get(int stage, int k, int r) const { return Raw<T, V>::get(slot[stage][k][r][lane]); }
+    // Row r of tensor k, whose rows were copied from p on (row 0), sn apart.
+    __device__ __forceinline__ Lanes<V> get(int stage, int k, int r, const T *p, long long sn) const {
+        if constexpr (WIDE) {
+            using RT = typename Raw<T, V>::type;
+            return Raw<T, V>::get(reinterpret_cast<const RT *>(slot[stage][k][r])[lane]);
+        } else {
+            const unsigned shift = ((unsigned)reinterpret_cast<uintptr_t>(p) + r * (unsigned)sn * (unsigned)sizeof(T)) & 15u;
+            const T *row = reinterpret_cast<const T *>(slot[stage][k][r] + shift);
+            Lanes<V> x;
+#pragma unroll
+            for (int v = 0; v < V; v++) x.set(v, to_f32<T>(row[v * 32 + lane]));
+            return x;
+        }
+    }
 };
 
-template <typename T, int V, int W, int NT, int R, int S> struct Tiles {
-    typename Raw<T, V>::type slot[W][S][NT][R][32];
-    Joint<V, W> joint;
+template <typename Ring, int W, int NT, int R, int S> using Slots = unsigned char[W][S][NT][R][Ring::kPitch];
+
+template <typename T, int V, bool WIDE, int W, int R, int S> struct Tiles {
+    using Row = la::Row<T, V, WIDE>;
+    using Ring = la::Ring<T, V, 2, R, S, WIDE>;
+    __align__(16) Slots<Ring, W, 2, R, S> slot;
+    __align__(16) Joint<V, W> joint;
 };
 
 template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la_view g, la_view out, Dims s,
                                                                   const float *h0, float *hN) {
+    using Sh = Tiles<T, V, WIDE, W, R, S>;
+    using Row = typename Sh::Row;
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &sh = *reinterpret_cast<Tiles<T, V, W, 2, R, S> *>(smem);
+    auto &sh = *reinterpret_cast<Sh *>(smem);
     pdl_wait_cta();
     const Place<V> q(s, s.segments);
-    Join<V, W> join(sh.joint, s.segments > 1 ? s.start + q.at : h0 ? h0 + q.at : nullptr, q.left);
-    Ring<T, V, 2, R, S, WIDE> ring(sh.slot[join.warp], join.lane);
+    Join<Row, V, W> join(sh.joint, s.segments > 1 ? s.start + q.at : h0 ? h0 + q.at : nullptr, q.left);
+    const typename Sh::Ring ring{sh.slot[join.warp], join.lane};
     const T *px = q.template strip<T>(x), *pg = q.template strip<T>(g);
     T *po = q.template strip<T>(out);
     const long long first = q.from + join.warp * R;   // this warp's rows in the first tile
     const int tiles = (int)((q.to - q.from + W * R - 1) / (W * R));
     auto fetch = [&](int it, int stage) {
         const long long t = first + (long long)it * (W * R);
-        ring.begin(stage);
         if (t < q.to) {
             const int n = (int)min((long long)R, q.to - t);
             ring.copy(stage, 0, px + t * x.sn, x.sn, n, q.left);
@@ -327,12 +343,14 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
         ring.template wait<S - 1>();
         const long long t0 = first + (long long)it * (W * R);
         const int n = (int)min((long long)R, max(q.to - t0, 0LL));
+        const T *rx = px + t0 * x.sn, *rg = pg + t0 * g.sn;
         Lanes<V> a[R], u[R];
 #pragma unroll
         for (int r = 0; r < R; r++) {
             Lanes<V> w;
-            gate_of<GATE, V>(ring.get(stage, 1, r), a[r], w);
-            u[r] = GATE == LA_GATE_SIGMOID ? mul(w, ring.get(stage, 0, r)) : ring.get(stage, 0, r);
+            gate_of<GATE, V>(ring.get(stage, 1, r, rg, g.sn), a[r], w);
+            u[r] = ring.get(stage, 0, r, rx, x.sn);
+            if (GATE == LA_GATE_SIGMOID) u[r] = mul(w, u[r]);
         }
         __syncwarp();   // the stage is free
         fetch(it + S, stage);
@@ -350,39 +368,43 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
 #pragma unroll
         for (int r = 0; r < R; r++, p += out.sn) {
             h = fma(a[r], h, u[r]);
-            if (r < n) store_row<T, V>(p, join.lane, q.left, h);
+            if (r < n) Row::store(p, join.lane, q.left, h);
         }
     }
-    clear_rows<T, V, W>(po, out.sn, q, s);
+    clear_rows<Row, T, V, W>(po, out.sn, q, s);
     if (q.last()) join.end(hN ? hN + q.at : nullptr, q.left);
 }
 
 // (A, H) of every segment but the last, and a copy of the state that the walk
 // starts from (a caller's hN may be its h0).  Warps take consecutive eighths of
 // a segment and meet once at its end.  BACK: the backward's maps, of g and dout.
-template <typename T, int V, int W, int R, int S> struct MapTiles {
-    typename Raw<T, V>::type slot[W][S][2][R][32];
-    float A[W][32 * V], H[W][32 * V];
+template <typename T, int V, bool WIDE, int W, int R, int S> struct MapTiles {
+    using Row = la::Row<T, V, WIDE>;
+    using Ring = la::Ring<T, V, 2, R, S, WIDE>;
+    __align__(16) Slots<Ring, W, 2, R, S> slot;
+    __align__(16) float A[W][32 * V], H[W][32 * V];
 };
 template <typename T, int GATE, int V, bool WIDE, bool BACK, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_view x, Dims s, const float *state) {
+    using Sh = MapTiles<T, V, WIDE, W, R, S>;
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &sh = *reinterpret_cast<MapTiles<T, V, W, R, S> *>(smem);
+    auto &sh = *reinterpret_cast<Sh *>(smem);
     pdl_wait_cta();
     const Place<V> q(s, s.segments - 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Ring<T, V, 2, R, S, WIDE> ring(sh.slot[warp], lane);
+    const typename Sh::Ring ring{sh.slot[warp], lane};
     const T *px = q.template strip<T>(x), *pg = q.template strip<T>(g);
     const long long per = s.rows / W, first = min(q.from + warp * per, q.to), last = min(first + per, q.to);
     const int pieces = (int)((last - first + R - 1) / R);
+    const long long nx = BACK ? -x.sn : x.sn, ng = BACK ? -g.sn : g.sn;   // to the next row of the walk
+    px += (BACK ? q.len - 1 : 0) * x.sn + first * nx;
+    pg += (BACK ? q.len - 1 : 0) * g.sn + first * ng;
     auto fetch = [&](int i, int stage) {
-        const long long t = first + (long long)i * R;
-        ring.begin(stage);
-        if (t < last) {
-            const int n = (int)min((long long)R, last - t);
-            const long long row = BACK ? q.len - 1 - t : t;
-            ring.copy(stage, 0, px + row * x.sn, BACK ? -x.sn : x.sn, n, q.left);
-            ring.copy(stage, 1, pg + row * g.sn, BACK ? -g.sn : g.sn, n, q.left);
+        const long long t = (long long)i * R;
+        if (first + t < last) {
+            const int n = (int)min((long long)R, last - first - t);
+            ring.copy(stage, 0, px + t * nx, nx, n, q.left);
+            ring.copy(stage, 1, pg + t * ng, ng, n, q.left);
         }
         ring.commit();
     };
@@ -394,8 +416,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_vi
         const int n = (int)min((long long)R, last - (first + (long long)i * R));
         auto step = [&](int r) {
             Lanes<V> a, w;
-            gate_of<GATE, V>(ring.get(stage, 1, r), a, w);
-            const Lanes<V> v = ring.get(stage, 0, r);
+            gate_of<GATE, V>(ring.get(stage, 1, r, pg + (long long)i * R * ng, ng), a, w);
+            const Lanes<V> v = ring.get(stage, 0, r, px + (long long)i * R * nx, nx);
             A = mul(A, a);
             if (BACK) H = mul(a, add(v, H));
             else H = fma(a, H, GATE == LA_GATE_SIGMOID ? mul(w, v) : v);
@@ -413,15 +435,17 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_vi
     put_lanes(&sh.A[warp][lane * V], finite(A));
     put_lanes(&sh.H[warp][lane * V], H);
     __syncthreads();
-    for (int c = threadIdx.x; c < 32 * V && c < q.left; c += 32 * W) {
+    for (int c = threadIdx.x; c < 32 * V; c += 32 * W) {
+        const int d = Sh::Row::channel_at(c);
+        if (d >= q.left) continue;
         float a = 1.f, h = 0.f;
 #pragma unroll
         for (int w = 0; w < W; w++) {
             h = fmaf(sh.A[w][c], h, sh.H[w][c]);
             a = finite(a * sh.A[w][c]);
         }
-        s.maps[q.segment * s.channels + q.at + c] = make_float2(a, h);
-        if (q.segment == 0) s.start[q.at + c] = state ? state[q.at + c] : 0.f;
+        s.maps[q.segment * s.channels + q.at + d] = make_float2(a, h);
+        if (q.segment == 0) s.start[q.at + d] = state ? state[q.at + d] : 0.f;
     }
 }
 
@@ -477,9 +501,13 @@ __global__ void __launch_bounds__(kShortThreads) rec_short_kernel(la_view x, la_
 // which the token before adds to its own gradient.  The rows of g and dout are
 // free once they have become a, w and d, those of h_{t-1} and x only after the
 // join, so they go through two rings.
-template <typename T, int V, int W, int NL, int R, int S> struct BackTiles {
-    typename Raw<T, V>::type early[W][S][2][R][32], late[W][S][NL][R][32];
-    Joint<V, W> joint;
+template <typename T, int V, bool WIDE, int W, int NL, int R, int S> struct BackTiles {
+    using Row = la::Row<T, V, WIDE>;
+    using Early = Ring<T, V, 2, R, S, WIDE>;
+    using Late = Ring<T, V, NL, R, S, WIDE>;
+    __align__(16) Slots<Early, W, 2, R, S> early;
+    __align__(16) Slots<Late, W, NL, R, S> late;
+    __align__(16) Joint<V, W> joint;
 };
 
 template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
@@ -488,13 +516,15 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
                                                                    const float *dhN, float *dh0) {
     constexpr bool kSigmoid = GATE == LA_GATE_SIGMOID;
     constexpr int NL = kSigmoid ? 2 : 1;
+    using Sh = BackTiles<T, V, WIDE, W, NL, R, S>;
+    using Row = typename Sh::Row;
     extern __shared__ __align__(16) unsigned char smem[];
-    auto &sh = *reinterpret_cast<BackTiles<T, V, W, NL, R, S> *>(smem);
+    auto &sh = *reinterpret_cast<Sh *>(smem);
     pdl_wait_cta();
     const Place<V> q(s, s.segments);
-    Join<V, W> join(sh.joint, s.segments > 1 ? s.start + q.at : dhN ? dhN + q.at : nullptr, q.left);
-    Ring<T, V, 2, R, S, WIDE> early(sh.early[join.warp], join.lane);
-    Ring<T, V, NL, R, S, WIDE> late(sh.late[join.warp], join.lane);
+    Join<Row, V, W> join(sh.joint, s.segments > 1 ? s.start + q.at : dhN ? dhN + q.at : nullptr, q.left);
+    const typename Sh::Early early{sh.early[join.warp], join.lane};
+    const typename Sh::Late late{sh.late[join.warp], join.lane};
     const T *px = kSigmoid ? q.template strip<T>(x) : nullptr, *pg = q.template strip<T>(g);
     const T *po = q.template strip<T>(out), *pd = q.template strip<T>(dout);
     T *pdx = q.template strip<T>(dx), *pdg = q.template strip<T>(dg);
@@ -503,7 +533,6 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
     const int tiles = (int)((q.to - q.from + W * R - 1) / (W * R));
     auto fetch_early = [&](int it, int stage) {   // rows t, t - 1, ...
         const long long t = first - (long long)it * (W * R);
-        early.begin(stage);
         if (t >= end) {
             const int n = (int)min((long long)R, t - end + 1);
             early.copy(stage, 0, pg + t * g.sn, -g.sn, n, q.left);
@@ -513,7 +542,6 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
     };
     auto fetch_late = [&](int it, int stage) {
         const long long t = first - (long long)it * (W * R);
-        late.begin(stage);
         if (t >= end) {
             const int n = (int)min((long long)R, t - end + 1);
             late.copy(stage, 0, po + (t - 1) * out.sn, -out.sn, (int)min((long long)n, t), q.left);
@@ -528,11 +556,13 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
         early.template wait<2 * S - 1>();   // commits in turn: early, late, early, ...
         const long long t0 = first - (long long)it * (W * R);
         const int n = (int)min((long long)R, max(t0 - end + 1, 0LL));
+        const T *rg = pg + t0 * g.sn, *rd = pd + t0 * dout.sn, *rb = po + (t0 - 1) * out.sn;
+        const T *rx = kSigmoid ? px + t0 * x.sn : nullptr;
         Lanes<V> a[R], w[R], d[R];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-            d[r] = early.get(stage, 1, r);
-            gate_of<GATE, V>(early.get(stage, 0, r), a[r], w[r]);
+            d[r] = early.get(stage, 1, r, rd, -dout.sn);
+            gate_of<GATE, V>(early.get(stage, 0, r, rg, -g.sn), a[r], w[r]);
         }
         __syncwarp();
         fetch_early(it + S, stage);
@@ -549,11 +579,11 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
         T *to_x = pdx + t0 * dx.sn, *to_g = pdg + t0 * dg.sn;
 #pragma unroll
         for (int r = 0; r < R; r++, to_x -= dx.sn, to_g -= dg.sn) {
-            Lanes<V> before = late.get(stage, 0, r);
+            Lanes<V> before = late.get(stage, 0, r, rb, -out.sn);
             if (t0 == r) {   // the first token: the state that the forward started from
 #pragma unroll
                 for (int v = 0; v < V; v++) {
-                    const int c = join.lane * V + v;
+                    const int c = Row::channel(join.lane, v);
                     before.set(v, h0 && c < q.left ? h0[q.at + c] : 0.f);
                 }
             }
@@ -562,21 +592,21 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
             Lanes<V> ox = l, og;
             if constexpr (kSigmoid) {
                 ox = mul(l, w[r]);
-                og = mul(mul(mu, w[r]), fma(late.get(stage, NL - 1, r), all<V>(-1.f), before));
+                og = mul(mul(mu, w[r]), fma(late.get(stage, NL - 1, r, rx, -x.sn), all<V>(-1.f), before));
             } else {
                 og = mul(GATE == LA_GATE_LOG ? mu : l, before);
             }
             if (r < n) {
-                store_row<T, V>(to_x, join.lane, q.left, ox);
-                store_row<T, V>(to_g, join.lane, q.left, og);
+                Row::store(to_x, join.lane, q.left, ox);
+                Row::store(to_g, join.lane, q.left, og);
             }
         }
         __syncwarp();
         fetch_late(it + S, stage);
         stage = stage == S - 1 ? 0 : stage + 1;
     }
-    clear_rows<T, V, W>(pdx, dx.sn, q, s);
-    clear_rows<T, V, W>(pdg, dg.sn, q, s);
+    clear_rows<Row, T, V, W>(pdx, dx.sn, q, s);
+    clear_rows<Row, T, V, W>(pdg, dg.sn, q, s);
     if (q.last()) join.end(dh0 ? dh0 + q.at : nullptr, q.left);
 }
 
@@ -630,7 +660,7 @@ cudaError_t segment_maps(const RecProblem &p, const Dims &s) {
     if (s.segments == 1) return cudaSuccess;
     using C = Pre<32 * V * (int)sizeof(T)>;
     return launch_tiles<C>(rec_maps_kernel<T, GATE, V, WIDE, BACK, C::W, C::R, C::S, C::CTAS>,
-                           sizeof(MapTiles<T, V, C::W, C::R, C::S>), p, s, s.segments - 1, p.g, BACK ? p.dout : p.x, s,
+                           sizeof(MapTiles<T, V, WIDE, C::W, C::R, C::S>), p, s, s.segments - 1, p.g, BACK ? p.dout : p.x, s,
                            BACK ? p.dhN : p.h0);
 }
 
@@ -649,7 +679,7 @@ bool few_ctas(const RecProblem &p, const Dims &s) {
 
 struct Forward {
     template <typename T, int GATE, int V, bool WIDE> static cudaError_t run(const RecProblem &p) {
-        if (p.N <= kShortRows) return short_v<T, GATE, V>(p);
+        if (p.N <= kShortRows) return short_v<T, GATE, WIDE ? V : 1>(p);
         const Dims s = dims_of<V>(p);
         const cudaError_t e = segment_maps<T, GATE, V, WIDE, false>(p, s);
         if (e != cudaSuccess) return e;
@@ -659,7 +689,7 @@ struct Forward {
     template <typename T, int GATE, int V, bool WIDE, typename C>
     static cudaError_t tiles(const RecProblem &p, const Dims &s) {
         return launch_tiles<C>(rec_forward_kernel<T, GATE, V, WIDE, C::W, C::R, C::S, C::CTAS>,
-                               sizeof(Tiles<T, V, C::W, 2, C::R, C::S>), p, s, s.segments, p.x, p.g, p.out, s, p.h0,
+                               sizeof(Tiles<T, V, WIDE, C::W, C::R, C::S>), p, s, s.segments, p.x, p.g, p.out, s, p.h0,
                                p.hN);
     }
 };
@@ -675,7 +705,7 @@ struct Backward {
     template <typename T, int GATE, int V, bool WIDE, typename C>
     static cudaError_t tiles(const RecProblem &p, const Dims &s) {
         return launch_tiles<C>(rec_backward_kernel<T, GATE, V, WIDE, C::W, C::R, C::S, C::CTAS>,
-                               sizeof(BackTiles<T, V, C::W, GATE == LA_GATE_SIGMOID ? 2 : 1, C::R, C::S>), p, s,
+                               sizeof(BackTiles<T, V, WIDE, C::W, GATE == LA_GATE_SIGMOID ? 2 : 1, C::R, C::S>), p, s,
                                s.segments, p.x, p.g, p.out, p.dout, p.dx, p.dg, s, p.h0, p.dhN, p.dh0);
     }
 };
@@ -688,20 +718,18 @@ int row_alignment(const RecProblem &p, int size) {
     return (int)(bits & (~bits + 1));
 }
 
-// Channels a lane takes: 8 bytes of a row where rows start on 16 bytes (half of
-// that where the last strip would be less than half full), else 4, or one value.
+// Channels a lane takes: 8 bytes of a row, half of that where the last strip would
+// be less than half full.
+template <typename Call, typename T, int GATE> cudaError_t choose(const RecProblem &p) {
+    constexpr int V = 8 / (int)sizeof(T), C = 32 * V;
+    const bool half = p.D % C != 0 && p.D % C <= C / 2 && p.D < 8 * C;
+    if (row_alignment(p, sizeof(T)) == 16)
+        return half ? Call::template run<T, GATE, V / 2, true>(p) : Call::template run<T, GATE, V, true>(p);
+    return half ? Call::template run<T, GATE, V / 2, false>(p) : Call::template run<T, GATE, V, false>(p);
+}
+
 template <typename Call, int GATE> cudaError_t choose(const RecProblem &p) {
-    const bool f32 = p.dtype == LA_DTYPE_F32;
-    const int align = row_alignment(p, f32 ? 4 : 2), wide = f32 ? 64 : 128;
-    if (align == 16) {
-        const bool half = p.D % wide != 0 && p.D % wide <= wide / 2 && p.D < 8 * wide;
-        if (f32) return half ? Call::template run<float, GATE, 1, true>(p) : Call::template run<float, GATE, 2, true>(p);
-        return half ? Call::template run<__nv_bfloat16, GATE, 2, true>(p)
-                    : Call::template run<__nv_bfloat16, GATE, 4, true>(p);
-    }
-    if (f32) return Call::template run<float, GATE, 1, false>(p);
-    return align >= 4 ? Call::template run<__nv_bfloat16, GATE, 2, false>(p)
-                      : Call::template run<__nv_bfloat16, GATE, 1, false>(p);
+    return p.dtype == LA_DTYPE_F32 ? choose<Call, float, GATE>(p) : choose<Call, __nv_bfloat16, GATE>(p);
 }
 
 template <typename Call> cudaError_t choose_gate(const RecProblem &p) {
