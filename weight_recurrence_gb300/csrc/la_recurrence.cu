@@ -678,6 +678,7 @@ bool few_ctas(const RecProblem &p, const Dims &s) {
 }
 
 struct Forward {
+    static constexpr int kUnsplit = kSms / 2 + 1;
     template <typename T, int GATE, int V, bool WIDE> static cudaError_t run(const RecProblem &p) {
         if (p.N <= kShortRows) return short_v<T, GATE, WIDE ? V : 1>(p);
         const Dims s = dims_of<V>(p);
@@ -695,6 +696,7 @@ struct Forward {
 };
 
 struct Backward {
+    static constexpr int kUnsplit = kSms * 2 / 3 + 1;
     template <typename T, int GATE, int V, bool WIDE> static cudaError_t run(const RecProblem &p) {
         const Dims s = dims_of<V>(p);
         const cudaError_t e = segment_maps<T, GATE, V, WIDE, true>(p, s);
@@ -718,11 +720,17 @@ int row_alignment(const RecProblem &p, int size) {
     return (int)(bits & (~bits + 1));
 }
 
-// Channels a lane takes: 8 bytes of a row, half of that where the last strip would
-// be less than half full.
+// Channels a lane takes: 8 bytes of a row.  Half of that where the last strip would
+// be less than half full, and where it makes enough strips to do without segments:
+// from half as many as SMs in the forward, whose segments cost more (64 strips of
+// 4096 tokens, bf16: 53 us in segments, 36 us as 128 narrow strips; 40 of 8192: 68
+// and 62 us), from two thirds in the backward (the same: 80 and 68 us; 92 and 119 us).
 template <typename Call, typename T, int GATE> cudaError_t choose(const RecProblem &p) {
     constexpr int V = 8 / (int)sizeof(T), C = 32 * V;
-    const bool half = p.D % C != 0 && p.D % C <= C / 2 && p.D < 8 * C;
+    const long long heads = (long long)p.B * p.H, strips = heads * ((p.D + C - 1) / C);
+    const long long narrow = heads * ((p.D + C / 2 - 1) / (C / 2));
+    const bool half = (p.D % C != 0 && p.D % C <= C / 2 && p.D < 8 * C) ||
+                      (strips * 2 <= kSms && narrow >= Call::kUnsplit);
     if (row_alignment(p, sizeof(T)) == 16)
         return half ? Call::template run<T, GATE, V / 2, true>(p) : Call::template run<T, GATE, V, true>(p);
     return half ? Call::template run<T, GATE, V / 2, false>(p) : Call::template run<T, GATE, V, false>(p);
