@@ -93,7 +93,7 @@ template <typename T, int TPR, int K, bool WIDE> struct Share {
 // A thread's shares of NT tensors on their way, S rows deep: 16-byte pieces
 // through its own places in shared memory (no other thread touches them, so no
 // barrier), single values through registers, one row ahead.  S = 0: loaded when
-// they are taken (the widest rows, whose threads have no room for more).
+// they are taken (the widest rows, a CTA each, whose threads have no room for more).
 template <typename T, int TPR, int K, bool WIDE, int NT, int S> struct Feed {
     using Sh = Share<T, TPR, K, WIDE>;
     static constexpr bool kShared = WIDE && S > 0, kHeld = !WIDE && S > 0;
@@ -174,28 +174,45 @@ template <int TPR, int N> struct Sums {
 #pragma unroll
             for (int n = 0; n < N; n++) v[n] += __shfl_xor_sync(~0u, v[n], o);
         if constexpr (TPR > 32) {
-            const int warp = threadIdx.x / 32;
-            if (threadIdx.x % 32 == 0) {
+            constexpr int NW = TPR / 32;
+            const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+            if (lane == 0) {
 #pragma unroll
                 for (int n = 0; n < N; n++) sh[turn][n][warp] = v[n];
             }
             __syncthreads();
 #pragma unroll
             for (int n = 0; n < N; n++) {
-                // every warp adds the warps' sums in the same tree
-                float s = threadIdx.x % 32 < TPR / 32 ? sh[turn][n][threadIdx.x % 32] : 0.f;
+                // every thread adds the warps' sums in the same order
+                if constexpr (NW <= 8) {
+                    float s = sh[turn][n][0];
 #pragma unroll
-                for (int o = TPR / 64; o > 0; o /= 2) s += __shfl_xor_sync(~0u, s, o);
-                v[n] = __shfl_sync(~0u, s, 0);
+                    for (int i = 1; i < NW; i++) s += sh[turn][n][i];
+                    v[n] = s;
+                } else {
+                    float s = lane < NW ? sh[turn][n][lane] : 0.f;
+#pragma unroll
+                    for (int o = NW / 2; o > 0; o /= 2) s += __shfl_xor_sync(~0u, s, o);
+                    v[n] = __shfl_sync(~0u, s, 0);
+                }
             }
             turn ^= 1;
         }
     }
 };
 
-template <typename T> __device__ __forceinline__ T *row_at(const la_rows &v, long long r) {
-    return static_cast<T *>(v.data) + r * v.stride;
-}
+// A tensor's rows as a group meets them, `step` rows apart.
+template <typename T> struct Walk {
+    T *row;
+    long long to_next;
+    __device__ __forceinline__ Walk(const la_rows &v, long long first, long long step)
+        : row(static_cast<T *>(v.data) + first * v.stride), to_next(step * v.stride) {}
+    __device__ __forceinline__ T *next() {
+        T *r = row;
+        row += to_next;
+        return r;
+    }
+};
 
 template <int TPR> constexpr int threads_of() { return TPR > 256 ? TPR : TPR > 32 ? TPR : 256; }
 
@@ -211,16 +228,18 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_forward_kernel(Nor
     pdl_wait_cta();
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     F feed{smem + threadIdx.x, threads_of<TPR>(), lane, p.C};
-    const long long step = (long long)gridDim.x * GROUPS;
+    const long long step = (long long)gridDim.x * GROUPS, first = (long long)blockIdx.x * GROUPS + group;
+    Walk<const T> x_ahead(p.x, first, step), res_ahead(p.res, first, step), x_here = x_ahead, res_here = res_ahead;
+    Walk<T> sum_here(p.sum, first, step), y_here(p.y, first, step);
     auto fetch = [&](long long r, int stage) {
         if (r < p.rows) {
-            feed.fetch(stage, 0, row_at<T>(p.x, r));
-            if (p.res.data) feed.fetch(stage, 1, row_at<T>(p.res, r));
+            feed.fetch(stage, 0, x_ahead.next());
+            if (p.res.data) feed.fetch(stage, 1, res_ahead.next());
         }
         feed.commit();
     };
 #pragma unroll
-    for (int i = 0; i < F::DEPTH; i++) fetch((long long)blockIdx.x * GROUPS + group + i * step, i);
+    for (int i = 0; i < F::DEPTH; i++) fetch(first + i * step, i);
     float2 w[E2], b[E2];
     load_columns<TPR, K, Sh::VEC, WIDE>(w, p.w, lane, p.C, 1.f);
     load_columns<TPR, K, Sh::VEC, WIDE>(b, p.b, lane, p.C, 0.f);
@@ -228,20 +247,19 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_forward_kernel(Nor
     // a CTA's groups run the same number of rounds (their barriers and shuffles meet)
     for (long long base = (long long)blockIdx.x * GROUPS; base < p.rows; base += step) {
         const long long r = base + group;
-        const long long at = min(r, p.rows - 1);   // a group without a row takes along
         feed.wait();
-        Sh a = feed.take(stage, 0, row_at<T>(p.x, at));
+        Sh a = feed.take(stage, 0, x_here.next());
         float2 v[E2];
 #pragma unroll
         for (int i = 0; i < E2; i++) v[i] = a.get(i);
         if (p.res.data) {
-            const Sh c = feed.take(stage, 1, row_at<T>(p.res, at));
+            const Sh c = feed.take(stage, 1, res_here.next());
 #pragma unroll
             for (int i = 0; i < E2; i++) {   // the stream as it is kept, and normalised
                 a.set(i, add_pair(v[i], c.get(i)));
                 v[i] = a.get(i);
             }
-            if (p.sum.data && r < p.rows) a.store(row_at<T>(p.sum, r), lane, p.C);
+            if (p.sum.data && r < p.rows) a.store(sum_here.next(), lane, p.C);
         }
         fetch(r + F::DEPTH * step, stage);
         stage = stage == F::DEPTH - 1 ? 0 : stage + 1;
@@ -272,7 +290,7 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_forward_kernel(Nor
             Sh y;
 #pragma unroll
             for (int i = 0; i < E2; i++) y.set(i, fma_pair(mul_pair(v[i], make_float2(rstd, rstd)), w[i], b[i]));
-            y.store(row_at<T>(p.y, r), lane, p.C);
+            y.store(y_here.next(), lane, p.C);
             if (p.mean && lane == 0) p.mean[r] = mean, p.rstd[r] = rstd;
         }
     }
@@ -294,13 +312,16 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_backward_kernel(No
     pdl_wait_cta();
     const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
     F feed{smem + threadIdx.x, threads_of<TPR>(), lane, p.C};
-    const long long step = (long long)gridDim.x * GROUPS;
+    const long long step = (long long)gridDim.x * GROUPS, first = (long long)blockIdx.x * GROUPS + group;
+    Walk<const T> dy_ahead(p.y, first, step), s_ahead(p.x, first, step), dsum_ahead(p.res, first, step);
+    Walk<const T> dy_here = dy_ahead, s_here = s_ahead, dsum_here = dsum_ahead;
+    Walk<T> ds_here(p.ds, first, step);
     float mean = 0.f, rstd = 0.f;
     auto fetch = [&](long long r, int stage) {
         if (r < p.rows) {
-            feed.fetch(stage, 0, row_at<T>(p.y, r));
-            feed.fetch(stage, 1, row_at<T>(p.x, r));
-            if (p.res.data) feed.fetch(stage, 2, row_at<T>(p.res, r));
+            feed.fetch(stage, 0, dy_ahead.next());
+            feed.fetch(stage, 1, s_ahead.next());
+            if (p.res.data) feed.fetch(stage, 2, dsum_ahead.next());
         }
         feed.commit();
     };
@@ -308,8 +329,8 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_backward_kernel(No
         if (r < p.rows) mean = p.mean[r], rstd = p.rstd[r];
     };
 #pragma unroll
-    for (int i = 0; i < F::DEPTH; i++) fetch((long long)blockIdx.x * GROUPS + group + i * step, i);
-    next_stats((long long)blockIdx.x * GROUPS + group);
+    for (int i = 0; i < F::DEPTH; i++) fetch(first + i * step, i);
+    next_stats(first);
     float2 w[kOutside ? 1 : E2], dw[kOutside ? 1 : E2], db[kOutside ? 1 : E2];
     if constexpr (kOutside) {
 #pragma unroll
@@ -322,11 +343,10 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_backward_kernel(No
     int stage = 0;
     for (long long base = (long long)blockIdx.x * GROUPS; base < p.rows; base += step) {
         const long long r = base + group;
-        const long long at = min(r, p.rows - 1);
         feed.wait();
-        const Sh dy = feed.take(stage, 0, row_at<T>(p.y, at)), s = feed.take(stage, 1, row_at<T>(p.x, at));
+        const Sh dy = feed.take(stage, 0, dy_here.next()), s = feed.take(stage, 1, s_here.next());
         Sh extra;
-        if (p.res.data) extra = feed.take(stage, 2, row_at<T>(p.res, at));
+        if (p.res.data) extra = feed.take(stage, 2, dsum_here.next());
         const float2 m = make_float2(-mean, -mean), rs = make_float2(rstd, rstd);
         fetch(r + F::DEPTH * step, stage);
         next_stats(r + step);
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_backward_kernel(No
                 const float2 d = fma_pair(xh[i], b, add_pair(g[i], a));
                 ds.set(i, p.res.data ? fma_pair(rs, d, extra.get(i)) : mul_pair(rs, d));
             }
-            ds.store(row_at<T>(p.ds, r), lane, p.C);
+            ds.store(ds_here.next(), lane, p.C);
         }
     }
     if constexpr (GROUPS > 1) __syncthreads();   // every thread has taken its last rows
@@ -395,8 +415,9 @@ __global__ void __launch_bounds__(threads_of<TPR>(), CTAS) ln_backward_kernel(No
     }
 }
 
-// Adds the CTAs' column sums: 32 columns a CTA, its warps taking the parts in turn.
-constexpr int kFinishWarps = 16;
+// Adds the CTAs' column sums: 32 columns a CTA, its warps taking the parts in turn,
+// kAhead of them on their way at once (with 4 at once it took 9 us, whatever C).
+constexpr int kFinishWarps = 32, kAhead = 10;
 __global__ void __launch_bounds__(32 * kFinishWarps) ln_finish_kernel(const float *ws, float *dw, float *db, int C,
                                                                       int parts) {
     __shared__ float sh[kFinishWarps][33];
@@ -404,19 +425,29 @@ __global__ void __launch_bounds__(32 * kFinishWarps) ln_finish_kernel(const floa
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     float a = 0.f;
     if (c < 2 * C) {
-#pragma unroll 4
-        for (int i = warp; i < parts; i += kFinishWarps) a += ws[(long long)i * 2 * C + c];
+        for (int i0 = warp; i0 < parts; i0 += kAhead * kFinishWarps) {
+            float v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) {
+                const int i = i0 + k * kFinishWarps;
+                v[k] = i < parts ? ws[(long long)i * 2 * C + c] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; k++) a += v[k];
+        }
     }
     sh[warp][lane] = a;
     __syncthreads();
-    if (warp == 0 && c < 2 * C) {
-        a = 0.f;
+    static_assert(kFinishWarps == 32, "");   // warp w adds column w
+    a = sh[lane][warp];
 #pragma unroll
-        for (int w = 0; w < kFinishWarps; w++) a += sh[w][lane];
-        if (c < C) {
-            if (dw) dw[c] = a;
+    for (int o = 16; o > 0; o /= 2) a += __shfl_xor_sync(~0u, a, o);
+    const int column = blockIdx.x * 32 + warp;
+    if (lane == 0 && column < 2 * C) {
+        if (column < C) {
+            if (dw) dw[column] = a;
         } else if (db) {
-            db[c - C] = a;
+            db[column - C] = a;
         }
     }
 }
@@ -427,21 +458,22 @@ int ctas_of(long long rows, int groups, int per_sm) {
     return (int)std::min((long long)kSms * per_sm, (rows + groups - 1) / groups);
 }
 
-// Rows on their way (S) and CTAs a SM, within the registers and shared memory
-// that the widths leave.  Measured (bf16, forward | backward): rows of 64 13.3 |
-// 26.3 us for 262144 with 4 CTAs and 4 rows | 3 and 3 (5 and 3: 17.0; 4 and 2:
-// 32.2); rows of 2048 92.6 | 96.5 us for 32768 with 6 and 2 | 3 and 3 (4 and 4:
-// 98.1; 4 and 2: 111).
+// Rows on their way (S) and CTAs a SM (counted for CTAs of 256 threads), within the
+// registers and shared memory that the widths leave.  Measured (bf16, forward |
+// backward): 262144 rows of 64, a piece a thread: 13.3 | 24.2 us with 4 CTAs and 4
+// rows | 3 and 3 (forward with 5 and 3: 17.0, backward with 4 and 2: 32); 32768 rows
+// of 2048 with the residual, 4 pieces a thread: 86 | 91 us with 2 and 2 | 1 and 2
+// (forward with 3 CTAs, 80 registers: 114; backward with 1 row on its way: 100).
 template <typename T, int TPR, int K, bool WIDE> struct Shape {
-    static constexpr int THREADS = threads_of<TPR>(), PER = 256;   // CTAs counted for 256 threads
-    static constexpr bool kLean = WIDE || sizeof(T) == 4;          // single bf16 values take more registers
-    static constexpr int FWD_S = K == 1 ? (TPR <= 32 ? 4 : 2) : K == 4 ? 1 : THREADS == 1024 ? 2 : 3;
+    static constexpr int THREADS = threads_of<TPR>();
+    static constexpr bool kLean = WIDE || sizeof(T) == 4;   // single bf16 values take more registers
+    static constexpr int per_sm(int ctas) { return ctas * 256 / THREADS; }
+    static constexpr int FWD_S = THREADS == 1024 && K == 4 ? 1 : K == 1 ? 4 : 2;
     static constexpr int FWD_CTAS = THREADS == 1024  ? 1
                                     : THREADS == 512 ? (kLean ? 2 : 1)
-                                    : K == 1         ? (!kLean ? 2 : TPR <= 32 ? 4 : 6) * PER / THREADS
-                                                     : (kLean ? 4 : 2);
+                                                     : per_sm(K == 1 ? (kLean ? 4 : 2) : K == 2 ? (kLean ? 3 : 2) : 2);
     static constexpr int BWD_S = K == 1 ? 3 : THREADS < 1024 ? 2 : K == 2 && WIDE ? 1 : 0;
-    static constexpr int BWD_CTAS = THREADS >= 512 ? 1 : K == 1 ? (kLean ? 3 : 2) * PER / THREADS : kLean ? 2 : 1;
+    static constexpr int BWD_CTAS = THREADS >= 512 ? 1 : per_sm(K == 1 ? (kLean ? 3 : 2) : K == 2 ? (kLean ? 2 : 1) : 1);
 };
 
 struct Forward {
@@ -489,10 +521,17 @@ template <typename Call, typename T, bool WIDE> cudaError_t by_width(const NormP
     if (pieces <= 16) return Call::template run<T, 16, 1, WIDE>(p);
     if (pieces <= 32) return Call::template run<T, 32, 1, WIDE>(p);
     if (pieces <= 64) return Call::template run<T, 32, 2, WIDE>(p);
-    if (pieces <= 128) return Call::template run<T, 128, 1, WIDE>(p);
-    if (pieces <= 256) return Call::template run<T, 256, 1, WIDE>(p);
-    if (pieces <= 512) return Call::template run<T, 256, 2, WIDE>(p);
-    if (pieces <= 1024) return Call::template run<T, 512, 2, WIDE>(p);
+    if constexpr (WIDE) {   // 4 pieces a thread share the sums' cost (rows of 2048: 87 | 91 us, with 1 piece 89 | 103 us)
+        if (pieces <= 128) return Call::template run<T, 32, 4, WIDE>(p);
+        if (pieces <= 256) return Call::template run<T, 64, 4, WIDE>(p);
+        if (pieces <= 512) return Call::template run<T, 128, 4, WIDE>(p);
+        if (pieces <= 1024) return Call::template run<T, 256, 4, WIDE>(p);
+    } else {                // whose shares take more registers
+        if (pieces <= 128) return Call::template run<T, 64, 2, WIDE>(p);
+        if (pieces <= 256) return Call::template run<T, 128, 2, WIDE>(p);
+        if (pieces <= 512) return Call::template run<T, 256, 2, WIDE>(p);
+        if (pieces <= 1024) return Call::template run<T, 512, 2, WIDE>(p);
+    }
     if constexpr (sizeof(T) == 4)
         if (pieces > 2048) return Call::template run<T, 1024, 4, WIDE>(p);
     return Call::template run<T, 1024, 2, WIDE>(p);
