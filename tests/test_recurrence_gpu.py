@@ -340,6 +340,24 @@ def test_on_a_side_stream():
     assert torch.equal(out, want) and torch.equal(dx, wdx) and torch.equal(dg, wdg)
 
 
+def test_inputs_freed_right_after_a_call_on_another_stream():
+    """The allocator keeps memory that a given stream still reads."""
+    x, g, _, h0, _ = _inputs(1, 1, 20000, 256, torch.bfloat16, "sigmoid", 72)
+    want = la.la_recurrence_forward(x, g, h0=h0)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)          # about 10 ms: the call waits behind it
+    xs, gs = x.clone(), g.clone()
+    torch.cuda.current_stream().synchronize()
+    out = la.la_recurrence_forward(xs, gs, h0=h0, stream=side)
+    size = xs.shape
+    del xs, gs
+    rubbish = [torch.full(size, float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    side.synchronize()
+    assert torch.equal(out, want) and len(rubbish) == 2
+
+
 def test_in_a_graph():
     x, g, dout, h0, dhN = _inputs(2, 1, 600, 128, torch.bfloat16, "sigmoid", 81)
     hN, dh0 = torch.empty_like(h0), torch.empty_like(h0)

@@ -90,10 +90,12 @@ template <typename T = float> T *data(const at::Tensor &t) {
 }
 
 // The stream of a call (None: the current one, else its handle), and the place
-// where the call allocates.
+// where the call allocates.  The caller's tensors may be memory of another stream:
+// on a stream that was given, the allocator is told that they are in use there, so
+// that one freed right after the call is not handed out again too early.
 class Place {
   public:
-    Place(PyObject *stream, at::Device device) {
+    Place(PyObject *stream, at::Device device, std::initializer_list<const at::Tensor *> used) {
         if (!device.is_cuda()) bad_value("tensors must be on a CUDA device");
         if (device.index() != c10::cuda::current_device()) bad_value("tensors must be on the current CUDA device");
         if (stream == Py_None) {
@@ -101,10 +103,14 @@ class Place {
         } else {
             stream_ = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
             if (PyErr_Occurred()) throw Error{nullptr, ""};
-            guard_.reset_stream(c10::cuda::getStreamFromExternal(stream_, device.index()));
+            const auto given = c10::cuda::getStreamFromExternal(stream_, device.index());
+            for (const at::Tensor *t : used)
+                if (t->defined()) t->record_stream(given);
+            guard_.reset_stream(given);
         }
     }
     la_stream_t stream() const { return reinterpret_cast<la_stream_t>(stream_); }
+    void use(const at::Tensor &t) const { t.record_stream(*guard_.current_stream()); }
 
   private:
     cudaStream_t stream_;
@@ -200,7 +206,7 @@ PyObject *recurrence_forward(PyObject *const *a) {
     array("h0", h0, state, device);
     array("hN", hN, state, device);
     array("lens", lens, {s.B}, device, at::kInt);
-    const Place place(a[7], device);
+    const Place place(a[7], device, {&x, &g, &given, &h0, &hN, &lens});
     const at::Tensor out = out_like(given, x);
     const size_t need = calls.recurrence_workspace_bytes(s);
     const at::Tensor ws = workspace(x, need == kInvalid ? 0 : need);   // the call itself says what is wrong
@@ -219,7 +225,7 @@ PyObject *recurrence_step(PyObject *const *a) {
     like("g", g, x.sizes(), x.scalar_type(), device);
     like("y", given, x.sizes(), x.scalar_type(), device);
     array("h", h, x.sizes(), device);
-    const Place place(a[5], device);
+    const Place place(a[5], device, {&x, &g, &h, &given});
     const at::Tensor y = out_like(given, x);
     return result(calls.recurrence_step(view_of("x", x, true), view_of("g", g, true), view_of("y", y, true), s,
                                         (la_gate)PyLong_AsLong(a[3]), data(h), place.stream()),
@@ -246,7 +252,7 @@ PyObject *recurrence_backward(PyObject *const *a) {
     array("dhN", dhN, state, device);
     array("dh0", dh0, state, device);
     array("lens", lens, {s.B}, device, at::kInt);
-    const Place place(a[11], device);
+    const Place place(a[11], device, {&x, &g, &out, &dout, &h0, &dhN, &dh0, &lens, &given_x, &given_g});
     const at::Tensor dx = out_like(given_x, g), dg = out_like(given_g, g);
     const size_t need = calls.recurrence_workspace_bytes(s);
     const at::Tensor ws = workspace(g, need == kInvalid ? 0 : need);
@@ -279,7 +285,7 @@ PyObject *layernorm_forward(PyObject *const *a) {
     array("rstd", given_rstd, lead, device);
     const double eps = PyFloat_AsDouble(a[3]);
     if (PyErr_Occurred()) throw Error{nullptr, ""};
-    const Place place(a[10], device);
+    const Place place(a[10], device, {&x, &w, &b, &res, &given_y, &given_sum, &given_mean, &given_rstd});
     const at::Tensor y = out_like(given_y, x);
     at::Tensor sum, mean, rstd;
     if (res.defined()) sum = out_like(given_sum, x);
@@ -308,7 +314,7 @@ PyObject *layernorm_backward(PyObject *const *a) {
     array("rstd", rstd, lead, device);
     array("dw", given_w, {C}, device);
     array("db", given_b, {C}, device);
-    const Place place(a[9], device);
+    const Place place(a[9], device, {&dy, &s, &w, &mean, &rstd, &dsum, &given, &given_w, &given_b});
     const at::Tensor ds = out_like(given, dy), dw = out_float(given_w, dy, {C}), db = out_float(given_b, dy, {C});
     const size_t need = calls.layernorm_workspace_bytes(rows, small(C), dtype);
     const at::Tensor ws = workspace(dy, need == kInvalid ? 0 : need);
@@ -358,7 +364,13 @@ PyObject *grad(PyObject *const *a) {
     array("norm", given, {}, first.device());
     const double max_norm = clip ? PyFloat_AsDouble(a[1]) : 0.0;
     if (PyErr_Occurred()) throw Error{nullptr, ""};
-    const Place place(a[4], first.device());
+    const Place place(a[4], first.device(), {&given});
+    if (a[4] != Py_None)
+        for (Py_ssize_t i = 0; i < n; i++) place.use(required("grads", grads[i]));
+    if (a[4] != Py_None && clip && a[2] != Py_None) {
+        const List out(a[2]);
+        for (Py_ssize_t i = 0; i < n; i++) place.use(required("out", out[i]));
+    }
     const at::Tensor norm = out_float(given, first, {});
     const size_t need = calls.grad_workspace_bytes((int)n);
     const at::Tensor ws = workspace(first, need);
