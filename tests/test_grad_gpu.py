@@ -103,6 +103,25 @@ def test_unaligned_views(off):
         assert (dst[:off + 1] == 7.0).all() and (dst[8001:] == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("off", [0, 1, 3, 7])
+def test_long_tensors_at_odd_offsets(off, dtype):
+    """Many chunks of a tensor that starts between 16-byte boundaries, to a
+    destination that starts alike and to one that does not."""
+    n = 300007
+    buf = _grads([n + 16], [dtype], 10 + off)[0]
+    ts = [buf[off:off + n]]
+    ref, tol = layer.global_norm(ts), _tol(ts)
+    assert abs(la.la_grad_norm(ts).item() - ref) <= tol * ref
+    r = ts[0].double().cpu().numpy() * (0.5 / (ref + 1e-6))
+    for to in (off, off + 2):
+        dst = torch.full_like(buf, 7.0)
+        la.la_grad_clip(ts, 0.5, out=[dst[to:to + n]])
+        err = np.abs(dst[to:to + n].double().cpu().numpy() - r)
+        assert np.all(err <= np.abs(r) * (torch.finfo(dtype).eps / 2 + tol + 4 * U) + 1e-38)
+        assert (dst[:to] == 7.0).all() and (dst[to + n:] == 7.0).all()
+
+
 def test_past_32_bits():
     """One tensor of more than 2^31 values."""
     n = (1 << 31) + 4099
