@@ -30,7 +30,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSms = 152;
 constexpr int kCtas = 8 * kSms;      // at most, per launch, each with a partial sum
-constexpr int kFew = 32, kMany = 512;   // tensors of one launch
+constexpr int kFew = 32, kMany = 512;   // tensors of one launch (a long table costs: 4 Mi values 10.5 | 11.0 us)
 
 struct Item {
     const void *src;

@@ -12,9 +12,14 @@
 // tiles: each warp takes R consecutive rows, first forms (A, H) of them, then
 // learns the state before them (the warps' maps joined through shared memory)
 // and runs the recurrence proper from it.  Every value is read once and written
-// once.  Where the strips alone would leave SMs empty, a sequence is cut into
+// once (8 x 4096 tokens of 2048 channels, bf16, sigmoid gate: forward 63 us,
+// 6.3 TB/s, backward 117 us, 6.9 TB/s with what the L2 still holds of it; fp32 the
+// same rates).  Where the strips alone would leave SMs empty, a sequence is cut into
 // segments, one CTA each, after a first launch that forms each segment's (A, H)
-// alone; that reads x and g (g and dout) a second time.  (Clusters of CTAs that
+// alone; that reads x and g (g and dout) a second time (65536 tokens of 1024
+// channels: forward 106 us, 6.3 TB/s over both readings, of which the maps take
+// 42; backward 171 us).  (Sequences cut into 2, 4 or 8 calls, so that the second
+// reading meets the L2: 113, 125 and 173 us.  Clusters of CTAs that
 // walk one sequence side by side and exchange their maps through distributed
 // shared memory read everything once, but wait for one another at every tile:
 // 1.1 us for 512 rows, 142 us for N = 65536, D = 64.)  No atomics and no flags,
@@ -29,7 +34,6 @@
 
 namespace la {
 namespace {
-
 
 struct Dims {
     const int *lens;
@@ -450,7 +454,9 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_vi
 }
 
 // Up to kShortRows tokens (a decoded token among them) there is nothing to
-// split: a thread takes its channels' few rows in order.
+// split: a thread takes its channels' few rows in order, bound by latency.  (64
+// sequences of 1024 channels, bf16: 16 tokens 4.1 us, in tiles 5.5; 32 tokens 13.4
+// and 6.1.  One token of them 1.8 us, half a megabyte.)
 constexpr int kShortRows = 16, kShortThreads = 128;
 
 template <typename T, int GATE, int V>
@@ -618,8 +624,8 @@ template <int ROW, int ROWS, int S_, int C_> struct Tile {
 };
 // Many CTAs: two a SM hide each other's joins.  No more CTAs than SMs: twice the
 // rows a tile for the same number of joins (128 strips of 4096 tokens, bf16:
-// forward 63 us, backward 126 us, against 71 and 141 us with the small tiles; 256
-// strips of 2048: 69 and 109 us against 63 and 109 us).
+// forward 63 us, backward 117 us, against 68 and 137 us with the small tiles; 304
+// segments of 65536 tokens: 115 and 176 us against 106 and 171 us).
 template <int ROW> using Fwd = Tile<ROW, 8, 2, 2>;
 template <int ROW> using FwdFew = Tile<ROW, 16, 3, 1>;
 template <int ROW> using Bwd = Tile<ROW, 4, 2, 2>;
@@ -628,18 +634,23 @@ template <int ROW> using Pre = Tile<ROW, 8, 2, 3>;
 constexpr int kSms = 152;
 constexpr int kSegmentRows = 64;   // a multiple of the warps, and of the tiles' rows (their half for narrow rows)
 
-// Segments of a strip: none of it (1) where the strips fill half of the SMs, else
-// as many as give every SM two CTAs, of at least kSegmentRows tokens.
-int segments_of(long long strips, int N, long long *rows) {
-    long long n = strips * 2 <= kSms ? 2 * kSms / strips : 1;
+// Segments of a strip: none of it (1) where the strips fill half of the SMs (64
+// narrow ones of 2048 tokens, bf16: 18.0 | 24.7 us in segments, 31.7 | 58.5 without;
+// 128: 19.9 | 35.7 us without) or the sequence has at most `whole` tokens (8 strips,
+// forward | backward: 128 tokens 5.4 | 5.9 us in segments, 3.5 | 5.2 without; 256:
+// 5.6 | 6.1 and 5.3 | 8.7; 512: 6.0 | 6.6 and 9.0 | 15.7), else as many as give
+// every SM two CTAs, of at least kSegmentRows tokens (512 tokens: 6.0 | 6.6 us with
+// 64, 6.3 | 8.4 with 128).
+int segments_of(long long strips, int N, int whole, long long *rows) {
+    long long n = strips * 2 <= kSms && N > whole ? 2 * kSms / strips : 1;
     n = std::min(n, ((long long)N + kSegmentRows - 1) / kSegmentRows);
     *rows = (((long long)N + n - 1) / n + kSegmentRows - 1) / kSegmentRows * kSegmentRows;
     return (int)(((long long)N + *rows - 1) / *rows);
 }
 
-template <int V> Dims dims_of(const RecProblem &p) {
+template <int V> Dims dims_of(const RecProblem &p, int whole) {
     Dims s{p.lens, p.H, p.N, p.D, (p.D + 32 * V - 1) / (32 * V), 1, 0, (long long)p.B * p.H * p.D, nullptr, nullptr};
-    s.segments = segments_of((long long)p.B * p.H * s.strips, p.N, &s.rows);
+    s.segments = segments_of((long long)p.B * p.H * s.strips, p.N, whole, &s.rows);
     s.maps = static_cast<float2 *>(p.ws);
     s.start = reinterpret_cast<float *>(s.maps + (s.segments - 1) * s.channels);
     return s;
@@ -668,7 +679,7 @@ template <typename T, int GATE, int V> cudaError_t short_v(const RecProblem &p) 
     const long long groups = (long long)p.B * p.H * (p.D / V);
     const cudaError_t e =
         launch_pdl(rec_short_kernel<T, GATE, V>, dim3((unsigned)((groups + kShortThreads - 1) / kShortThreads)),
-                   dim3(kShortThreads), 0, p.stream, 0u, p.x, p.g, p.out, dims_of<V>(p), groups, p.h0, p.hN);
+                   dim3(kShortThreads), 0, p.stream, 0u, p.x, p.g, p.out, dims_of<V>(p, kShortRows), groups, p.h0, p.hN);
     count_launches(1);
     return e;
 }
@@ -678,10 +689,10 @@ bool few_ctas(const RecProblem &p, const Dims &s) {
 }
 
 struct Forward {
-    static constexpr int kUnsplit = kSms / 2 + 1;
+    static constexpr int kUnsplit = kSms / 2 + 1, kWhole = 256;
     template <typename T, int GATE, int V, bool WIDE> static cudaError_t run(const RecProblem &p) {
         if (p.N <= kShortRows) return short_v<T, GATE, WIDE ? V : 1>(p);
-        const Dims s = dims_of<V>(p);
+        const Dims s = dims_of<V>(p, kWhole);
         const cudaError_t e = segment_maps<T, GATE, V, WIDE, false>(p, s);
         if (e != cudaSuccess) return e;
         constexpr int ROW = 32 * V * (int)sizeof(T);
@@ -696,9 +707,9 @@ struct Forward {
 };
 
 struct Backward {
-    static constexpr int kUnsplit = kSms * 2 / 3 + 1;
+    static constexpr int kUnsplit = kSms * 2 / 3 + 1, kWhole = 128;
     template <typename T, int GATE, int V, bool WIDE> static cudaError_t run(const RecProblem &p) {
-        const Dims s = dims_of<V>(p);
+        const Dims s = dims_of<V>(p, kWhole);
         const cudaError_t e = segment_maps<T, GATE, V, WIDE, true>(p, s);
         if (e != cudaSuccess) return e;
         constexpr int ROW = 32 * V * (int)sizeof(T);
@@ -755,7 +766,7 @@ template <typename Call> cudaError_t choose_gate(const RecProblem &p) {
 // there is more than one segment.
 size_t recurrence_ws_bytes(const la_shape &s) {
     const long long channels = (long long)s.B * s.H * s.D;
-    if (s.N <= kSegmentRows || channels == 0) return 0;
+    if (s.N <= Backward::kWhole || channels == 0) return 0;   // the shorter of the two
     const long long strips = (long long)s.B * s.H * ((s.D + 127) / 128);   // the fewest that any lane width gives
     if (strips * 2 > kSms) return 0;
     const long long most = std::min(2LL * kSms / strips, ((long long)s.N + kSegmentRows - 1) / kSegmentRows);
