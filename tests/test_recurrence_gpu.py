@@ -127,7 +127,9 @@ def _both(x, g, dout, gate, h0=None, dhN=None, lens=None, want_states=True):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("gate", GATES)
 @pytest.mark.parametrize("B,H,N,D", [(1, 1, 1, 1), (2, 3, 1, 16), (1, 1, 2, 33), (2, 1, 7, 5), (3, 2, 64, 64),
-                                     (1, 2, 65, 128), (2, 1, 129, 200), (1, 1, 1000, 130), (5, 1, 300, 257)])
+                                     (1, 2, 65, 128), (2, 1, 129, 200), (1, 1, 1000, 130), (5, 1, 300, 257),
+                                     (2, 1, 16, 40), (2, 1, 17, 40), (1, 1, 128, 70), (1, 1, 256, 70), (1, 1, 257, 70),
+                                     (3, 1, 513, 333)])
 def test_parity(B, H, N, D, gate, dtype):
     x, g, dout, h0, dhN = _inputs(B, H, N, D, dtype, gate, B * 1000 + N + D)
     _both(x, g, dout, gate, h0, dhN)
@@ -172,10 +174,11 @@ def test_lengths(N, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [131, 700])
 @pytest.mark.parametrize("D,off", [(64, 0), (64, 1), (40, 3), (33, 0)])
-def test_views(D, off, dtype):
+def test_views(D, off, N, dtype):
     """Token-major projections, odd offsets, a repeated input, outputs as views."""
-    B, H, N = 2, 3, 131
+    B, H = 2, 3
     x, g, dout, h0, dhN = _inputs(B, H, N, D, dtype, "sigmoid", 77 + off)
     both = torch.zeros(B, N, H, 2 * D + 5, dtype=dtype, device=DEV)
     both[..., off:off + D] = x.transpose(1, 2)
