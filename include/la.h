@@ -338,9 +338,11 @@ typedef struct {
  *   LA_GATE_SIGMOID  a = 1/(1 + e^-g),  u = (1 - a) x
  * LA_GATE_LOG rounds an a next to 1 once, and LA_GATE_SIGMOID has both a and
  * 1 - a within 2^-21 (1 + |g|) of themselves, so that long memories keep their
- * length.  Products of gates over runs of tokens are formed in fp32 (held at its
- * largest value past it): with |a| > 1 throughout, a state that is not 0 can
- * reach infinity before its own value would.
+ * length.  Runs of tokens are joined by the products of their gates, in fp32.
+ * Where those overflow (|a| > 1 over many tokens, an infinite gate or state) the
+ * tokens are walked in order instead, so NaN, infinities and states that grow are
+ * what token by token gives, at a walk's speed.  A product below fp32's range is
+ * 0: a share of less than 2^-126 of a state that many tokens lie behind is lost.
  */
 typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOG = 1, LA_GATE_SIGMOID = 2 } la_gate;
 

@@ -13,8 +13,8 @@
 // learns the state before them (the warps' maps joined through shared memory)
 // and runs the recurrence proper from it.  Every value is read once and written
 // once (8 x 4096 tokens of 2048 channels, bf16, sigmoid gate: forward 63 us,
-// 6.3 TB/s, backward 117 us, 6.9 TB/s with what the L2 still holds of it; fp32 the
-// same rates).  Where the strips alone would leave SMs empty, a sequence is cut into
+// 6.3 TB/s, backward 117 to 125 us from box to box, 6.4 to 6.9 TB/s with what the L2
+// still holds of it; fp32 the same rates).  Where the strips alone would leave SMs empty, a sequence is cut into
 // segments, one CTA each, after a first launch that forms each segment's (A, H)
 // alone; that reads x and g (g and dout) a second time (65536 tokens of 1024
 // channels: forward 106 us, 6.3 TB/s over both readings, of which the maps take
@@ -25,6 +25,7 @@
 // 1.1 us for 512 rows, 142 us for N = 65536, D = 64.)  No atomics and no flags,
 // and the grouping depends on the sizes alone: equal calls give equal bits.
 #include <algorithm>
+#include <cfloat>
 #include <initializer_list>
 #include <type_traits>
 
@@ -97,10 +98,52 @@ template <typename T, int V, bool WIDE> struct Row {
     }
 };
 
-// A product of gates past fp32's range would turn an empty state into NaN
-// (inf * 0): it is held at the largest finite value instead.
-__device__ __forceinline__ float finite(float A) {
-    return fminf(fmaxf(A, -3.402823466e38f), 3.402823466e38f);
+// Joining by products fails where the walk in order does not: a product of gates
+// past fp32's range is inf, or NaN (inf * 0) after a gate of 0 or on an empty
+// state, and one below it is 0, which an infinite state turns into NaN.  None of
+// these ever becomes finite again along a chain of joins, so what is finite is
+// right.  What is not is walked again token by token, by one thread a channel: a
+// segment whose start it is the end of, or the rows of a CTA after its last tile
+// (there only values that are not finite are written, the others keep their bits).
+// A state that was NaN before stays NaN either way.  Walking costs up to 0.25 us a token
+// (8 x 4096 tokens of 2048 channels, every one with a NaN at its start: forward 0.6 to
+// 0.9 ms, backward 1.0 to 1.5); noticing it costs 1 % of a pass or less.
+__device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= FLT_MAX; }
+
+// `n` tokens of one channel in order: load(t) fetches a token's values, several
+// tokens ahead; step(t, values, h) returns the state after the token.
+template <typename Load, typename Step>
+__device__ __forceinline__ float in_order(long long n, float h, Load load, Step step) {
+    constexpr int R = 4;
+    for (long long t = 0; t < n; t += R) {
+        decltype(load(t)) v[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) v[r] = load(min(t + r, n - 1));
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            if (t + r < n) h = step(t + r, v[r], h);
+    }
+    return h;
+}
+// One token: v = x, or BACK: dout.
+template <int GATE, bool BACK> __device__ __forceinline__ float next_state(float h, float g, float v, float *w) {
+    Lanes<1> a, u;
+    gate_of<GATE, 1>(Lanes<1>{{g}}, a, u);
+    *w = u.p[0];
+    return BACK ? a.p[0] * (v + h) : fmaf(a.p[0], h, GATE == LA_GATE_SIGMOID ? u.p[0] * v : v);
+}
+// The state after n tokens from g and x (BACK: dout) on, gn and xn apart.
+template <typename T, int GATE, bool BACK>
+__device__ __noinline__ float state_after(const T *g, long long gn, const T *x, long long xn, long long n, float h) {
+    return in_order(
+        n, h, [=](long long t) { return make_float2(to_f32<T>(g[t * gn]), to_f32<T>(x[t * xn])); },
+        [=](long long, float2 v, float s) {
+            float w;
+            return next_state<GATE, BACK>(s, v.x, v.y, &w);
+        });
+}
+template <typename T> __device__ __forceinline__ void mend(T *p, float was, float v) {
+    if (!is_finite(was)) *p = from_f32<T>(v);
 }
 
 // The joining of a tile's maps (A, H), one per warp and channel.  For that the
@@ -114,6 +157,7 @@ template <int V, int W> struct Joint {
     static constexpr int G = W / V, C = 32 * V;
     static_assert(G * V == W, "");
     float A[2][W][C + 4], H[2][W][C + 4];   // the 4: owners of a warp read distinct banks
+    float start[C];                         // the channels' states before the CTA's rows
 };
 
 template <int V> using Vec = std::conditional_t<V == 4, float4, std::conditional_t<V == 2, float2, float>>;
@@ -124,52 +168,66 @@ template <int V> __device__ __forceinline__ Lanes<V> get_lanes(const float *from
     const Vec<V> r = *reinterpret_cast<const Vec<V> *>(from);
     return *reinterpret_cast<const Lanes<V> *>(&r);
 }
-template <int V> __device__ __forceinline__ Lanes<V> finite(const Lanes<V> &A) {
-    Lanes<V> r;
-#pragma unroll
-    for (int v = 0; v < V; v++) r.set(v, finite(A.get(v)));
-    return r;
-}
 
 template <typename Row, int V, int W> struct Join {
     using J = Joint<V, W>;
     J &j;
     int warp, lane, at, sub; // at: position of the owned channel, sub: which of its owners
     int channel;
+    bool real;               // whether the owned channel exists (else its maps are rubbish)
     float state;             // of the owned channel
+    float zero = 0.f;        // NaN once a joined state was not finite
     int set = 0;
 
     // first: the strip's first channel of the state before the CTA's rows.
     __device__ __forceinline__ Join(J &j_, const float *first, int left)
         : j(j_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31), at(threadIdx.x / J::G), sub(threadIdx.x % J::G),
-          channel(Row::channel_at(threadIdx.x / J::G)) {
-        state = first && channel < left ? first[channel] : 0.f;
+          channel(Row::channel_at(threadIdx.x / J::G)), real(channel < left) {
+        state = first && real ? first[channel] : 0.f;
     }
     // Over the segments before this one; maps: their strip's first channel,
-    // `pitch` apart.  The owners of a channel take equal runs of them.
-    __device__ __forceinline__ void skip(const float2 *maps, int segments, long long pitch, int left) {
-        if (segments == 0) return;
+    // `pitch` apart.  The owners of a channel take equal runs of them.  walk(c, i, h):
+    // state_after() channel c's tokens of segment i.
+    template <typename Walk>
+    __device__ __forceinline__ void skip(const float2 *maps, int segments, long long pitch, Walk walk) {
+        const float first = state;
         float a = 1.f, h = 0.f;
-        if (channel < left) {
+        if (real) {
             const int to = (sub + 1) * segments / J::G;
 #pragma unroll 16
             for (int i = sub * segments / J::G; i < to; i++) {
                 const float2 m = maps[i * pitch + channel];
                 h = fmaf(m.x, h, m.y);
-                a = finite(m.x * a);
+                a *= m.x;
             }
         }
 #pragma unroll
         for (int i = 0; i < J::G; i++)
             state = fmaf(__shfl_sync(~0u, a, i, J::G), state, __shfl_sync(~0u, h, i, J::G));
+        if (real && !is_finite(state)) {
+            state = first;
+            for (int i = 0; i < segments && state == state; i++) {
+                const float2 m = maps[i * pitch + channel];
+                const float after = fmaf(m.x, state, m.y);
+                state = is_finite(after) ? after : walk(channel, i, state);
+            }
+        }
+        if (sub == 0) j.start[at] = state;
     }
-    __device__ __forceinline__ void end(float *first, int left) {
-        if (first && channel < left && sub == 0) first[channel] = state;
+    // After the last tile, by all threads.  redo(c, h): walks channel c's rows of the CTA
+    // from the state h and mends them.  The state goes to `first`, if there is one.
+    template <typename Redo> __device__ __forceinline__ void end(float *first, Redo redo) {
+        const bool bad = real && !(zero == 0.f && is_finite(state));
+        const unsigned all = __ballot_sync(~0u, bad) >> (lane / J::G * J::G) & ((1u << J::G) - 1);
+        if (__syncthreads_or(bad)) {   // and the rows are written
+            if (all && sub == 0 && j.start[at] == j.start[at]) state = redo(channel, j.start[at]);
+        }
+        if (first && real && sub == 0) first[channel] = state;
     }
 
     // A, H: this thread's rows; returns the state before them.
     __device__ __forceinline__ Lanes<V> operator()(const Lanes<V> &A, const Lanes<V> &H) {
-        put_lanes(&j.A[set][warp][lane * V], finite(A));
+        put_lanes(&j.A[set][warp][lane * V], A);
         put_lanes(&j.H[set][warp][lane * V], H);
         __syncthreads();
         float a[V], h[V], ta = 1.f, th = 0.f;
@@ -177,13 +235,12 @@ template <typename Row, int V, int W> struct Join {
         for (int i = 0; i < V; i++) a[i] = j.A[set][sub * V + i][at], h[i] = j.H[set][sub * V + i][at];
 #pragma unroll
         for (int i = 0; i < V; i++) ta *= a[i], th = fmaf(a[i], th, h[i]);
-        ta = finite(ta);
         float ea = 1.f, eh = 0.f;   // map of the owners before this one
         if constexpr (J::G > 1) {
 #pragma unroll
             for (int o = 1; o < J::G; o *= 2) {
                 const float oa = __shfl_up_sync(~0u, ta, o, J::G), oh = __shfl_up_sync(~0u, th, o, J::G);
-                if (sub >= o) th = fmaf(ta, oh, th), ta = finite(ta * oa);
+                if (sub >= o) th = fmaf(ta, oh, th), ta *= oa;
             }
             ea = __shfl_up_sync(~0u, ta, 1, J::G);
             eh = __shfl_up_sync(~0u, th, 1, J::G);
@@ -198,6 +255,8 @@ template <typename Row, int V, int W> struct Join {
             j.H[set][sub * V + i][at] = before;
             before = fmaf(a[i], before, h[i]);
         }
+        // the state after this owner's warps, by other products than the channel's own state
+        zero = fmaf(before, 0.f, zero);
         __syncthreads();
         const Lanes<V> r = get_lanes<V>(&j.H[set][warp][lane * V]);
         set ^= 1;
@@ -205,15 +264,15 @@ template <typename Row, int V, int W> struct Join {
     }
 };
 
-// A CTA's place: its sequence, its channels, its rows [from, to) in the order
-// of the walk.
+// A CTA's place (`cta`: its number): its sequence, its channels, its rows
+// [from, to) in the order of the walk.
 template <int V> struct Place {
     long long b, h, at;      // at: its first channel in [B,H,D]
     int d0, left, len, segment;
     long long from, to;
-    __device__ __forceinline__ Place(const Dims &s, int segments) {
-        const unsigned strip = blockIdx.x / segments;
-        segment = blockIdx.x % segments;
+    __device__ __forceinline__ Place(const Dims &s, int segments, unsigned cta = blockIdx.x) {
+        const unsigned strip = cta / segments;
+        segment = cta % segments;
         const long long bh = strip / s.strips;
         b = bh / s.H;
         h = bh % s.H;
@@ -316,6 +375,21 @@ template <typename T, int V, bool WIDE, int W, int R, int S> struct Tiles {
     __align__(16) Joint<V, W> joint;
 };
 
+// A channel's `n` rows from x, g, out on, for Join::end().
+template <typename T, int GATE>
+__device__ __noinline__ float redo_forward(const T *x, long long xn, const T *g, long long gn, T *out, long long on,
+                                           long long n, float h) {
+    struct Row1 { float x, g, out; };
+    return in_order(
+        n, h, [=](long long t) { return Row1{to_f32<T>(x[t * xn]), to_f32<T>(g[t * gn]), to_f32<T>(out[t * on])}; },
+        [=](long long t, const Row1 &v, float s) {
+            float w;
+            s = next_state<GATE, false>(s, v.g, v.x, &w);
+            mend(out + t * on, v.out, s);
+            return s;
+        });
+}
+
 template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la_view g, la_view out, Dims s,
                                                                   const float *h0, float *hN) {
@@ -341,7 +415,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
         ring.commit();
     };
     for (int i = 0; i < S; i++) fetch(i, i);
-    join.skip(s.maps + q.at, q.segment, s.channels, q.left);
+    join.skip(s.maps + q.at, q.segment, s.channels, [&](int c, int i, float h) {
+        const long long t = min(i * s.rows, (long long)q.len), end = min(t + s.rows, (long long)q.len);
+        return state_after<T, GATE, false>(pg + t * g.sn + c, g.sn, px + t * x.sn + c, x.sn, end - t, h);
+    });
     int stage = 0;
     for (int it = 0; it < tiles; it++) {
         ring.template wait<S - 1>();
@@ -376,7 +453,10 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
         }
     }
     clear_rows<Row, T, V, W>(po, out.sn, q, s);
-    if (q.last()) join.end(hN ? hN + q.at : nullptr, q.left);
+    join.end(hN && q.last() ? hN + q.at : nullptr, [&](int c, float h) {
+        return redo_forward<T, GATE>(px + q.from * x.sn + c, x.sn, pg + q.from * g.sn + c, g.sn, po + q.from * out.sn + c,
+                                     out.sn, q.to - q.from, h);
+    });
 }
 
 // (A, H) of every segment but the last, and a copy of the state that the walk
@@ -436,7 +516,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_vi
         fetch(i + S, stage);
         stage = stage == S - 1 ? 0 : stage + 1;
     }
-    put_lanes(&sh.A[warp][lane * V], finite(A));
+    put_lanes(&sh.A[warp][lane * V], A);
     put_lanes(&sh.H[warp][lane * V], H);
     __syncthreads();
     for (int c = threadIdx.x; c < 32 * V; c += 32 * W) {
@@ -446,7 +526,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_vi
 #pragma unroll
         for (int w = 0; w < W; w++) {
             h = fmaf(sh.A[w][c], h, sh.H[w][c]);
-            a = finite(a * sh.A[w][c]);
+            a *= sh.A[w][c];
         }
         s.maps[q.segment * s.channels + q.at + d] = make_float2(a, h);
         if (q.segment == 0) s.start[q.at + d] = state ? state[q.at + d] : 0.f;
@@ -516,6 +596,32 @@ template <typename T, int V, bool WIDE, int W, int NL, int R, int S> struct Back
     __align__(16) Joint<V, W> joint;
 };
 
+// A channel's `n` rows from x, g, dout, dx, dg down, for Join::end(); out: the row
+// before the first of them; whole: the last of them is the sequence's first, which
+// has h0 before it.
+template <typename T, int GATE>
+__device__ __noinline__ float redo_backward(const T *x, long long xn, const T *g, long long gn, const T *out, long long on,
+                                            const T *dout, long long dn, T *dx, long long dxn, T *dg, long long dgn,
+                                            float h0, bool whole, long long n, float mu) {
+    constexpr bool kSigmoid = GATE == LA_GATE_SIGMOID;
+    struct Row1 { float x, g, before, dout, dx, dg; };
+    return in_order(
+        n, mu,
+        [=](long long i) {
+            const long long above = whole && i == n - 1 ? i - 1 : i;   // (its own row's out is not used)
+            return Row1{kSigmoid ? to_f32<T>(x[-i * xn]) : 0.f, to_f32<T>(g[-i * gn]), to_f32<T>(out[-above * on]),
+                        to_f32<T>(dout[-i * dn]), to_f32<T>(dx[-i * dxn]), to_f32<T>(dg[-i * dgn])};
+        },
+        [=](long long i, const Row1 &v, float s) {
+            float w;
+            const float l = v.dout + s, before = whole && i == n - 1 ? h0 : v.before;
+            s = next_state<GATE, true>(s, v.g, v.dout, &w);
+            mend(dx - i * dxn, v.dx, kSigmoid ? l * w : l);
+            mend(dg - i * dgn, v.dg, kSigmoid ? s * w * (before - v.x) : (GATE == LA_GATE_LOG ? s : l) * before);
+            return s;
+        });
+}
+
 template <typename T, int GATE, int V, bool WIDE, int W, int R, int S, int CTAS>
 __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, la_view g, la_view out, la_view dout,
                                                                    la_view dx, la_view dg, Dims s, const float *h0,
@@ -556,7 +662,11 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
         late.commit();
     };
     for (int i = 0; i < S; i++) fetch_early(i, i), fetch_late(i, i);
-    join.skip(s.maps + q.at, q.segment, s.channels, q.left);
+    join.skip(s.maps + q.at, q.segment, s.channels, [&](int c, int i, float mu) {
+        const long long t = min(i * s.rows, (long long)q.len), end = min(t + s.rows, (long long)q.len);
+        const long long row = q.len - 1 - t;
+        return state_after<T, GATE, true>(pg + row * g.sn + c, -g.sn, pd + row * dout.sn + c, -dout.sn, end - t, mu);
+    });
     int stage = 0;
     for (int it = 0; it < tiles; it++) {
         early.template wait<2 * S - 1>();   // commits in turn: early, late, early, ...
@@ -613,7 +723,20 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
     }
     clear_rows<Row, T, V, W>(pdx, dx.sn, q, s);
     clear_rows<Row, T, V, W>(pdg, dg.sn, q, s);
-    if (q.last()) join.end(dh0 ? dh0 + q.at : nullptr, q.left);
+    join.end(dh0 && q.last() ? dh0 + q.at : nullptr, [&](int c, float mu) {
+        // the place anew, from the CTA's number: held in registers through the walk it would
+        // cost 1.3 us of 25 (4 x 16 sequences of 2048 tokens, 64 channels)
+        unsigned cta;
+        asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(cta));
+        const Place<V> q(s, s.segments, cta);
+        const T *px = kSigmoid ? q.template strip<T>(x) : nullptr, *pg = q.template strip<T>(g);
+        const T *po = q.template strip<T>(out), *pd = q.template strip<T>(dout);
+        T *pdx = q.template strip<T>(dx), *pdg = q.template strip<T>(dg);
+        const long long t = q.len - 1 - q.from;
+        return redo_backward<T, GATE>(px + t * x.sn + c, x.sn, pg + t * g.sn + c, g.sn, po + (t - 1) * out.sn + c, out.sn,
+                                      pd + t * dout.sn + c, dout.sn, pdx + t * dx.sn + c, dx.sn, pdg + t * dg.sn + c,
+                                      dg.sn, h0 ? h0[q.at + c] : 0.f, q.to == q.len, q.to - q.from, mu);
+    });
 }
 
 // Tiles: W warps of R rows a CTA, S of them on their way, CTAS CTAs a SM.  ROW:
@@ -701,8 +824,8 @@ struct Forward {
     template <typename T, int GATE, int V, bool WIDE, typename C>
     static cudaError_t tiles(const RecProblem &p, const Dims &s) {
         return launch_tiles<C>(rec_forward_kernel<T, GATE, V, WIDE, C::W, C::R, C::S, C::CTAS>,
-                               sizeof(Tiles<T, V, WIDE, C::W, C::R, C::S>), p, s, s.segments, p.x, p.g, p.out, s, p.h0,
-                               p.hN);
+                               sizeof(Tiles<T, V, WIDE, C::W, C::R, C::S>), p, s, s.segments,
+                               p.x, p.g, p.out, s, p.h0, p.hN);
     }
 };
 
@@ -719,7 +842,8 @@ struct Backward {
     static cudaError_t tiles(const RecProblem &p, const Dims &s) {
         return launch_tiles<C>(rec_backward_kernel<T, GATE, V, WIDE, C::W, C::R, C::S, C::CTAS>,
                                sizeof(BackTiles<T, V, WIDE, C::W, GATE == LA_GATE_SIGMOID ? 2 : 1, C::R, C::S>), p, s,
-                               s.segments, p.x, p.g, p.out, p.dout, p.dx, p.dg, s, p.h0, p.dhN, p.dh0);
+                               s.segments, p.x, p.g, p.out, p.dout,
+                               p.dx, p.dg, s, p.h0, p.dhN, p.dh0);
     }
 };
 
