@@ -321,7 +321,7 @@ template <typename T, int V, int NT, int R, int S, bool WIDE> struct Ring {
     // Rows 0 .. n - 1 of tensor `k`: row r at p + r * sn (p: the row's first
     // channel of the strip), `left` channels of it exist.
     __device__ __forceinline__ void copy(int stage, int k, const T *p, long long sn, int n, int left) const {
-        const int piece = lane % kPieces, row = lane / kPieces, bytes = min(left * (int)sizeof(T), kRow);
+        const int piece = lane % kPieces, row = lane / kPieces, bytes = min(left, 32 * V) * (int)sizeof(T);
         const long long step = sn * (long long)sizeof(T);
         const unsigned char *from = reinterpret_cast<const unsigned char *>(p) + row * step;
         unsigned char *to = slot[stage][k][row] + piece * 16;
@@ -771,8 +771,11 @@ int segments_of(long long strips, int N, int whole, long long *rows) {
     return (int)(((long long)N + *rows - 1) / *rows);
 }
 
+// Groups of C channels in a row.
+int strips_of(int D, int C) { return (int)(((long long)D + C - 1) / C); }
+
 template <int V> Dims dims_of(const RecProblem &p, int whole) {
-    Dims s{p.lens, p.H, p.N, p.D, (p.D + 32 * V - 1) / (32 * V), 1, 0, (long long)p.B * p.H * p.D, nullptr, nullptr};
+    Dims s{p.lens, p.H, p.N, p.D, strips_of(p.D, 32 * V), 1, 0, (long long)p.B * p.H * p.D, nullptr, nullptr};
     s.segments = segments_of((long long)p.B * p.H * s.strips, p.N, whole, &s.rows);
     s.maps = static_cast<float2 *>(p.ws);
     s.start = reinterpret_cast<float *>(s.maps + (s.segments - 1) * s.channels);
@@ -862,8 +865,8 @@ int row_alignment(const RecProblem &p, int size) {
 // and 62 us), from two thirds in the backward (the same: 80 and 68 us; 92 and 119 us).
 template <typename Call, typename T, int GATE> cudaError_t choose(const RecProblem &p) {
     constexpr int V = 8 / (int)sizeof(T), C = 32 * V;
-    const long long heads = (long long)p.B * p.H, strips = heads * ((p.D + C - 1) / C);
-    const long long narrow = heads * ((p.D + C / 2 - 1) / (C / 2));
+    const long long heads = (long long)p.B * p.H, strips = heads * strips_of(p.D, C);
+    const long long narrow = heads * strips_of(p.D, C / 2);
     const bool half = (p.D % C != 0 && p.D % C <= C / 2 && p.D < 8 * C) ||
                       (strips * 2 <= kSms && narrow >= Call::kUnsplit);
     if (row_alignment(p, sizeof(T)) == 16)
@@ -891,7 +894,7 @@ template <typename Call> cudaError_t choose_gate(const RecProblem &p) {
 size_t recurrence_ws_bytes(const la_shape &s) {
     const long long channels = (long long)s.B * s.H * s.D;
     if (s.N <= Backward::kWhole || channels == 0) return 0;   // the shorter of the two
-    const long long strips = (long long)s.B * s.H * ((s.D + 127) / 128);   // the fewest that any lane width gives
+    const long long strips = (long long)s.B * s.H * strips_of(s.D, 128);   // the fewest that any lane width gives
     if (strips * 2 > kSms) return 0;
     const long long most = std::min(2LL * kSms / strips, ((long long)s.N + kSegmentRows - 1) / kSegmentRows);
     return (size_t)most * channels * sizeof(float2);
