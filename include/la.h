@@ -434,7 +434,9 @@ la_status la_layernorm_backward(la_rows dy, la_rows s, la_rows dsum, la_rows ds,
 
 /*
  * One tensor of a list: n contiguous values at src, and dst for the calls
- * that write (dst may be src).  src and dst need their element's alignment.
+ * that write.  src and dst need their element's alignment.  dst may be its own
+ * src; otherwise no dst of a list may overlap another dst or any src (equal
+ * starts are LA_ERR_INVALID_ARG): a tensor that a model uses twice is listed once.
  */
 typedef struct {
     const void *src;

@@ -543,7 +543,8 @@ def la_grad_norm(grads, norm=None, stream=None):
 def la_grad_clip(grads, max_norm, out=None, norm=None, stream=None):
     """Scales every tensor of a list by min(1, max_norm / (norm + 1e-6)) with
     the global norm, in place or into the tensors of out; returns the norm (an
-    fp32 scalar on the device)."""
+    fp32 scalar on the device).  No tensor may be listed twice, nor be the out of
+    another (LAError)."""
     st, norm = _bound().grad(grads, float(max_norm), out, norm, _handle(stream))
     _check(st, "la_grad_clip")
     return norm
