@@ -51,3 +51,39 @@ def test_clip_refuses_tensors_that_coincide(lib, count, a, b):
 
     for change in (same_tensor, same_dst, crossed, swapped):
         assert call(change) == INVALID, change.__name__
+
+
+def _r(i, stride=16):
+    return la.la_rows(0x100000 * (i + 1) if i is not None else None, stride)
+
+
+def test_layernorm_forward_refuses_outputs_that_coincide(lib):
+    f = lib.la_layernorm_forward
+    x, res, sum_, y, w, b, mean, rstd = range(8)
+
+    def call(**same):              # name=i: the pointer of argument i
+        at = {n: same.get(n, i) for n, i in zip(("x", "res", "sum", "y", "w", "b", "mean", "rstd"), range(8))}
+        return f(_r(at["x"]), _r(at["res"]), _r(at["sum"]), _r(at["y"]), _p(at["w"]), _p(at["b"]), _p(at["mean"]),
+                 _p(at["rstd"]), 4, 16, F32, 1e-5, None)
+    for name in ("sum", "mean", "rstd"):
+        for other in {"w": w, "b": b, "y": y, "sum": sum_, "mean": mean, "rstd": rstd}.items():
+            if other[0] != name:
+                assert call(**{name: other[1]}) == INVALID, (name, other[0])
+    for name in ("mean", "rstd", "y"):
+        assert call(**{name: x}) == INVALID
+        assert call(**{name: res}) == INVALID
+
+
+def test_layernorm_backward_refuses_outputs_that_coincide(lib):
+    f = lib.la_layernorm_backward
+    need = lib.la_layernorm_workspace_bytes(4, 16, F32)
+    names = ("dy", "s", "dsum", "ds", "w", "mean", "rstd", "dw", "db")
+
+    def call(**same):
+        at = {n: same.get(n, i) for i, n in enumerate(names)}
+        return f(_r(at["dy"]), _r(at["s"]), _r(at["dsum"]), _r(at["ds"]), _p(at["w"]), _p(at["mean"]), _p(at["rstd"]),
+                 _p(at["dw"]), _p(at["db"]), 4, 16, F32, _p(20), need, None)
+    for name in ("ds", "dw", "db"):
+        for i, other in enumerate(names):
+            if other != name:
+                assert call(**{name: i}) == INVALID, (name, other)

@@ -196,6 +196,10 @@ la_status la_layernorm_forward(la_rows x, la_rows res, la_rows sum, la_rows y, c
     if ((same(sum.data, x.data) && sum.stride != x.stride) || (same(sum.data, res.data) && sum.stride != res.stride))
         return LA_ERR_INVALID_ARG;
     if (same(mean, rstd)) return LA_ERR_INVALID_ARG;
+    for (const void *i : {(const void *)w, (const void *)b, (const void *)mean, (const void *)rstd})
+        if (same(sum.data, i)) return LA_ERR_INVALID_ARG;
+    for (const void *i : {(const void *)x.data, (const void *)res.data, (const void *)w, (const void *)b})
+        if (same(mean, i) || same(rstd, i)) return LA_ERR_INVALID_ARG;
     NormProblem p{};
     p.x = x, p.res = res, p.sum = sum, p.y = y, p.w = w, p.b = b, p.mean = mean, p.rstd = rstd;
     p.rows = rows, p.C = C, p.dtype = dtype, p.eps = eps, p.stream = (cudaStream_t)stream;
@@ -227,6 +231,9 @@ la_status la_layernorm_backward(la_rows dy, la_rows s, la_rows dsum, la_rows ds,
     for (const void *i : {(const void *)dy.data, (const void *)s.data, (const void *)dsum.data, (const void *)w,
                           (const void *)mean, (const void *)rstd, (const void *)dw, (const void *)db})
         if (same(ds.data, i)) return LA_ERR_INVALID_ARG;
+    for (const void *i : {(const void *)dy.data, (const void *)s.data, (const void *)dsum.data, (const void *)mean,
+                          (const void *)rstd})
+        if (same(dw, i) || same(db, i)) return LA_ERR_INVALID_ARG;
     const size_t need = layernorm_ws_bytes(rows, C);
     if ((dw || db) && (ws_bytes < need || !aligned(workspace, 16))) return LA_ERR_INVALID_ARG;
     NormProblem p{};
