@@ -7,7 +7,9 @@ statically, so the library depends on nothing but the driver.  The checked
 variant (``--checked``) compiles the same sources with ``-DLA_CHECKED`` into
 ``_build_checked/`` and ``lib/liblinattn_checked.so``.  ``csrc/la_torch.cpp``,
 the Python binding of part of the calls, compiles with g++ against the installed
-PyTorch's headers into ``lib/_la_torch.so`` (it finds the library at run time).
+PyTorch's headers into ``lib/_la_torch.so`` (it finds the library at run time);
+without PyTorch the library is built alone, and another PyTorch than the binding
+was made for makes it anew.
 
     python -m weight_recurrence_gb300.build [--force] [--verbose] [--checked]
 """
@@ -65,14 +67,42 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir():
+    """Folder of the installed PyTorch (located, not imported), or None."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def torch_identity():
+    """What the binding depends on besides its source: PyTorch's place and version and
+    the interpreter's; None without PyTorch."""
+    torch = _torch_dir()
+    if torch is None:
+        return None
+    try:
+        with open(os.path.join(torch, "version.py")) as f:
+            version = f.read()
+    except OSError:
+        version = ""
+    return "\n".join((sys.version, torch, version))
+
+
 def binding_command(out: str):
-    """g++ command line that makes the binding (torch is located, not imported)."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """g++ command line that makes the binding."""
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", *("-I" + i for i in inc), BINDING_SRC, "-o", out,
             "-L" + os.path.join(torch, "lib"), "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ltorch_python", "-ldl"]
+
+
+def _read(path: str):
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return None
 
 
 def build_variants(variants=("release",), force: bool = False, verbose: bool = False, extra_flags=()):
@@ -83,7 +113,10 @@ def build_variants(variants=("release",), force: bool = False, verbose: bool = F
     hdrs = headers()
     plan, procs = [], []
     bound = None
-    if force or _stale(BINDING, [BINDING_SRC, os.path.join(os.path.dirname(PKG), "include", "la.h")]):
+    made_for = os.path.join(PKG, VARIANTS["release"][0], "la_torch.made_for")
+    identity = torch_identity()
+    if identity is not None and (force or _read(made_for) != identity or
+                                 _stale(BINDING, [BINDING_SRC, os.path.join(os.path.dirname(PKG), "include", "la.h")])):
         bound = BINDING + ".tmp%d" % os.getpid()
         procs.append((BINDING_SRC, subprocess.Popen(binding_command(bound), stdout=subprocess.PIPE,
                                                     stderr=subprocess.STDOUT)))
@@ -109,10 +142,13 @@ def build_variants(variants=("release",), force: bool = False, verbose: bool = F
             sys.stderr.write(out.decode(errors="replace"))
         if p.returncode != 0:
             failed.append(src)
-    if failed:
-        raise RuntimeError("compilation failed for: " + ", ".join(failed))
-    if bound:
+    if bound and BINDING_SRC not in failed:
         os.replace(bound, BINDING)
+        os.makedirs(os.path.dirname(made_for), exist_ok=True)
+        with open(made_for, "w") as f:
+            f.write(identity)
+    if set(failed) - {BINDING_SRC}:
+        raise RuntimeError("compilation failed for: " + ", ".join(failed))
     for lib, objs, started in plan:
         if force or started or _stale(lib, objs):
             tmp = lib + ".tmp%d" % os.getpid()
@@ -121,6 +157,8 @@ def build_variants(variants=("release",), force: bool = False, verbose: bool = F
                 print(" ".join(cmd), flush=True)
             subprocess.check_call(cmd)
             os.replace(tmp, lib)
+    if failed:   # the libraries are there, the binding is not
+        raise RuntimeError("compilation failed for: " + ", ".join(failed))
     return [lib for lib, _, _ in plan]
 
 
