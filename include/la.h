@@ -336,13 +336,14 @@ typedef struct {
  *   LA_GATE_DECAY    a = g,             u = x
  *   LA_GATE_LOG      a = e^g,           u = x
  *   LA_GATE_SIGMOID  a = 1/(1 + e^-g),  u = (1 - a) x
- * LA_GATE_LOG rounds an a next to 1 once, and LA_GATE_SIGMOID has both a and
- * 1 - a within 2^-21 (1 + |g|) of themselves, so that long memories keep their
- * length.  Runs of tokens are joined by the products of their gates, in fp32.
- * Where those overflow (|a| > 1 over many tokens, an infinite gate or state) the
- * tokens are walked in order instead, so NaN, infinities and states that grow are
- * what token by token gives, at a walk's speed.  A product below fp32's range is
- * 0: a share of less than 2^-126 of a state that many tokens lie behind is lost.
+ * With fp32 data a and 1 - a are within 2^-20 of themselves (below 2^-126 they
+ * count as 0), with bf16 data within 2^-21 (1 + |g|); an a next to 1 is rounded
+ * once, so that long memories keep their length.
+ * Runs of tokens are joined by the products of their gates, in fp32.  Where those
+ * overflow (|a| > 1 over many tokens, an infinite gate or state) the tokens are
+ * walked in order instead, so NaN, infinities and states that grow are what token
+ * by token gives, at a walk's speed.  A product below fp32's range is 0: a share of
+ * less than 2^-126 of an earlier state is lost.
  */
 typedef enum { LA_GATE_DECAY = 0, LA_GATE_LOG = 1, LA_GATE_SIGMOID = 2 } la_gate;
 

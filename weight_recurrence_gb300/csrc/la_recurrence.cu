@@ -126,9 +126,9 @@ __device__ __forceinline__ float in_order(long long n, float h, Load load, Step 
     return h;
 }
 // One token: v = x, or BACK: dout.
-template <int GATE, bool BACK> __device__ __forceinline__ float next_state(float h, float g, float v, float *w) {
+template <typename T, int GATE, bool BACK> __device__ __forceinline__ float next_state(float h, float g, float v, float *w) {
     Lanes<1> a, u;
-    gate_of<GATE, 1>(Lanes<1>{{g}}, a, u);
+    gate_of<T, GATE, 1>(Lanes<1>{{g}}, a, u);
     *w = u.p[0];
     return BACK ? a.p[0] * (v + h) : fmaf(a.p[0], h, GATE == LA_GATE_SIGMOID ? u.p[0] * v : v);
 }
@@ -139,7 +139,7 @@ __device__ __noinline__ float state_after(const T *g, long long gn, const T *x, 
         n, h, [=](long long t) { return make_float2(to_f32<T>(g[t * gn]), to_f32<T>(x[t * xn])); },
         [=](long long, float2 v, float s) {
             float w;
-            return next_state<GATE, BACK>(s, v.x, v.y, &w);
+            return next_state<T, GATE, BACK>(s, v.x, v.y, &w);
         });
 }
 template <typename T> __device__ __forceinline__ void mend(T *p, float was, float v) {
@@ -384,7 +384,7 @@ __device__ __noinline__ float redo_forward(const T *x, long long xn, const T *g,
         n, h, [=](long long t) { return Row1{to_f32<T>(x[t * xn]), to_f32<T>(g[t * gn]), to_f32<T>(out[t * on])}; },
         [=](long long t, const Row1 &v, float s) {
             float w;
-            s = next_state<GATE, false>(s, v.g, v.x, &w);
+            s = next_state<T, GATE, false>(s, v.g, v.x, &w);
             mend(out + t * on, v.out, s);
             return s;
         });
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_forward_kernel(la_view x, la
 #pragma unroll
         for (int r = 0; r < R; r++) {
             Lanes<V> w;
-            gate_of<GATE, V>(ring.get(stage, 1, r, rg, g.sn), a[r], w);
+            gate_of<T, GATE, V>(ring.get(stage, 1, r, rg, g.sn), a[r], w);
             u[r] = ring.get(stage, 0, r, rx, x.sn);
             if (GATE == LA_GATE_SIGMOID) u[r] = mul(w, u[r]);
         }
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_maps_kernel(la_view g, la_vi
         const int n = (int)min((long long)R, last - (first + (long long)i * R));
         auto step = [&](int r) {
             Lanes<V> a, w;
-            gate_of<GATE, V>(ring.get(stage, 1, r, pg + (long long)i * R * ng, ng), a, w);
+            gate_of<T, GATE, V>(ring.get(stage, 1, r, pg + (long long)i * R * ng, ng), a, w);
             const Lanes<V> v = ring.get(stage, 0, r, px + (long long)i * R * nx, nx);
             A = mul(A, a);
             if (BACK) H = mul(a, add(v, H));
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kShortThreads) rec_short_kernel(la_view x, la_
         for (int r = 0; r < R; r++) {
             if (t0 + r >= len) break;
             Lanes<V> a, w;
-            gate_of<GATE, V>(Raw<T, V>::get(rg[r]), a, w);
+            gate_of<T, GATE, V>(Raw<T, V>::get(rg[r]), a, w);
             c = fma(a, c, mul(w, Raw<T, V>::get(rx[r])));
             *reinterpret_cast<RT *>(po + (t0 + r) * out.sn) = Raw<T, V>::put(c);
         }
@@ -586,7 +586,12 @@ __global__ void __launch_bounds__(kShortThreads) rec_short_kernel(la_view x, la_
 // The same walk from the last token to the first: the state is mu_t = a_t l_t,
 // which the token before adds to its own gradient.  The rows of g and dout are
 // free once they have become a, w and d, those of h_{t-1} and x only after the
-// join, so they go through two rings.
+// join, so they go through two rings.  h_{t-1} is the forward's output as it was
+// stored: for bf16 data within 2^-8 of its size where the forward itself carries fp32.
+// Only dg has it as a factor, and is itself rounded to bf16 (8 x 4096 x 2048, sigmoid: dg
+// 1.8e-3 off the exact one in the mean square, 1.7e-3 with fp32 states; dx, dh0 and the
+// carried l do not depend on it).  The fp32 states would have to be kept by the caller,
+// twice the bytes of out, or formed again from all of x and g, a second walk.
 template <typename T, int V, bool WIDE, int W, int NL, int R, int S> struct BackTiles {
     using Row = la::Row<T, V, WIDE>;
     using Early = Ring<T, V, 2, R, S, WIDE>;
@@ -615,7 +620,7 @@ __device__ __noinline__ float redo_backward(const T *x, long long xn, const T *g
         [=](long long i, const Row1 &v, float s) {
             float w;
             const float l = v.dout + s, before = whole && i == n - 1 ? h0 : v.before;
-            s = next_state<GATE, true>(s, v.g, v.dout, &w);
+            s = next_state<T, GATE, true>(s, v.g, v.dout, &w);
             mend(dx - i * dxn, v.dx, kSigmoid ? l * w : l);
             mend(dg - i * dgn, v.dg, kSigmoid ? s * w * (before - v.x) : (GATE == LA_GATE_LOG ? s : l) * before);
             return s;
@@ -678,7 +683,7 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
 #pragma unroll
         for (int r = 0; r < R; r++) {
             d[r] = early.get(stage, 1, r, rd, -dout.sn);
-            gate_of<GATE, V>(early.get(stage, 0, r, rg, -g.sn), a[r], w[r]);
+            gate_of<T, GATE, V>(early.get(stage, 0, r, rg, -g.sn), a[r], w[r]);
         }
         __syncwarp();
         fetch_early(it + S, stage);
