@@ -455,7 +455,8 @@ size_t la_grad_workspace_bytes(int count);
 /*
  * Global norm over all tensors (a host array, read before the call returns):
  *   *norm = sqrt(sum of the squares of every value of every tensor)
- * (squares and sums in fp32 and in a fixed order, the last level in 64 bits).
+ * (squares and sums in fp32, over positive terms, in a fixed order: equal calls
+ * give equal bits).
  *   norm: device pointer to one fp32 value.  No values at all give 0.
  */
 la_status la_grad_norm(const la_tensor *tensors, int count, float *norm, void *workspace, size_t ws_bytes,
@@ -465,7 +466,8 @@ la_status la_grad_norm(const la_tensor *tensors, int count, float *norm, void *w
  * Clipping by the global norm: norm as above, then for every tensor
  *   dst = min(1, max_norm / (norm + 1e-6)) src
  * on the device, without a host round trip.  A norm that is NaN makes every
- * value NaN; an infinite one makes finite values 0 (and infinite ones NaN).
+ * value NaN; an infinite one makes finite values 0 and infinite ones NaN (every
+ * value NaN if max_norm is infinite too).
  *   max_norm: >= 0.
  */
 la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
