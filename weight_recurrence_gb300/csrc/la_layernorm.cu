@@ -14,9 +14,13 @@
 //
 // Measured: 32768 rows of 2048, bf16, with the residual: forward 86 us (6.2 TB/s),
 // backward 91 us (5.9 TB/s); 262144 rows of 64: 13.3 and 24.2 us; 16 rows of 2048:
-// 2.0 us (latency).  Rows of 8192 keep 6.4 TB/s forward and 4.8 backward, whose
-// sums then leave room for 8 warps an SM; at 16384 they live in shared memory and
-// the rows are loaded when they are due (2.2 TB/s).
+// 2.0 us (latency).  Wide rows keep 5.5 to 6.4 TB/s forward.  Backward, 64 Mi bf16
+// values: rows of 8192 4.8 TB/s (83 us), their sums leave room for 8 warps an SM; rows
+// of 16384 2.2 TB/s (185 us), their sums live in shared memory with one row on its
+// way.  32 Mi fp32 values: rows of 4096 5.8 TB/s (69 us), of 8192, with the sums in shared
+// memory, 4.5 (89 us), of 16384, whose rows are loaded when they are due, 3.3 (123 us).
+// Wide rows off 16 bytes are taken by single values: 8191 bf16 values 3.4 TB/s forward,
+// 1.4 backward.
 #include <algorithm>
 
 #include "la_layer.h"

@@ -41,7 +41,7 @@ struct Dims {
     int H, N, D;
     int strips;        // groups of 32 lanes' channels in a sequence
     int segments;      // CTAs of a strip
-    long long rows;    // tokens of a segment (a multiple of a tile's)
+    long long rows;    // tokens of a segment (a multiple of kSegmentRows)
     long long channels;   // B*H*D
     float2 *maps;      // [segments - 1][B*H*D] (A, H) of the segments but the last
     float *start;      // [B*H*D] the state before the first
@@ -745,8 +745,8 @@ __global__ void __launch_bounds__(32 * W, CTAS) rec_backward_kernel(la_view x, l
 }
 
 // Tiles: W warps of R rows a CTA, S of them on their way, CTAS CTAs a SM.  ROW:
-// bytes of a strip's row; rows of 256 bytes come by ROWS a warp, narrower ones by
-// as many more (at most ROWS * 2 where they are 64).
+// bytes of a strip's row, 256 or 128; rows of 256 bytes come by ROWS a warp, those of
+// 128 by twice as many.
 template <int ROW, int ROWS, int S_, int C_> struct Tile {
     static constexpr int W = 8, R = ROW == 256 ? ROWS : ROWS * 2, S = S_, CTAS = C_;
 };
@@ -760,7 +760,10 @@ template <int ROW> using Bwd = Tile<ROW, 4, 2, 2>;
 template <int ROW> using BwdFew = Tile<ROW, 8, 3, 1>;
 template <int ROW> using Pre = Tile<ROW, 8, 2, 3>;
 constexpr int kSms = 152;
-constexpr int kSegmentRows = 64;   // a multiple of the warps, and of the tiles' rows (their half for narrow rows)
+// A multiple of the warps, which share a segment's rows evenly in the maps' launch.  A
+// tile has 32 to 256 rows: in segments as short as this one the larger tiles leave
+// half to three quarters of their warps without rows.
+constexpr int kSegmentRows = 64;
 
 // Segments of a strip: none of it (1) where the strips fill half of the SMs (64
 // narrow ones of 2048 tokens, bf16: 18.0 | 24.7 us in segments, 31.7 | 58.5 without;
