@@ -307,8 +307,9 @@ la_status la_decode_step_variant(const void *q, const void *k, const void *v, co
                                  float *S, float *z, la_shape s, la_variant var, la_stream_t stream);
 
 /* ------------------------------------------- the layer around the attention
- * A gated linear recurrence, layer norm and the clipping of gradients: what a
- * recurrent layer's training and serving step runs next to the calls above.
+ * A gated linear recurrence, layer norm, the clipping of gradients, linear
+ * attention with decays, and the norm and rotation of its queries and keys: what
+ * a recurrent layer's training and serving step runs next to the calls above.
  * They share the conventions at the top except these: sizes are free (no set
  * of head widths), and tensors are views with strides, whose pointers need
  * their element's alignment only (16-byte aligned rows run wider loads).
@@ -472,6 +473,126 @@ la_status la_grad_norm(const la_tensor *tensors, int count, float *norm, void *w
  */
 la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
                        size_t ws_bytes, la_stream_t stream);
+
+/*
+ * Linear attention with a decay for each head.  With a = e^g, g = log_decay of
+ * the head, and rows as everywhere (x.y the product of two rows):
+ *   S_i = a S_{i-1} + k_i v_i^T,   out_i = scale q_i^T S_i
+ *       = scale (sum over j <= i of a^(i-j) (q_i.k_j) v_j + a^(i+1) q_i^T S_0)
+ * q and k enter as they are (no feature map, no denominator).
+ *   q, k: [B,H,N,D]; v, out: [B,H,N,M], views of dtype s.dtype; any
+ *      1 <= D, M <= 128 (larger: LA_ERR_UNSUPPORTED).
+ *   log_decay: H fp32 values on the device; 0 forgets nothing, -infinity
+ *      keeps the token itself alone; above 0 the state grows.
+ *   S0, SN: [B,H,D,M] contiguous fp32, the state before the first token
+ *      (NULL: 0) and the one after the last (NULL: not wanted); SN may be S0.
+ *   out.data NULL: the state alone (q is not read and its data may be NULL;
+ *      SN has to be given).
+ *   lens: as la_recurrence_forward: rows of sequence b at or past lens[b] add
+ *      nothing, whatever they hold, their rows of out are 0, and SN is the
+ *      state after lens[b] tokens.
+ *   workspace: la_decay_workspace_bytes(s, 0) bytes.
+ * A token's NaN and infinities make what sees them not finite, as token by
+ * token does; rows that do not see it are what they are without it.
+ * All arithmetic is fp32; out is rounded once.
+ */
+la_status la_decay_forward(la_view q, la_view k, la_view v, la_view out, const float *log_decay, const int *lens,
+                           la_shape s, float scale, const float *S0, float *SN, void *workspace, size_t ws_bytes,
+                           la_stream_t stream);
+
+/*
+ * Bytes of device workspace la_decay_forward (backward = 0) or
+ * la_decay_backward (1) needs: the states at the segments' starts where few
+ * heads are cut into segments (0: none, NULL is accepted).  (size_t)-1 for an
+ * invalid shape.
+ */
+size_t la_decay_workspace_bytes(la_shape s, int backward);
+
+/*
+ * One token of every sequence: q, k [B,H,D], v, y [B,H,M] (views without the
+ * token dimension: sn and s.N are ignored), S [B,H,D,M] fp32 updated in place.
+ * The same as la_decay_forward over one token with S0 = SN = S, in fp32
+ * arithmetic for both dtypes.
+ */
+la_status la_decay_step(la_view q, la_view k, la_view v, la_view y, const float *log_decay, la_shape s, float scale,
+                        float *S, la_stream_t stream);
+
+/*
+ * Backward of la_decay_forward.  Given dout = dL/dout and dSN = dL/dSN, with
+ * G_N-1 = scale q_N-1 dout_N-1^T + dSN and G_i = scale q_i dout_i^T + a G_{i+1}:
+ *   dq_i = scale S_i dout_i,  dk_i = G_i v_i,  dv_i = G_i^T k_i,  dS0 = a G_0
+ * (the decays are constants of the model and get no gradient).
+ *   dq, dk: [B,H,N,D], dv: [B,H,N,M] of dtype s.dtype; rows past a length are 0.
+ *   S0: as given to the forward; dSN, dS0: [B,H,D,M] contiguous fp32 (NULL:
+ *      0; not wanted), two buffers.  Chaining segments of a sequence through
+ *      dS0 -> dSN gives the backward of the whole.
+ *   workspace: la_decay_workspace_bytes(s, 1) bytes.
+ * Arithmetic and everything else as la_decay_forward.
+ */
+la_status la_decay_backward(la_view q, la_view k, la_view v, la_view dout, la_view dq, la_view dk, la_view dv,
+                            const float *log_decay, const int *lens, la_shape s, float scale, const float *S0,
+                            const float *dSN, float *dS0, void *workspace, size_t ws_bytes, la_stream_t stream);
+
+/* Which channels of a head turn together: i and i + P, or 2i and 2i + 1 (i < P). */
+typedef enum { LA_PAIRS_HALF = 0, LA_PAIRS_ADJACENT = 1 } la_pairs;
+
+/*
+ * Rotation of P pairs of channels: pair i of token (b, n) turns by the angle
+ * position * freq[i], the position taken on the pair's axis.
+ *   pos: device int32, the position on axis a at pos[a*sa + b*sb + n*sn]
+ *      (strides in elements, 0 repeats); any int32 value.
+ *   freq: device, P fp32 values, radians a position.  The angle is taken mod
+ *      a turn in 64-bit fixed point before any rounding to fp32, so that far
+ *      positions keep their fraction.  A freq that is not finite gives NaN.
+ *   axes: host array of P axis numbers below A, read before the call returns
+ *      (NULL: all on axis 0).
+ *   A: axes of pos, 1 to 8; P: 0 to D/2.
+ */
+typedef struct {
+    const int *pos;
+    long long sa, sb, sn;
+    const float *freq;
+    const unsigned char *axes;
+    int A, P;
+    la_pairs pairs;
+} la_rotation;
+
+typedef struct {
+    int B, N, Hq, Hk, D;
+    la_dtype dtype;
+} la_qk_shape;
+
+/*
+ * Norm of every head of the queries and keys, and their rotation, in one pass:
+ *   n = x rstd w,  rstd = 1/sqrt(mean(x^2) + eps) over the head's D channels
+ *   (y_i, y_j) = (n_i cos - n_j sin, n_j cos + n_i sin) for the pairs (i, j);
+ *   the channels behind the 2P rotated ones: y = n.
+ *   q, qo: [B,Hq,N,D]; k, ko: [B,Hk,N,D], views of dtype s.dtype; Hk = 0: no
+ *      keys.  qo may be q and ko may be k (same strides): in place.
+ *   norm 0: n = x (wq and wk have to be NULL); else wq, wk: D fp32 values each,
+ *      or NULL (1).  eps >= 0.
+ *   D even, 2 <= D <= 256 (else LA_ERR_UNSUPPORTED).
+ * All arithmetic is fp32, y is rounded once.
+ */
+la_status la_qk_rotate_forward(la_view q, la_view k, la_view qo, la_view ko, const float *wq, const float *wk,
+                               la_rotation rot, la_qk_shape s, int norm, float eps, la_stream_t stream);
+
+/* Bytes of device workspace la_qk_rotate_backward needs; (size_t)-1 for an invalid shape. */
+size_t la_qk_rotate_workspace_bytes(la_qk_shape s);
+
+/*
+ * Backward of la_qk_rotate_forward: given dqo = dL/dqo and dko = dL/dko, and the
+ * forward's own inputs, with u the rotation of dy back by the same angle:
+ *   dx = rstd (u w - xh avg(u w xh)),  xh = x rstd      (norm 0: dx = u)
+ *   dw = sum over all heads and tokens of u xh
+ *   dq, dk: as q, k; dq may be dqo and dk may be dko (same strides).
+ *   dwq, dwk: D fp32 values each, or NULL (not wanted; NULL with norm 0).
+ *   workspace: la_qk_rotate_workspace_bytes(s) bytes where dwq or dwk is given
+ *      (the CTAs' sums, added in a fixed order: equal calls give equal bits).
+ */
+la_status la_qk_rotate_backward(la_view dqo, la_view dko, la_view q, la_view k, la_view dq, la_view dk,
+                                const float *wq, const float *wk, la_rotation rot, la_qk_shape s, int norm, float eps,
+                                float *dwq, float *dwk, void *workspace, size_t ws_bytes, la_stream_t stream);
 
 /*
  * Non-causal attention that allocates nothing, for callers that cannot

@@ -1,0 +1,263 @@
+"""GPU parity of the norm and rotation of queries and keys against the fp64
+oracle (oracle/decay.py).
+
+Tolerances, element by element, with u = 2^-24.  A sum over a head's D squares
+takes at most 8 + 5 additions on a lane's and the lanes' way and D products,
+so rstd is within 16 u of itself.  The turn is rounded to fp32 in half turns
+(an error of u / 2 of at most one half turn, so pi u / 2 in radians), its sine
+and cosine add 2 u each: an output n_i c - n_j s is within (16 + 8) u (|n_i| +
+|n_j|).  The gradient's average over D adds the same sums.  Sums over heads
+and tokens run on one thread's way over at most rows/32 + 700 additions.  An
+output's own rounding adds half a step.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decay
+from weight_recurrence_gb300 import la
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+U = 2.0 ** -24
+DTYPES = [torch.float32, torch.bfloat16]
+PAIRS = ["half", "adjacent"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _setup():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    la.lib()
+
+
+def _np(t):
+    return None if t is None else t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _close(name, got, ref, tol):
+    got = _np(got)
+    assert got.shape == ref.shape, (name, got.shape, ref.shape)
+    assert np.isfinite(got).all(), name
+    worst = np.abs(got - ref) / (tol + 1e-30)
+    assert worst.max(initial=0.0) <= 1.0, (name, float(worst.max()), np.unravel_index(worst.argmax(), worst.shape))
+
+
+def inputs(B, N, Hq, Hk, D, P, A, dtype, seed, layout="heads", far=100000):
+    rng = torch.Generator().manual_seed(seed)
+    mk = lambda H: torch.randn((B, H, N, D), generator=rng).to(dtype).to(DEV)  # noqa: E731
+    q, dq, k, dk = mk(Hq), mk(Hq), mk(Hk), mk(Hk)
+    if layout == "tokens":
+        both = torch.cat([t.transpose(1, 2).flatten(2) for t in (q, k)], dim=-1)
+        q = both[..., :Hq * D].unflatten(-1, (Hq, D)).transpose(1, 2)
+        k = both[..., Hq * D:].unflatten(-1, (Hk, D)).transpose(1, 2)
+    elif layout == "odd":
+        q, k, dq, dk = (torch.cat([t, t[..., :1]], dim=-1)[..., :-1] for t in (q, k, dq, dk))
+    pos = torch.randint(-far, far, (A, B, N), generator=rng, dtype=torch.int32).to(DEV)
+    freq = (10000.0 ** (-torch.arange(P, dtype=torch.float64) / max(P, 1))).float().to(DEV)
+    axes = tuple(int(x) for x in torch.randint(0, A, (P,), generator=rng))
+    wq, wk = (1 + 0.3 * torch.randn((2, D), generator=rng)).to(DEV)
+    return q, k, dq, dk, pos, freq, axes, wq, wk
+
+
+def _turned_abs(x, P, pairs):
+    """|x_i| + |x_j| of every channel's pair."""
+    i, j = decay._channels(P, pairs)
+    s = np.abs(x)
+    t = s.copy()
+    t[..., i] = t[..., j] = s[..., i] + s[..., j]
+    return t
+
+
+def check_one(name, x, dy, w, y, dx, dw, angle, eps, norm, pairs, dtype):
+    P, D = angle.shape[-1], x.shape[-1]
+    half = torch.finfo(dtype).eps / 2
+    xn, wn = _np(x), _np(w)
+    ref = decay.rotate(xn, angle, wn, eps, norm, pairs)
+    n = xn / np.sqrt((xn * xn).mean(-1, keepdims=True) + eps) if norm else xn
+    n = n if wn is None else n * wn
+    _close(name, y, ref, 24 * U * _turned_abs(n, P, pairs) + half * np.abs(ref))
+    if dx is None:
+        return
+    dyn = _np(dy)
+    rx, rw = decay.rotate_backward(dyn, xn, angle, wn, eps, norm, pairs)
+    ua = _turned_abs(dyn, P, pairs)
+    if norm:
+        r = 1 / np.sqrt((xn * xn).mean(-1, keepdims=True) + eps)
+        xh, wa = np.abs(xn) * r, np.ones(D) if wn is None else np.abs(wn)
+        size = r * (ua * wa + xh * (ua * wa * xh).mean(-1, keepdims=True))
+        _close("d" + name, dx, rx, 90 * U * size + half * np.abs(rx))
+        rows = xn.size // D
+        _close("dw" + name, dw, rw, (rows / 32 + 700 + 50) * U * (ua * xh).sum((0, 1, 2)))
+    else:
+        _close("d" + name, dx, rx, 24 * U * ua + half * np.abs(rx))
+        assert dw is None
+
+
+def check(B, N, Hq, Hk, D, P, A=1, dtype=torch.float32, seed=0, layout="heads", norm=True, pairs="half", weights=True,
+          eps=1e-6, far=100000):
+    q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(B, N, Hq, Hk, D, P, A, dtype, seed, layout, far)
+    if not (norm and weights):
+        wq = wk = None
+    if Hk == 0:
+        k = dko = wk = None
+    how = dict(wq=wq, wk=wk, eps=eps, norm=norm, pairs=pairs, axes=axes)
+    qo, ko = la.la_qk_rotate_forward(q, k, pos, freq, **how)
+    dq, dk, dwq, dwk = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, **how)
+    angle = decay.angles(pos.cpu().numpy(), freq.cpu().numpy(), axes)
+    check_one("q", q, dqo, wq, qo, dq, dwq, angle, eps, norm, pairs, dtype)
+    if Hk:
+        check_one("k", k, dko, wk, ko, dk, dwk, angle, eps, norm, pairs, dtype)
+    else:
+        assert ko is None and dk is None and dwk is None
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pairs", PAIRS)
+@pytest.mark.parametrize("D,P", [(64, 32), (128, 64), (256, 128), (32, 16), (16, 8), (64, 16), (128, 20), (80, 40), (80, 20),
+                                 (96, 31), (6, 3), (2, 1), (2, 0), (64, 0), (130, 65), (254, 3), (8, 4), (8, 1)])
+def test_widths(D, P, pairs, dtype):
+    check(2, 9, 3, 2, D, P, dtype=dtype, pairs=pairs, seed=D + P)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("norm,weights", [(True, True), (True, False), (False, False)])
+@pytest.mark.parametrize("layout", ["heads", "tokens", "odd"])
+@pytest.mark.parametrize("pairs", PAIRS)
+def test_layouts(pairs, layout, norm, weights, dtype):
+    check(2, 37, 5, 3, 64, 24, A=3, dtype=dtype, pairs=pairs, layout=layout, norm=norm, weights=weights)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,N,Hq,Hk", [(1, 1, 1, 0), (1, 1, 1, 1), (64, 1, 16, 4), (1, 1, 40, 8), (3, 1000, 4, 1), (1, 5000, 9, 9),
+                                       (5000, 1, 3, 2), (7, 701, 2, 0)])
+def test_counts(B, N, Hq, Hk, dtype):
+    check(B, N, Hq, Hk, 64, 32, dtype=dtype, seed=N)
+    check(B, N, Hq, Hk, 48, 11, A=2, dtype=dtype, seed=N, pairs="adjacent")
+
+
+def test_more_tokens_than_the_backward_keeps_groups():
+    check(3, 9000, 2, 1, 64, 32, dtype=torch.bfloat16)
+    check(1, 9000, 1, 2, 34, 17, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("far", [1 << 24, (1 << 31) - 1])
+@pytest.mark.parametrize("pairs", PAIRS)
+def test_far_positions(far, pairs):
+    check(2, 50, 2, 2, 64, 32, A=2, pairs=pairs, far=far)
+
+
+def test_frequencies_over_their_range():
+    """Radians a position from far above a turn to next to nothing, of both signs; not finite: NaN for that pair alone."""
+    q, k, _, _, pos, _, _, wq, wk = inputs(2, 40, 2, 2, 64, 32, 1, torch.float32, 3, far=1 << 20)
+    freq = torch.tensor([(-1.0) ** i * 2.0 ** (12 - 3 * i) * 1.3 for i in range(32)], device=DEV)
+    freq[30], freq[31] = 0.0, 1e-44
+    qo, _ = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk)
+    angle = decay.angles(pos.cpu().numpy(), freq.cpu().numpy())
+    check_one("q", q, None, wq, qo, None, None, angle, 1e-6, True, "half", torch.float32)
+    freq[5], freq[7] = float("nan"), float("inf")
+    got, _ = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk)
+    hit = [5, 7, 37, 39]
+    rest = [c for c in range(64) if c not in hit]
+    assert torch.isnan(got[..., hit]).all() and torch.equal(got[..., rest], qo[..., rest])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_position_forms(dtype):
+    """[N], [B,N] and [A,B,N], and views of them, give the same."""
+    q, k, _, _, pos, freq, _, wq, wk = inputs(2, 30, 2, 2, 64, 32, 1, dtype, 4)
+    pos = pos[:, :1].expand(1, 2, 30)
+    want = la.la_qk_rotate_forward(q, k, pos.contiguous(), freq, wq, wk)
+    wide = torch.zeros(2, 60, dtype=torch.int32, device=DEV)
+    wide[:, ::2] = pos[0]
+    for p in (pos[0, 0], pos[0], pos, wide[:, ::2]):
+        got = la.la_qk_rotate_forward(q, k, p, freq, wq, wk, axes=(0,) * 32)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pairs", PAIRS)
+@pytest.mark.parametrize("D,P", [(64, 32), (50, 13)])
+def test_in_place(D, P, pairs, dtype):
+    q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(2, 33, 4, 2, D, P, 2, dtype, 5, "tokens")
+    how = dict(wq=wq, wk=wk, pairs=pairs, axes=axes)
+    want = la.la_qk_rotate_forward(q, k, pos, freq, **how)
+    grads = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, **how)
+    got = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, dq=dqo, dk=dko, **how)
+    assert got[0] is not None and all(torch.equal(a, b) for a, b in zip(got, grads))
+    got = la.la_qk_rotate_forward(q, k, pos, freq, qo=q, ko=k, **how)
+    assert got[0].data_ptr() == q.data_ptr() and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_of_zeros_and_extremes(dtype):
+    q, k, dqo, dko, pos, freq, _, wq, wk = inputs(1, 8, 2, 2, 64, 32, 1, dtype, 6)
+    q[:, :, 3] = 0.0
+    q[:, :, 4, 5] = float("nan")
+    qo, _ = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk)
+    assert not qo[:, :, 3].any() and torch.isnan(qo[:, :, 4]).all()
+    assert torch.isfinite(qo[:, :, [0, 1, 2, 3, 5, 6, 7]]).all()
+    q[:, :, 4] = 1.0
+    dq = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk)[0]
+    assert torch.isfinite(dq).all()       # a row of zeros: 1/sqrt(eps) times the rest
+    angle = decay.angles(pos[None].cpu().numpy()[0], freq.cpu().numpy())
+    check_one("q", q, dqo, wq, la.la_qk_rotate_forward(q, k, pos, freq, wq, wk)[0], dq,
+              la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk)[2], angle, 1e-6, True, "half", dtype)
+
+
+def test_empty_batches():
+    for shape in ((0, 2, 5, 16), (2, 2, 0, 16), (2, 0, 5, 16)):
+        q = torch.zeros(shape, device=DEV)
+        pos, freq = torch.zeros(shape[0], shape[2], dtype=torch.int32, device=DEV), torch.ones(8, device=DEV)
+        assert la.la_qk_rotate_forward(q, q.clone(), pos, freq)[1].shape == shape
+        dq, dk, dwq, dwk = la.la_qk_rotate_backward(q, q.clone(), q, q.clone(), pos, freq)
+        assert dq.shape == shape and not dwq.any() and not dwk.any()
+
+
+def test_offsets_past_32_bits():
+    q, k, _, _, pos, freq, _, wq, wk = inputs(2, 20, 2, 1, 64, 32, 1, torch.bfloat16, 7)
+    far = (1 << 31) + 64
+    room = torch.empty(far + 20 * 512, dtype=torch.bfloat16, device=DEV)
+    at = lambda i, H: room.as_strided((2, H, 20, 64), (far, 64, 512, 1), 128 * i)  # noqa: E731
+    at(0, 2).copy_(q)
+    at(1, 1).copy_(k)
+    got = la.la_qk_rotate_forward(at(0, 2), at(1, 1), pos, freq, wq, wk, qo=at(2, 2), ko=at(3, 1))
+    want = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_streams_and_graphs():
+    def run(t):
+        q, k, dqo, dko, pos, freq, axes, wq, wk = t
+        how = dict(wq=wq, wk=wk, axes=axes)
+        return [*la.la_qk_rotate_forward(q, k, pos, freq, **how),
+                *la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, **how)]
+    sets = [list(inputs(2, 3000, 4, 2, 64, 32, 2, torch.bfloat16, s)) for s in range(3)]
+    for t in sets:
+        t[6] = sets[0][6]
+    want = [run(t) for t in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, t in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(run(t))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i % 2]))
+    held = [t.clone() if isinstance(t, torch.Tensor) else t for t in sets[0]]
+    with torch.cuda.stream(streams[0]):
+        run(held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run(held)
+    for i in (1, 2, 0):
+        for h, t in zip(held, sets[i]):
+            if isinstance(h, torch.Tensor):
+                h.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))

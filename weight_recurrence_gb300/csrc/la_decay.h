@@ -1,0 +1,61 @@
+// la_decay.h - linear attention with a decay for each head as sweeps: the one
+// pattern that the forward pass and each of the three gradients are.
+//
+// A sweep reads rows x_i, y_i (width D) and z_i (width M) and carries a state
+// (D x M).  With a = e^g, forwards:
+//   out_i = c_intra sum_{j<=i} a^(i-j) (x_i.y_j) z_j + c_inter a^(i+1) x_i S
+// and backwards in time, the state H entering behind the last of n tokens:
+//   out_i = c_intra sum_{j>=i} a^(j-i) (x_i.y_j) z_j + c_inter a^(n-1-i) x_i H
+// and the state after the sweep is
+//   forwards   a^n S + c_state sum_j a^(n-1-j) y_j z_j
+//   backwards  a^n H + c_state sum_j a^(j+1) y_j z_j
+//
+//            x     y     z     state                  c_intra c_inter c_state
+//   out      q     k     v     S0 -> SN               scale   scale   1
+//   dq       dout  v     k     S0 transposed          scale   scale   -
+//   dv       k     q     dout  dSN -> dS0, backwards  scale   1       scale
+//   dk       v     dout  q     dSN transposed, bw.    scale   1       -
+//
+// Few heads are cut into segments of tokens: a sweep over each segment gives
+// its sum alone, a scan over the segments the state at each one's start, and
+// the sweeps of all segments then run side by side.
+#pragma once
+
+#include "la_layer.h"
+
+namespace la {
+
+// What a state keeps over n tokens, a^n = x + y.  Next to 1 as 1 + (a^n - 1): a^n
+// rounded would shorten (or lengthen) a long memory a little with every chunk.
+// Else as a^n itself, which keeps its digits where it is small.
+__device__ __forceinline__ float2 kept(float g, int n) {
+    const float e = g * (float)n;
+    return e > -0.5f ? make_float2(1.f, expm1f(e)) : make_float2(expf(e), 0.f);
+}
+__device__ __forceinline__ float keep(float2 a, float s) { return fmaf(a.y, s, a.x * s); }
+
+struct DecaySweep {
+    la_view x, y, z, out;      // out.data null: the state alone (x is not read)
+    const float *start;        // state before the sweep, null: 0
+    float *end;                // state after it, null: not wanted
+    int D, M;                  // widths of x and y, of z and out
+    int transposed;            // start and end lie as [M][D], else [D][M]
+    int backwards;
+    float c_intra, c_inter, c_state;
+};
+
+constexpr int kDecayMaxSweeps = 3;
+
+struct DecayLaunch {
+    DecaySweep sweep[kDecayMaxSweeps];
+    int sweeps;
+    const float *log_decay;
+    const int *lens;
+    int B, H, N;
+    int segs, seg_tokens;      // segments of a sequence; tokens of one (a multiple of 128 if segs > 1)
+    int sums;                  // every segment by itself: start 0, end at [B*H][segs][D*M]
+    int starts;                // start at [B*H][segs][D*M]
+    cudaStream_t stream;
+};
+
+}  // namespace la

@@ -1,6 +1,7 @@
 // la_layer.cu - entry points of the operators around the attention: argument
-// checks on the host, then the launchers of la_recurrence.cu, la_layernorm.cu
-// and la_grad.cu.
+// checks on the host, then the launchers of la_recurrence.cu, la_layernorm.cu,
+// la_grad.cu, la_decay.cu and la_rotate.cu.
+#include <initializer_list>
 #include <memory>
 #include <new>
 
@@ -110,6 +111,53 @@ la_status check_distinct(const la_tensor *t, int count) {
         if (find(t[i].src)->dst) return LA_ERR_INVALID_ARG;
     }
     return LA_OK;
+}
+
+// Sizes of the attention with decays: every head is a CTA's (times its segments
+// and blocks of columns) and its state's offset stays in 64 bits.
+la_status check_decay(const la_shape &s) {
+    if (s.B < 0 || s.H < 0 || s.N < 0 || s.D < 1 || s.M < 1 || !dtype_ok(s.dtype)) return LA_ERR_INVALID_ARG;
+    if (s.D > kDecayMaxD || s.M > kDecayMaxD) return LA_ERR_UNSUPPORTED;
+    if ((__int128)s.B * s.H * 8 > 0x7fffffff) return LA_ERR_UNSUPPORTED;
+    if (s.N > 0x7fffffff - 256) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+// A state buffer: given ones are fp32 arrays.
+bool states_ok(std::initializer_list<const void *> states) {
+    for (const void *p : states)
+        if (p && !aligned(p, 4)) return false;
+    return true;
+}
+bool any_same(const void *a, std::initializer_list<const void *> others) {
+    for (const void *p : others)
+        if (same(a, p)) return true;
+    return false;
+}
+
+la_status check_qk(const la_qk_shape &s) {
+    if (s.B < 0 || s.N < 0 || s.Hq < 0 || s.Hk < 0 || s.D < 1 || !dtype_ok(s.dtype)) return LA_ERR_INVALID_ARG;
+    if (s.D > kRotateMaxD || s.D % 2) return LA_ERR_UNSUPPORTED;
+    if ((__int128)s.B * s.N > (1LL << 34)) return LA_ERR_UNSUPPORTED;
+    return LA_OK;
+}
+
+la_status check_rotation(const la_rotation &r, const la_qk_shape &s) {
+    if (r.A < 1 || r.A > 8 || r.P < 0 || r.P > s.D / 2) return LA_ERR_INVALID_ARG;
+    if (r.pairs != LA_PAIRS_HALF && r.pairs != LA_PAIRS_ADJACENT) return LA_ERR_INVALID_ARG;
+    if (r.P == 0) return LA_OK;
+    if (r.axes)
+        for (int i = 0; i < r.P; i++)
+            if (r.axes[i] >= r.A) return LA_ERR_INVALID_ARG;
+    if (s.B == 0 || s.N == 0) return LA_OK;   // no positions
+    if (!aligned(r.pos, 4) || !aligned(r.freq, 4)) return LA_ERR_INVALID_ARG;
+    if (!stride_ok(r.sa) || !stride_ok(r.sb) || !stride_ok(r.sn)) return LA_ERR_INVALID_ARG;
+    return LA_OK;
+}
+
+// An output that may be the input it comes from, row for row.
+bool in_place_ok(const la_view &out, const la_view &in) {
+    return out.data != in.data || (out.sb == in.sb && out.sh == in.sh && out.sn == in.sn);
 }
 
 }  // namespace
@@ -271,6 +319,156 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
     const la_status st = check_grads(tensors, count, norm, workspace, ws_bytes, true);
     if (st != LA_OK) return st;
     return from_cuda(grad_norm_clip(tensors, count, max_norm, norm, workspace, (cudaStream_t)stream));
+}
+
+size_t la_decay_workspace_bytes(la_shape s, int backward) {
+    return check_decay(s) == LA_OK ? decay_ws_bytes(s, backward != 0) : (size_t)-1;
+}
+
+la_status la_decay_forward(la_view q, la_view k, la_view v, la_view out, const float *log_decay, const int *lens,
+                           la_shape s, float scale, const float *S0, float *SN, void *workspace, size_t ws_bytes,
+                           la_stream_t stream) {
+    la_status st = check_decay(s);
+    if (st != LA_OK) return st;
+    if (s.B == 0 || s.H == 0) return LA_OK;
+    if (!states_ok({S0, SN, lens}) || !aligned(log_decay, 4)) return LA_ERR_INVALID_ARG;
+    if (out.data == nullptr && SN == nullptr) return LA_ERR_INVALID_ARG;
+    if (any_same(SN, {log_decay, lens})) return LA_ERR_INVALID_ARG;
+    if (s.N == 0) {
+        s.D *= s.M;   // a state of D M values
+        return from_cuda(pass_state(SN, S0, s, (cudaStream_t)stream));
+    }
+    if (!view_ok(k, s.dtype) || !view_ok(v, s.dtype)) return LA_ERR_INVALID_ARG;
+    if (out.data) {
+        if (!view_ok(q, s.dtype) || !view_ok(out, s.dtype) || !nested(out, s.B, s.H, s.N, s.M)) return LA_ERR_INVALID_ARG;
+        if (any_same(out.data, {q.data, k.data, v.data, log_decay, lens, S0, SN})) return LA_ERR_INVALID_ARG;
+    }
+    if (any_same(SN, {out.data ? q.data : nullptr, k.data, v.data})) return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(decay_ws_bytes(s, false), workspace, ws_bytes)) return LA_ERR_INVALID_ARG;
+    DecayProblem p{};
+    p.q = q, p.k = k, p.v = v, p.out = out, p.log_decay = log_decay, p.lens = lens, p.S0 = S0, p.SN = SN;
+    p.B = s.B, p.H = s.H, p.N = s.N, p.D = s.D, p.M = s.M, p.dtype = s.dtype, p.scale = scale;
+    p.ws = workspace, p.stream = (cudaStream_t)stream;
+    return from_cuda(decay_forward(p));
+}
+
+la_status la_decay_step(la_view q, la_view k, la_view v, la_view y, const float *log_decay, la_shape s, float scale,
+                        float *S, la_stream_t stream) {
+    s.N = 1;
+    q.sn = k.sn = v.sn = y.sn = 0;
+    const la_status st = check_decay(s);
+    if (st != LA_OK) return st;
+    if (s.B == 0 || s.H == 0) return LA_OK;
+    if (!aligned(S, 4) || !aligned(log_decay, 4)) return LA_ERR_INVALID_ARG;
+    if (!view_ok(q, s.dtype) || !view_ok(k, s.dtype) || !view_ok(v, s.dtype) || !view_ok(y, s.dtype) ||
+        !nested(y, s.B, s.H, 1, s.M))
+        return LA_ERR_INVALID_ARG;
+    if (any_same(y.data, {q.data, k.data, v.data, log_decay, S}) || any_same(S, {q.data, k.data, v.data, log_decay}))
+        return LA_ERR_INVALID_ARG;
+    DecayProblem p{};
+    p.q = q, p.k = k, p.v = v, p.out = y, p.log_decay = log_decay, p.SN = S;
+    p.B = s.B, p.H = s.H, p.N = 1, p.D = s.D, p.M = s.M, p.dtype = s.dtype, p.scale = scale;
+    p.stream = (cudaStream_t)stream;
+    return from_cuda(decay_step(p));
+}
+
+la_status la_decay_backward(la_view q, la_view k, la_view v, la_view dout, la_view dq, la_view dk, la_view dv,
+                            const float *log_decay, const int *lens, la_shape s, float scale, const float *S0,
+                            const float *dSN, float *dS0, void *workspace, size_t ws_bytes, la_stream_t stream) {
+    la_status st = check_decay(s);
+    if (st != LA_OK) return st;
+    if (s.B == 0 || s.H == 0) return LA_OK;
+    if (!states_ok({S0, dSN, dS0, lens}) || !aligned(log_decay, 4)) return LA_ERR_INVALID_ARG;
+    if (any_same(dS0, {S0, dSN, log_decay, lens})) return LA_ERR_INVALID_ARG;
+    if (s.N == 0) {
+        s.D *= s.M;
+        return from_cuda(pass_state(dS0, dSN, s, (cudaStream_t)stream));
+    }
+    for (const la_view *w : {&q, &k, &v, &dout, &dq, &dk, &dv})
+        if (!view_ok(*w, s.dtype)) return LA_ERR_INVALID_ARG;
+    if (!nested(dq, s.B, s.H, s.N, s.D) || !nested(dk, s.B, s.H, s.N, s.D) || !nested(dv, s.B, s.H, s.N, s.M))
+        return LA_ERR_INVALID_ARG;
+    const void *outs[] = {dq.data, dk.data, dv.data, dS0};
+    for (const void *o : outs)
+        if (any_same(o, {q.data, k.data, v.data, dout.data, S0, dSN, log_decay, lens})) return LA_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; i++)
+        for (int j = 0; j < i; j++)
+            if (same(outs[i], outs[j])) return LA_ERR_INVALID_ARG;
+    if (!workspace_ok(decay_ws_bytes(s, true), workspace, ws_bytes)) return LA_ERR_INVALID_ARG;
+    DecayProblem p{};
+    p.q = q, p.k = k, p.v = v, p.dout = dout, p.dq = dq, p.dk = dk, p.dv = dv, p.log_decay = log_decay, p.lens = lens;
+    p.S0 = S0, p.dSN = dSN, p.dS0 = dS0;
+    p.B = s.B, p.H = s.H, p.N = s.N, p.D = s.D, p.M = s.M, p.dtype = s.dtype, p.scale = scale;
+    p.ws = workspace, p.stream = (cudaStream_t)stream;
+    return from_cuda(decay_backward(p));
+}
+
+size_t la_qk_rotate_workspace_bytes(la_qk_shape s) {
+    return check_qk(s) == LA_OK ? rotate_ws_bytes(s) : (size_t)-1;
+}
+
+// The checks that both directions share; y: qo, ko or dq, dk; dy: null data forward.
+static la_status check_rotate(const la_view *x, const la_view *y, const la_view *dy, const float *const *w,
+                              const la_rotation &rot, const la_qk_shape &s, int norm, float eps) {
+    la_status st = check_qk(s);
+    if (st != LA_OK) return st;
+    st = check_rotation(rot, s);
+    if (st != LA_OK) return st;
+    if (norm ? !(eps >= 0.f) : w[0] != nullptr || w[1] != nullptr) return LA_ERR_INVALID_ARG;
+    if (!states_ok({w[0], w[1]})) return LA_ERR_INVALID_ARG;
+    if (s.B == 0 || s.N == 0) return LA_OK;
+    const int H[2] = {s.Hq, s.Hk};
+    for (int i = 0; i < 2; i++) {
+        if (H[i] == 0) continue;
+        if (!view_ok(x[i], s.dtype) || !view_ok(y[i], s.dtype) || (dy && !view_ok(dy[i], s.dtype))) return LA_ERR_INVALID_ARG;
+        if (!nested(y[i], s.B, H[i], s.N, s.D)) return LA_ERR_INVALID_ARG;
+        if (any_same(y[i].data, {w[0], w[1], rot.P ? rot.pos : nullptr, rot.P ? rot.freq : nullptr})) return LA_ERR_INVALID_ARG;
+        // in place only on the rows that the output comes from
+        if (!in_place_ok(y[i], dy ? dy[i] : x[i]) || (dy && y[i].data == x[i].data)) return LA_ERR_INVALID_ARG;
+        const int o = 1 - i;
+        if (H[o] == 0) continue;
+        if (any_same(y[i].data, {x[o].data, y[o].data, dy ? dy[o].data : nullptr})) return LA_ERR_INVALID_ARG;
+    }
+    return LA_OK;
+}
+
+la_status la_qk_rotate_forward(la_view q, la_view k, la_view qo, la_view ko, const float *wq, const float *wk,
+                               la_rotation rot, la_qk_shape s, int norm, float eps, la_stream_t stream) {
+    const la_view x[2] = {q, k}, y[2] = {qo, ko};
+    const float *const w[2] = {wq, wk};
+    const la_status st = check_rotate(x, y, nullptr, w, rot, s, norm, eps);
+    if (st != LA_OK || s.B == 0 || s.N == 0 || s.Hq + s.Hk == 0) return st;
+    RotateProblem p{};
+    p.q = q, p.k = k, p.qo = qo, p.ko = ko, p.wq = wq, p.wk = wk, p.rot = rot, p.s = s, p.norm = norm != 0, p.eps = eps;
+    p.stream = (cudaStream_t)stream;
+    return from_cuda(rotate_forward(p));
+}
+
+la_status la_qk_rotate_backward(la_view dqo, la_view dko, la_view q, la_view k, la_view dq, la_view dk,
+                                const float *wq, const float *wk, la_rotation rot, la_qk_shape s, int norm, float eps,
+                                float *dwq, float *dwk, void *workspace, size_t ws_bytes, la_stream_t stream) {
+    const la_view x[2] = {q, k}, y[2] = {dq, dk}, dy[2] = {dqo, dko};
+    const float *const w[2] = {wq, wk};
+    const la_status st = check_rotate(x, y, dy, w, rot, s, norm, eps);
+    if (st != LA_OK) return st;
+    if (!states_ok({dwq, dwk}) || (!norm && (dwq || dwk)) || same(dwq, dwk)) return LA_ERR_INVALID_ARG;
+    const bool empty = s.B == 0 || s.N == 0;
+    for (const float *d : {dwq, dwk})
+        if (any_same(d, {wq, wk, rot.P ? rot.pos : nullptr, rot.P ? rot.freq : nullptr}) ||
+            (!empty && s.Hq && any_same(d, {q.data, dq.data, dqo.data})) ||
+            (!empty && s.Hk && any_same(d, {k.data, dk.data, dko.data})))
+            return LA_ERR_INVALID_ARG;
+    if (empty || s.Hq + s.Hk == 0) {   // sums over nothing
+        cudaError_t e = cudaSuccess;
+        for (float *d : {dwq, dwk})
+            if (d && e == cudaSuccess) e = cudaMemsetAsync(d, 0, (size_t)s.D * sizeof(float), (cudaStream_t)stream);
+        return from_cuda(e);
+    }
+    if ((dwq || dwk) && (ws_bytes < rotate_ws_bytes(s) || !aligned(workspace, 16))) return LA_ERR_INVALID_ARG;
+    RotateProblem p{};
+    p.q = q, p.k = k, p.qo = dq, p.ko = dk, p.dqo = dqo, p.dko = dko, p.wq = wq, p.wk = wk, p.rot = rot, p.s = s;
+    p.norm = norm != 0, p.eps = eps, p.dwq = dwq, p.dwk = dwk, p.ws = workspace, p.stream = (cudaStream_t)stream;
+    return from_cuda(rotate_backward(p));
 }
 
 }  // extern "C"

@@ -42,6 +42,13 @@ struct Calls {
     decltype(&la_grad_workspace_bytes) grad_workspace_bytes;
     decltype(&la_grad_norm) grad_norm;
     decltype(&la_grad_clip) grad_clip;
+    decltype(&la_decay_workspace_bytes) decay_workspace_bytes;
+    decltype(&la_decay_forward) decay_forward;
+    decltype(&la_decay_step) decay_step;
+    decltype(&la_decay_backward) decay_backward;
+    decltype(&la_qk_rotate_forward) qk_rotate_forward;
+    decltype(&la_qk_rotate_workspace_bytes) qk_rotate_workspace_bytes;
+    decltype(&la_qk_rotate_backward) qk_rotate_backward;
 } calls;
 
 std::string shape_text(at::IntArrayRef s) {
@@ -380,6 +387,206 @@ PyObject *grad(PyObject *const *a) {
                   {norm});
 }
 
+float number(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) throw Error{nullptr, ""};
+    return (float)v;
+}
+
+// Shape of the attention with decays: k [B,H,N,D] and v [B,H,N,M] (no N for a step).
+la_shape decay_shape(const at::Tensor &k, const at::Tensor &v, bool step) {
+    const auto a = k.sizes(), b = v.sizes();
+    const size_t dims = step ? 3 : 4;
+    if (a.size() != dims || b.size() != dims)
+        bad_value(step ? "k must be [B,H,D] and v [B,H,M]" : "k must be [B,H,N,D] and v [B,H,N,M]");
+    if (a.slice(0, dims - 1) != b.slice(0, dims - 1)) bad_value("k and v must agree in all but the last dimension");
+    if (a.back() < 1 || b.back() < 1) bad_value("k and v must have a channel");
+    return {small(a[0]), small(a[1]), step ? 1 : small(a[2]), small(a.back()), small(b.back()), dtype_of(k)};
+}
+c10::SmallVector<int64_t, 4> with_last(const at::Tensor &x, int64_t n) {
+    c10::SmallVector<int64_t, 4> s(x.sizes().begin(), x.sizes().end());
+    s.back() = n;
+    return s;
+}
+
+// (q, k, v, log_decay, scale, S0, SN, lens, out, want_out, stream) -> (status, out)
+PyObject *decay_forward(PyObject *const *a) {
+    const at::Tensor &q = tensor("q", a[0]), &k = required("k", a[1]), &v = required("v", a[2]);
+    const at::Tensor &g = required("log_decay", a[3]), &S0 = tensor("S0", a[5]), &SN = tensor("SN", a[6]);
+    const at::Tensor &lens = tensor("lens", a[7]), &given = tensor("out", a[8]);
+    const bool want = PyObject_IsTrue(a[9]);
+    const la_shape s = decay_shape(k, v, false);
+    const auto device = k.device();
+    if (want && !q.defined()) bad_value("q is required");
+    if (!want && given.defined()) bad_value("out needs want_out");
+    if (!want && !SN.defined()) bad_value("nothing is wanted: want_out or SN");
+    like("q", q, k.sizes(), k.scalar_type(), device);
+    like("v", v, v.sizes(), k.scalar_type(), device);
+    like("out", given, v.sizes(), k.scalar_type(), device);
+    array("log_decay", g, {s.H}, device);
+    array("S0", S0, {s.B, s.H, s.D, s.M}, device);
+    array("SN", SN, {s.B, s.H, s.D, s.M}, device);
+    array("lens", lens, {s.B}, device, at::kInt);
+    const float scale = number(a[4]);
+    const Place place(a[10], device, {&q, &k, &v, &g, &S0, &SN, &lens, &given});
+    at::Tensor out;
+    if (want) out = out_like(given, v);
+    const size_t need = calls.decay_workspace_bytes(s, 0);
+    const at::Tensor ws = workspace(k, need == kInvalid ? 0 : need);
+    return result(calls.decay_forward(view_of("q", q, false), view_of("k", k, false), view_of("v", v, false),
+                                      view_of("out", out, false), data(g), data<int>(lens), s, scale, data(S0), data(SN),
+                                      data<void>(ws), need, place.stream()),
+                  {out});
+}
+
+// (q, k, v, S, log_decay, scale, y, stream) -> (status, y)
+PyObject *decay_step(PyObject *const *a) {
+    const at::Tensor &q = required("q", a[0]), &k = required("k", a[1]), &v = required("v", a[2]);
+    const at::Tensor &S = required("S", a[3]), &g = required("log_decay", a[4]), &given = tensor("y", a[6]);
+    const la_shape s = decay_shape(k, v, true);
+    const auto device = k.device();
+    like("q", q, k.sizes(), k.scalar_type(), device);
+    like("v", v, v.sizes(), k.scalar_type(), device);
+    like("y", given, v.sizes(), k.scalar_type(), device);
+    array("log_decay", g, {s.H}, device);
+    array("S", S, {s.B, s.H, s.D, s.M}, device);
+    const float scale = number(a[5]);
+    const Place place(a[7], device, {&q, &k, &v, &S, &g, &given});
+    const at::Tensor y = out_like(given, v);
+    return result(calls.decay_step(view_of("q", q, true), view_of("k", k, true), view_of("v", v, true),
+                                   view_of("y", y, true), data(g), s, scale, data(S), place.stream()),
+                  {y});
+}
+
+// (q, k, v, dout, log_decay, scale, S0, dSN, dS0, lens, dq, dk, dv, stream) -> (status, dq, dk, dv)
+PyObject *decay_backward(PyObject *const *a) {
+    const at::Tensor &q = required("q", a[0]), &k = required("k", a[1]), &v = required("v", a[2]);
+    const at::Tensor &dout = required("dout", a[3]), &g = required("log_decay", a[4]), &S0 = tensor("S0", a[6]);
+    const at::Tensor &dSN = tensor("dSN", a[7]), &dS0 = tensor("dS0", a[8]), &lens = tensor("lens", a[9]);
+    const at::Tensor &gq = tensor("dq", a[10]), &gk = tensor("dk", a[11]), &gv = tensor("dv", a[12]);
+    const la_shape s = decay_shape(k, v, false);
+    const auto device = k.device();
+    like("q", q, k.sizes(), k.scalar_type(), device);
+    like("v", v, v.sizes(), k.scalar_type(), device);
+    like("dout", dout, v.sizes(), k.scalar_type(), device);
+    like("dq", gq, k.sizes(), k.scalar_type(), device);
+    like("dk", gk, k.sizes(), k.scalar_type(), device);
+    like("dv", gv, v.sizes(), k.scalar_type(), device);
+    array("log_decay", g, {s.H}, device);
+    for (const auto &st : {std::make_pair("S0", &S0), std::make_pair("dSN", &dSN), std::make_pair("dS0", &dS0)})
+        array(st.first, *st.second, {s.B, s.H, s.D, s.M}, device);
+    array("lens", lens, {s.B}, device, at::kInt);
+    const float scale = number(a[5]);
+    const Place place(a[13], device, {&q, &k, &v, &dout, &g, &S0, &dSN, &dS0, &lens, &gq, &gk, &gv});
+    const at::Tensor dq = out_like(gq, k), dk = out_like(gk, k), dv = out_like(gv, v);
+    const size_t need = calls.decay_workspace_bytes(s, 1);
+    const at::Tensor ws = workspace(k, need == kInvalid ? 0 : need);
+    return result(calls.decay_backward(view_of("q", q, false), view_of("k", k, false), view_of("v", v, false),
+                                       view_of("dout", dout, false), view_of("dq", dq, false), view_of("dk", dk, false),
+                                       view_of("dv", dv, false), data(g), data<int>(lens), s, scale, data(S0), data(dSN),
+                                       data(dS0), data<void>(ws), need, place.stream()),
+                  {dq, dk, dv});
+}
+
+// What the rotation's two calls take alike: q [B,Hq,N,D], k [B,Hk,N,D] or none, positions, frequencies, axes.
+struct Rotation {
+    la_qk_shape s;
+    la_rotation r;
+    Rotation(const at::Tensor &q, const at::Tensor &k, const at::Tensor &pos, const at::Tensor &freq, PyObject *pairs,
+             PyObject *axes) {
+        const auto sh = q.sizes();
+        if (sh.size() != 4 || sh[3] < 1) bad_value("q must be [B,Hq,N,D]");
+        if (k.defined() && (k.dim() != 4 || k.size(0) != sh[0] || k.size(2) != sh[2] || k.size(3) != sh[3]))
+            bad_value("k must be [B,Hk,N,D] with q's B, N and D");
+        const auto device = q.device();
+        like("k", k, k.sizes(), q.scalar_type(), device);
+        s = {small(sh[0]), small(sh[2]), small(sh[1]), k.defined() ? small(k.size(1)) : 0, small(sh[3]), dtype_of(q)};
+        if (freq.dim() != 1) bad_value("freq must be [P]");
+        array("freq", freq, freq.sizes(), device);
+        const int64_t d = pos.dim();
+        if (d < 1 || d > 3 || pos.size(d - 1) != sh[2] || (d > 1 && pos.size(d - 2) != sh[0]))
+            bad_value("pos must be [N], [B,N] or [A,B,N]");
+        like("pos", pos, pos.sizes(), at::kInt, device);
+        const auto st = pos.strides();
+        r.pos = data<int>(pos), r.freq = data(freq);
+        r.sn = st[d - 1], r.sb = d > 1 ? st[d - 2] : 0, r.sa = d > 2 ? st[0] : 0;
+        r.A = d > 2 ? small(pos.size(0)) : 1, r.P = small(freq.numel());
+        if (2 * (int64_t)r.P > sh[3]) bad_value("freq has more pairs than a head has");
+        r.pairs = (la_pairs)PyLong_AsLong(pairs), r.axes = nullptr;
+        if (axes != Py_None) {
+            char *bytes;
+            Py_ssize_t n;
+            if (PyBytes_AsStringAndSize(axes, &bytes, &n) < 0) throw Error{nullptr, ""};
+            if (n != r.P) bad_value("axes must have one entry per pair");
+            r.axes = reinterpret_cast<const unsigned char *>(bytes);
+        }
+    }
+};
+
+// (q, k, pos, freq, wq, wk, eps, norm, pairs, axes, qo, ko, stream) -> (status, qo, ko)
+PyObject *qk_rotate_forward(PyObject *const *a) {
+    const at::Tensor &q = required("q", a[0]), &k = tensor("k", a[1]), &pos = required("pos", a[2]);
+    const at::Tensor &freq = required("freq", a[3]), &wq = tensor("wq", a[4]), &wk = tensor("wk", a[5]);
+    const at::Tensor &gq = tensor("qo", a[10]), &gk = tensor("ko", a[11]);
+    const Rotation rot(q, k, pos, freq, a[8], a[9]);
+    const auto device = q.device();
+    const bool norm = PyObject_IsTrue(a[7]);
+    if (!norm && (wq.defined() || wk.defined())) bad_value("wq and wk need the norm");
+    if (!k.defined() && (wk.defined() || gk.defined())) bad_value("wk and ko need k");
+    array("wq", wq, {rot.s.D}, device);
+    array("wk", wk, {rot.s.D}, device);
+    like("qo", gq, q.sizes(), q.scalar_type(), device);
+    if (k.defined()) like("ko", gk, k.sizes(), k.scalar_type(), device);
+    const float eps = number(a[6]);
+    const Place place(a[12], device, {&q, &k, &pos, &freq, &wq, &wk, &gq, &gk});
+    const at::Tensor qo = out_like(gq, q);
+    at::Tensor ko;
+    if (k.defined()) ko = out_like(gk, k);
+    return result(calls.qk_rotate_forward(view_of("q", q, false), view_of("k", k, false), view_of("qo", qo, false),
+                                          view_of("ko", ko, false), data(wq), data(wk), rot.r, rot.s, norm, eps,
+                                          place.stream()),
+                  {qo, ko});
+}
+
+// (dqo, dko, q, k, pos, freq, wq, wk, eps, norm, pairs, axes, dq, dk, dwq, dwk, stream) -> (status, dq, dk, dwq, dwk)
+PyObject *qk_rotate_backward(PyObject *const *a) {
+    const at::Tensor &dqo = required("dqo", a[0]), &dko = tensor("dko", a[1]), &q = required("q", a[2]);
+    const at::Tensor &k = tensor("k", a[3]), &pos = required("pos", a[4]), &freq = required("freq", a[5]);
+    const at::Tensor &wq = tensor("wq", a[6]), &wk = tensor("wk", a[7]), &gq = tensor("dq", a[12]);
+    const at::Tensor &gk = tensor("dk", a[13]), &gwq = tensor("dwq", a[14]), &gwk = tensor("dwk", a[15]);
+    const Rotation rot(q, k, pos, freq, a[10], a[11]);
+    const auto device = q.device();
+    const bool norm = PyObject_IsTrue(a[9]);
+    if (!norm && (wq.defined() || wk.defined() || gwq.defined() || gwk.defined()))
+        bad_value("weights and their gradients need the norm");
+    if (k.defined() != dko.defined()) bad_value("dko and k go together");
+    if (!k.defined() && (wk.defined() || gk.defined() || gwk.defined())) bad_value("wk, dk and dwk need k");
+    like("dqo", dqo, q.sizes(), q.scalar_type(), device);
+    like("dq", gq, q.sizes(), q.scalar_type(), device);
+    if (k.defined()) {
+        like("dko", dko, k.sizes(), k.scalar_type(), device);
+        like("dk", gk, k.sizes(), k.scalar_type(), device);
+    }
+    array("wq", wq, {rot.s.D}, device);
+    array("wk", wk, {rot.s.D}, device);
+    array("dwq", gwq, {rot.s.D}, device);
+    array("dwk", gwk, {rot.s.D}, device);
+    const float eps = number(a[8]);
+    const Place place(a[16], device, {&dqo, &dko, &q, &k, &pos, &freq, &wq, &wk, &gq, &gk, &gwq, &gwk});
+    const at::Tensor dq = out_like(gq, q);
+    at::Tensor dk, dwq, dwk;
+    if (k.defined()) dk = out_like(gk, k);
+    if (norm) dwq = out_float(gwq, q, {rot.s.D});
+    if (norm && k.defined()) dwk = out_float(gwk, q, {rot.s.D});
+    const size_t need = calls.qk_rotate_workspace_bytes(rot.s);
+    const at::Tensor ws = workspace(q, norm && need != kInvalid ? need : 0);
+    return result(calls.qk_rotate_backward(view_of("dqo", dqo, false), view_of("dko", dko, false), view_of("q", q, false),
+                                           view_of("k", k, false), view_of("dq", dq, false), view_of("dk", dk, false),
+                                           data(wq), data(wk), rot.r, rot.s, norm, eps, data(dwq), data(dwk),
+                                           data<void>(ws), need, place.stream()),
+                  {dq, dk, dwq, dwk});
+}
+
 // (tensor, step) -> (address, sb, sh, sn) and (tensor) -> (address, stride): what a call hands to the library.
 PyObject *view(PyObject *const *a) {
     const la_view v = view_of("x", required("x", a[0]), PyObject_IsTrue(a[1]));
@@ -411,6 +618,13 @@ PyObject *use(PyObject *const *a) {
     get(c.grad_workspace_bytes, "la_grad_workspace_bytes");
     get(c.grad_norm, "la_grad_norm");
     get(c.grad_clip, "la_grad_clip");
+    get(c.decay_workspace_bytes, "la_decay_workspace_bytes");
+    get(c.decay_forward, "la_decay_forward");
+    get(c.decay_step, "la_decay_step");
+    get(c.decay_backward, "la_decay_backward");
+    get(c.qk_rotate_forward, "la_qk_rotate_forward");
+    get(c.qk_rotate_workspace_bytes, "la_qk_rotate_workspace_bytes");
+    get(c.qk_rotate_backward, "la_qk_rotate_backward");
     calls = c;
     Py_RETURN_NONE;
 }
@@ -439,6 +653,11 @@ PyMethodDef methods[] = {ENTRY(use, 1),
                          ENTRY(layernorm_forward, 11),
                          ENTRY(layernorm_backward, 10),
                          ENTRY(grad, 5),
+                         ENTRY(decay_forward, 11),
+                         ENTRY(decay_step, 8),
+                         ENTRY(decay_backward, 14),
+                         ENTRY(qk_rotate_forward, 13),
+                         ENTRY(qk_rotate_backward, 17),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_la_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -39,12 +39,15 @@ EXPORTED = ("la_workspace_bytes", "la_forward_noncausal", "la_forward_causal", "
             "la_debug_inject_bounds", "la_recurrence_workspace_bytes",
             "la_recurrence_forward", "la_recurrence_step",
             "la_recurrence_backward", "la_layernorm_forward", "la_layernorm_workspace_bytes",
-            "la_layernorm_backward", "la_grad_workspace_bytes", "la_grad_norm", "la_grad_clip")
+            "la_layernorm_backward", "la_grad_workspace_bytes", "la_grad_norm", "la_grad_clip",
+            "la_decay_forward", "la_decay_workspace_bytes", "la_decay_step", "la_decay_backward",
+            "la_qk_rotate_forward", "la_qk_rotate_workspace_bytes", "la_qk_rotate_backward")
 
 LA_FM = {"elu1": 0, "dpfp": 1, "poly2": 2}
 LA_NORM = {"den": 0, "sum": 1, "none": 2}
 LA_UPDATE = {"sum": 0, "delta": 1}
 LA_GATE = {"decay": 0, "log": 1, "sigmoid": 2}
+LA_PAIRS = {"half": 0, "adjacent": 1}
 
 
 class LAError(RuntimeError):
@@ -75,6 +78,17 @@ class la_rows(ctypes.Structure):
 class la_tensor(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_longlong),
                 ("dtype", ctypes.c_int)]
+
+
+class la_rotation(ctypes.Structure):
+    _fields_ = [("pos", ctypes.c_void_p), ("sa", ctypes.c_longlong), ("sb", ctypes.c_longlong),
+                ("sn", ctypes.c_longlong), ("freq", ctypes.c_void_p), ("axes", ctypes.c_char_p), ("A", ctypes.c_int),
+                ("P", ctypes.c_int), ("pairs", ctypes.c_int)]
+
+
+class la_qk_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("N", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("D", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 def variant(fm: str = "elu1", nu: int = 1, norm: str = "den", update: str = "sum") -> la_variant:
@@ -173,6 +187,20 @@ def _load(path: str) -> ctypes.CDLL:
         L.la_grad_norm.argtypes = [vp, i, vp, vp, sz, vp]
         L.la_grad_clip.restype = i
         L.la_grad_clip.argtypes = [vp, i, f, vp, vp, sz, vp]
+        L.la_decay_forward.restype = i
+        L.la_decay_forward.argtypes = [la_view] * 4 + [vp, vp, la_shape, f, vp, vp, vp, sz, vp]
+        L.la_decay_workspace_bytes.restype = sz
+        L.la_decay_workspace_bytes.argtypes = [la_shape, i]
+        L.la_decay_step.restype = i
+        L.la_decay_step.argtypes = [la_view] * 4 + [vp, la_shape, f, vp, vp]
+        L.la_decay_backward.restype = i
+        L.la_decay_backward.argtypes = [la_view] * 7 + [vp, vp, la_shape, f, vp, vp, vp, vp, sz, vp]
+        L.la_qk_rotate_forward.restype = i
+        L.la_qk_rotate_forward.argtypes = [la_view] * 4 + [vp, vp, la_rotation, la_qk_shape, i, f, vp]
+        L.la_qk_rotate_workspace_bytes.restype = sz
+        L.la_qk_rotate_workspace_bytes.argtypes = [la_qk_shape]
+        L.la_qk_rotate_backward.restype = i
+        L.la_qk_rotate_backward.argtypes = [la_view] * 6 + [vp, vp, la_rotation, la_qk_shape, i, f, vp, vp, vp, sz, vp]
         _loaded[path] = L
     return L
 
@@ -548,6 +576,79 @@ def la_grad_clip(grads, max_norm, out=None, norm=None, stream=None):
     st, norm = _bound().grad(grads, float(max_norm), out, norm, _handle(stream))
     _check(st, "la_grad_clip")
     return norm
+
+
+def la_decay_forward(q, k, v, log_decay, scale=1.0, S0=None, SN=None, lens=None, out=None, want_out=True, stream=None):
+    """Linear attention with a decay for each head: S_i = e^g S_{i-1} + k_i v_i^T,
+    out_i = scale q_i^T S_i, g = log_decay[h].
+
+    q, k: [B,H,N,D], v: [B,H,N,M], any strides but the channels'; log_decay: fp32
+    [H], at most 0 for states that do not grow.  S0, SN: fp32 [B,H,D,M], the
+    state before the first token and after the last; SN may be S0.  lens: int32
+    [B]; rows past a length are 0.  want_out=False: the state alone (q may be
+    None).  Returns out."""
+    st, out = _bound().decay_forward(q, k, v, log_decay, scale, S0, SN, lens, out, want_out, _handle(stream))
+    _check(st, "la_decay_forward")
+    return out
+
+
+def la_decay_step(q, k, v, S, log_decay, scale=1.0, y=None, stream=None):
+    """One token: q, k [B,H,D], v [B,H,M]; S the fp32 state [B,H,D,M], updated in
+    place.  Returns y = scale q^T S in v's type."""
+    st, y = _bound().decay_step(q, k, v, S, log_decay, scale, y, _handle(stream))
+    _check(st, "la_decay_step")
+    return y
+
+
+def la_decay_backward(q, k, v, dout, log_decay, scale=1.0, S0=None, dSN=None, dS0=None, lens=None, dq=None, dk=None,
+                      dv=None, stream=None):
+    """Gradients (dq, dk, dv) of la_decay_forward given dout = dL/dout.  S0, lens:
+    as given to the forward; dSN: gradient of its SN; dS0 (fp32, written):
+    gradient of S0.  log_decay gets none."""
+    st, dq, dk, dv = _bound().decay_backward(q, k, v, dout, log_decay, scale, S0, dSN, dS0, lens, dq, dk, dv,
+                                             _handle(stream))
+    _check(st, "la_decay_backward")
+    return dq, dk, dv
+
+
+def _pairs_code(pairs: str) -> int:
+    code = LA_PAIRS.get(pairs)
+    if code is None:
+        raise ValueError("pairs must be one of %s" % ", ".join(LA_PAIRS))
+    return code
+
+
+def _axes_bytes(axes):
+    return None if axes is None else bytes(axes)
+
+
+def la_qk_rotate_forward(q, k, pos, freq, wq=None, wk=None, eps=1e-6, norm=True, pairs="half", axes=None, qo=None,
+                         ko=None, stream=None):
+    """RMS norm of every head of q [B,Hq,N,D] and k [B,Hk,N,D] (or None) and the
+    rotation of its first 2 P channels by the angles position * freq, P =
+    len(freq), in one pass.
+
+    pos: int32 [N], [B,N] or [A,B,N] (A axes, as time, height and width); freq:
+    fp32 [P]; axes: the axis of each of the P pairs (None: all on the first).
+    pairs: "half" (channels i and i + P) or "adjacent" (2i and 2i + 1).  wq, wk:
+    fp32 [D] or None (1); norm=False: the rotation alone.  qo may be q, ko may be
+    k.  Returns (qo, ko)."""
+    st, qo, ko = _bound().qk_rotate_forward(q, k, pos, freq, wq, wk, eps, bool(norm), _pairs_code(pairs),
+                                            _axes_bytes(axes), qo, ko, _handle(stream))
+    _check(st, "la_qk_rotate_forward")
+    return qo, ko
+
+
+def la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq=None, wk=None, eps=1e-6, norm=True, pairs="half", axes=None,
+                          dq=None, dk=None, dwq=None, dwk=None, stream=None):
+    """Gradients (dq, dk, dwq, dwk) of la_qk_rotate_forward given dqo, dko and its
+    own inputs; dwq, dwk (fp32 [D]) are None with norm=False, dk and dwk without
+    keys.  dq may be dqo, dk may be dko."""
+    st, dq, dk, dwq, dwk = _bound().qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk, eps, bool(norm),
+                                                       _pairs_code(pairs), _axes_bytes(axes), dq, dk, dwq, dwk,
+                                                       _handle(stream))
+    _check(st, "la_qk_rotate_backward")
+    return dq, dk, dwq, dwk
 
 
 def la_get_last_error(stream=None, device=None) -> int:
