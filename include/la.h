@@ -494,7 +494,11 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
  *   workspace: la_decay_workspace_bytes(s, 0) bytes.
  * A token's NaN and infinities make what sees them not finite, as token by
  * token does; rows that do not see it are what they are without it.
- * All arithmetic is fp32; out is rounded once.
+ * bf16 rows on 16-byte boundaries (base and strides) run on tensor cores,
+ * their outputs the sums of bf16 products with the masked scores and the state
+ * rounded to bf16 once; the state itself takes the products of the rows as
+ * they are, its weights by three bf16 parts, in fp32.  fp32 data, and bf16
+ * off those boundaries, run fp32 arithmetic.
  */
 la_status la_decay_forward(la_view q, la_view k, la_view v, la_view out, const float *log_decay, const int *lens,
                            la_shape s, float scale, const float *S0, float *SN, void *workspace, size_t ws_bytes,

@@ -284,6 +284,7 @@ template <typename T> cudaError_t simt_decay(const DecayLaunch &l) {
 }
 
 cudaError_t run(const DecayLaunch &l, la_dtype dtype) {
+    if (tc_decay_supported(l, dtype)) return tc_decay(l);
     return dtype == LA_DTYPE_F32 ? simt_decay<float>(l) : simt_decay<__nv_bfloat16>(l);
 }
 

@@ -58,4 +58,8 @@ struct DecayLaunch {
     cudaStream_t stream;
 };
 
+// tensor cores (la_tc_decay.cu): bf16 rows on 16 byte boundaries
+bool tc_decay_supported(const DecayLaunch &l, la_dtype dtype);
+cudaError_t tc_decay(const DecayLaunch &l);
+
 }  // namespace la
