@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads) sweep_kernel(const DecayLaunch l) {
     float *S = sm, *X = S + D * kCols, *Y = X + kRows * ld, *Z = Y + kRows * ld, *A = Z + kRows * kCols;
     float *w = A + kRows * (kRows + 1);   // decays by 0..kRows tokens
     const int seg = blockIdx.x % l.segs, bh = blockIdx.x / l.segs, b = bh / l.H, h = bh % l.H, tid = threadIdx.x;
+    if (l.sums && seg == (s.backwards ? 0 : l.segs - 1)) return;   // nobody asks for that one
     const float g = l.log_decay[h];
     const int len = l.lens ? max(0, min(l.N, l.lens[b])) : l.N;
     const int first = seg * l.seg_tokens;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(256) scan_kernel(float *ws, const float *start
 #pragma unroll 4
     for (int i = 0; i < segs; i++) {
         const int seg = backwards ? segs - 1 - i : i;
-        const float sum = p[(size_t)seg * DM];
+        const float sum = i < segs - 1 ? p[(size_t)seg * DM] : 0.f;   // no state comes after the last one
         p[(size_t)seg * DM] = s;
         if (seg <= last) s = keep(seg == last ? part : whole, s) + sum;
     }
@@ -249,26 +250,36 @@ template <typename T> cudaError_t step(const DecayProblem &p) {
 
 // ------------------------------------------------------------- segments
 
-// Segments of a sequence: about two CTAs an SM where heads alone are fewer.
-int segments(int B, int H, int N, int blocks) {
-    const long long ctas = (long long)B * H * blocks;
-    const long long most = (N + 127) / 128;
-    if (ctas >= kSms || most < 2) return 1;
-    return (int)std::max(1LL, std::min(most, kSms / ctas));
-}
-
 struct Cut {
     int segs, tokens;
 };
-Cut cut_of(int B, int H, int N, int blocks) {
-    const int want = segments(B, H, N, blocks);
-    if (want == 1) return {1, std::max(N, 1)};
-    const int chunks = (N + 127) / 128, per = (chunks + want - 1) / want;
-    return {(chunks + per - 1) / per, per * 128};
+
+// Segments of a sequence.  `ctas` walk over the whole sequences side by side, one to
+// an SM; cut, there are `segs` times as many, which have first to find the states at
+// their starts: `sums` CTAs a segment, then a scan that moves `states` bytes a segment.
+// In chunks of 128 tokens (about 2.1 us): a CTA's start and end cost six, a chunk's sums
+// 0.9, a scan's launch two.  16 heads of 65536 tokens, D = M = 128: 4 segments 519 us,
+// 19 566; 16 heads of 16384, backward: 1 segment 278 us, 3 303.
+Cut cut_of(long long ctas, long long sums, double states, int N) {
+    const long long chunks = ((long long)N + 127) / 128;
+    long long best = 1;
+    double least = 0;
+    for (long long segs = 1; segs <= std::min<long long>(chunks, 4 * kSms) && (segs == 1 || ctas * segs <= 4 * kSms); segs++) {
+        const long long per = (chunks + segs - 1) / segs;
+        if (segs > 1 && (chunks + per - 1) / per != segs) continue;   // the same as fewer
+        auto waves = [&](long long n) { return (n + kSms - 1) / kSms; };
+        double cost = waves(ctas * segs) * (per + 6.0);
+        if (segs > 1) cost += waves(sums * (segs - 1)) * (0.9 * per + 6) + 2 + segs * states / (6.5e6 * 2.1);
+        if (segs == 1 || cost < least) best = segs, least = cost;
+    }
+    const long long per = (chunks + best - 1) / best;
+    return {(int)best, best == 1 ? std::max(N, 1) : (int)(per * 128)};
 }
 int blocks_of(int w) { return (w + kCols - 1) / kCols; }
 Cut cut_of(int B, int H, int N, int D, int M, bool backward) {
-    return cut_of(B, H, N, backward ? blocks_of(D) * 2 + blocks_of(M) : blocks_of(M));
+    const long long heads = (long long)B * H, d = blocks_of(D), m = blocks_of(M);
+    const double states = 16.0 * heads * D * M;   // written, scanned, read
+    return backward ? cut_of(heads * (2 * d + m), heads * 2 * m, 2 * states, N) : cut_of(heads * m, heads * m, states, N);
 }
 
 template <typename T> cudaError_t simt_decay(const DecayLaunch &l) {

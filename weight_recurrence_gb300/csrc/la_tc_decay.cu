@@ -14,16 +14,18 @@
 // as a^i a^-j, which overflows.  The score and the state (as an operand) are
 // each rounded to bf16 once; the state itself stays in fp32 registers, and the
 // rows that enter it are exact: y as it came, a^(n-1-j) z_j as three bf16 parts
-// (8 bits each), so that a state carried over thousands of tokens is as good
+// of 8 bits each (two where no state leaves), so that a state carried over thousands of tokens is as good
 // as fp32 sums.
 //
-// Masked places hold zeros, but 0 times a z_j that is not finite is NaN: a chunk
-// whose z holds such a value computes A z row by row from the tiles instead.
+// Masked places hold zeros, but 0 times a z_j that is not finite is NaN.  Such
+// values are taken out of z (not out of the parts that enter the state), and the
+// outputs that see them are made NaN.
 //
-// Roles (512 threads): warp 0 loads (TMA), warps 1-3 issue the MMAs of P, of the
-// outputs and of the state's increments, 4-7 decay and mask the scores, 8-11
-// weigh z, 12-15 keep the state and write the outputs.  Tiles are 128-byte
-// swizzled; every wait is bounded.
+// Roles (640 threads): warp 0 loads (TMA); warps 1-3 issue the MMAs of P, of the
+// outputs and of the state's increments.  Two groups of four warps (4-11) decay and
+// mask the scores and make the output rows, each for half of the columns; two more
+// (12-19) weigh z and keep the state, likewise.  Tiles are 128-byte swizzled; every
+// wait is bounded.
 #include <algorithm>
 
 #include "la_common.cuh"
@@ -39,11 +41,12 @@ namespace {
 using namespace tc;
 
 constexpr int kMB = 64;                    // columns of z that a CTA takes
-constexpr int kDecayThreads = 512;
+constexpr int kDecayThreads = 640;
 constexpr int kTile = kC * 128;            // 128 rows of 64 bf16 values
 
 struct TcSweep {
-    CUtensorMap x, y, z, out;
+    CUtensorMap x, y, z;
+    la_view rows;                          // the output's
     const float *start;
     float *end;
     int D, M, blocks;                      // blocks of kMB columns
@@ -61,28 +64,36 @@ struct TcDecayArgs {
 
 template <int DP> struct DecayCfg {
     static constexpr int SUB = DP / 64;                 // 64-column sub-tiles of x and y
-    static constexpr int STAGE = (2 * SUB + 1) * kTile;
-    static constexpr int NS = DP == 64 ? 3 : 2;
+    static constexpr int NS = DP == 64 ? 3 : 2;         // chunks whose tiles are held
     static constexpr int NSNAP = DP == 64 ? 2 : 1;      // state snapshots that fit
     static constexpr int SNAP = DP * 128;
-    static constexpr int OFF_ZW = NS * STAGE;           // three parts of the weighted z
+    static constexpr int OFF_X = 0;
+    static constexpr int OFF_Y = OFF_X + NS * SUB * kTile;
+    static constexpr int OFF_Z = OFF_Y + NS * SUB * kTile;
+    static constexpr int OFF_ZW = OFF_Z + NS * kTile;   // three parts of the weighted z
     static constexpr int OFF_SNAP = OFF_ZW + 3 * kTile;
     static constexpr int OFF_TAB = OFF_SNAP + NSNAP * SNAP;
-    // a^-32..a^128 (0 below 0), then a block's column factors
-    static constexpr int TAB = 32 + kC + 4;
-    static constexpr int OFF_COL = OFF_TAB + TAB * 4 + (16 - TAB * 4 % 16) % 16;
-    static constexpr int OFF_FLAG = OFF_COL + 32 * 4;   // [4 chunks][4 warps]: z not finite
-    static constexpr int NBARS = 2 * NS + 2 * 5 + 1 + 1 + 2 * 2 + 2 + 1;
-    static constexpr int OFF_BAR = OFF_FLAG + 64;
+    // decays by 0..128 tokens, then the factors of a block's columns, then those of a
+    // block on the diagonal by column - row, from -31 on
+    static constexpr int TAB = kC + 4;
+    static constexpr int OFF_COL = OFF_TAB + TAB * 4;
+    static constexpr int OFF_DIAG = OFF_COL + 32 * 4;
+    // chunks whose record of values of z that are not finite is held: chunk j's is
+    // written again for chunk j + NBAD, which needs z's tile of chunk j + NBAD - NS, so
+    // that chunk's A z and the output rows of the chunk before it
+    static constexpr int NBAD = 4;
+    static constexpr int OFF_FLAG = OFF_DIAG + 64 * 4;     // [NBAD][2 halves][8 warps]
+    static constexpr int OFF_BAD = OFF_FLAG + NBAD * 64;   // [NBAD][2][8][16 columns]: first or last row, a byte
+    static constexpr int OFF_BAR = OFF_BAD + NBAD * 256;
+    static constexpr int NBARS = 6 * NS + 5 * 2 + 4 + 1 + 4 + 2 + 1;
     static constexpr int OFF_TSLOT = OFF_BAR + 8 * NBARS;
     static constexpr int SMEM = OFF_TSLOT + 16;
-    static_assert(OFF_BAR % 8 == 0 && SMEM <= (int)kSmemMax, "shared memory budget");
-    // TMEM: two buffers of P (128 columns; then A as bf16 in the first 64, A z in
-    // the others) and x S (64); two increments of the state (64)
-    static __device__ __forceinline__ uint32_t col_p(int b) { return 192u * b; }
-    static __device__ __forceinline__ uint32_t col_az(int b) { return 192u * b + 64u; }
-    static __device__ __forceinline__ uint32_t col_xs(int b) { return 192u * b + 128u; }
-    static __device__ __forceinline__ uint32_t col_ds(int b) { return 384u + 64u * b; }
+    static_assert(NBAD > NS && OFF_BAR % 8 == 0 && SMEM <= (int)kSmemMax, "shared memory budget");
+    // TMEM: two buffers of P (128 columns; the scores as bf16 take the first half of
+    // each 64), x S and A z (64 each), and the increment of the state by the first part
+    // of z and by the others (64 each)
+    static __device__ __forceinline__ uint32_t col_p(int b) { return 128u * b; }
+    static constexpr uint32_t COL_XS = 256, COL_AZ = 320, COL_DS = 384;
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, uint64_t *bar, int x, int t, int h, int b) {
@@ -92,60 +103,126 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, uint64_
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(t), "r"(h), "r"(b), "r"(smem_u32(bar))
         : "memory");
 }
-__device__ __forceinline__ void tma_store_4d(const void *tmap, const void *src, int x, int t, int h, int b) {
-    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(tmap)),
-                 "r"(smem_u32(src)), "r"(x), "r"(t), "r"(h), "r"(b)
+// 32 lanes x 32 bit, 8 consecutive columns a thread.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
-__device__ __forceinline__ void state_sync() { asm volatile("bar.sync 2, 128;" ::: "memory"); }
-
-// The output row of a chunk whose z is not finite: A z from the tiles, without
-// the rows that the mask hides, and x S from TMEM (xs); the row goes where its x
-// lay, after its last read of it.  Whole warps call it.
-template <int DP>
-__device__ __noinline__ void row_by_hand(uint8_t *xt, const uint8_t *yt, const uint8_t *zt, const float *w, uint32_t xs,
-                                         int r, int rows, bool backwards, float intra, float inter) {
-    uint32_t out[kMB / 2];
-    const int j0 = backwards ? r : 0, j1 = r >= rows ? j0 : backwards ? rows : r + 1;
-    for (int c0 = 0; c0 < kMB; c0 += 16) {
-        float o[16];
-        for (int i = 0; i < 16; i++) o[i] = 0.f;
-        for (int j = j0; j < j1; j++) {
-            float p = 0.f;
-            for (int c = 0; c < DP; c += 2) {
-                const uint32_t off = (c / 64) * kTile;
-                const uint32_t a = *reinterpret_cast<const uint32_t *>(xt + off + sw128_offset(r, c % 64));
-                const uint32_t b = *reinterpret_cast<const uint32_t *>(yt + off + sw128_offset(j, c % 64));
-                p = fmaf(bf16lo(a), bf16lo(b), fmaf(bf16hi(a), bf16hi(b), p));
-            }
-            p = __bfloat162float(__float2bfloat16_rn(p * w[backwards ? j - r : r - j]));
-            for (int i = 0; i < 16; i += 2) {
-                const uint32_t z = *reinterpret_cast<const uint32_t *>(zt + sw128_offset(j, c0 + i));
-                o[i] = fmaf(p, bf16lo(z), o[i]);
-                o[i + 1] = fmaf(p, bf16hi(z), o[i + 1]);
-            }
-        }
-        __syncwarp();
-        uint32_t x[16];
-        tmem_ld16(xs + c0, x);
-        tmem_wait_ld();
-        for (int i = 0; i < 8; i++)
-            out[c0 / 2 + i] = r < rows ? pack_bf16x2(fmaf(intra, o[2 * i], inter * __uint_as_float(x[2 * i])),
-                                                     fmaf(intra, o[2 * i + 1], inter * __uint_as_float(x[2 * i + 1])))
-                                       : 0u;
+// A wait that sleeps in the barrier's hardware for up to about 20 us at a time: polls
+// without the time hint came back at once, and those of a dozen waiting warps were
+// three of four instructions that an SM issued (5000 -> 3500 clocks a chunk without
+// them).  Out of line but for the first try: the roles share one instruction cache.
+__device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    const uint64_t deadline = now_ns() + kWaitNs;
+    while (!*abort) {
+        if (try_wait_long(bar, parity)) return true;
+        if (now_ns() > deadline) *abort = 1;
     }
-    for (int c = 0; c < kMB; c += 8)
-        *reinterpret_cast<uint4 *>(xt + sw128_offset(r, c)) =
-            make_uint4(out[c / 2], out[c / 2 + 1], out[c / 2 + 2], out[c / 2 + 3]);
+    return false;
+}
+// As wait_bar and wait_bar_warp; a role that gave up raises the abort flag for the others.
+__device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, wait_one(bar, parity, abort));
+}
+
+// True in one lane of a converged warp.  The MMAs are issued under it by warps that
+// walk through their loops as a whole: descriptors then stay in uniform registers
+// and an MMA goes out every few clocks; issued by a lane that runs alone, each took 97.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// One arrival for a warp, whose lanes have each done what it stands for (and their
+// fences).
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float2 pair_at(const uint32_t (&v)[16], int i) {
+    return make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+}
+
+// The upper halves of two fp32 values: bf16, cut off.
+__device__ __forceinline__ uint32_t top_pair(float2 v) {
+    return __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x7632);
+}
+
+// Rows of z (16 columns from c0 on) with values that are not finite (any lane of the
+// warp has one): they become zeros in the tile, and the warp notes for every column its
+// first (backwards: last) row that had one, 255 (0: row + 1) for none.
+__device__ __noinline__ void take_out(uint8_t *zt, int r, int c0, uint8_t *note, bool backwards) {
+    const int lane = threadIdx.x & 31;
+    for (int c = 0; c < 16; ++c) {
+        uint16_t *p = reinterpret_cast<uint16_t *>(zt + sw128_offset(r, c0 + c));
+        const bool bad = (*p & 0x7fffu) >= 0x7f80u;
+        if (bad) *p = 0;
+        const uint32_t who = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) {
+            const int row = r + (backwards ? 31 - __clz(who) : __ffs(who) - 1);
+            note[c] = who == 0u ? (backwards ? 0 : 255) : backwards ? row + 1 : row;
+        }
+    }
+}
+
+// Which of the columns 32 grp..32 grp + 31 of row r see one of them; note: [2][8][16],
+// flag: [2][8].  Warps 2q and 2q + 1 wrote columns 16q..16q + 15.
+__device__ __noinline__ uint32_t seen_bad(int r, int grp, const uint8_t *note, const volatile int *flag, bool backwards) {
+    uint32_t hit = 0u;
+    for (int i = 0; i < 16; ++i) {
+        const int q = (i & 7) >> 1;
+        if (!flag[i] || q >> 1 != grp) continue;
+        for (int c = 0; c < 16; ++c)
+            if (backwards ? note[i * 16 + c] > r : note[i * 16 + c] <= r) hit |= 1u << (16 * (q & 1) + c);
+    }
+    return hit;
+}
+
+// 16 output values to a row on 16 bytes, `cols` of them.
+__device__ __noinline__ void store_some(__nv_bfloat16 *row, uint4 a, uint4 b, int cols) {
+    for (int i = 0; i < min(cols, 16); i += 8) {
+        const uint4 v = i == 0 ? a : b;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t pair = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
+            if (i + j < cols) reinterpret_cast<uint16_t *>(row)[i + j] = (uint16_t)(j & 1 ? pair >> 16 : pair);
+        }
+    }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16 *row, uint4 a, uint4 b, int cols) {
+    if (cols < 16) {
+        store_some(row, a, b, cols);
+    } else if ((reinterpret_cast<uintptr_t>(row) & 31) == 0) {   // a whole 32-byte sector
+        st_global_v8(row, a, b);
+    } else {
+        reinterpret_cast<uint4 *>(row)[0] = a;
+        reinterpret_cast<uint4 *>(row)[1] = b;
+    }
 }
 
 template <int DP>
 __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid_constant__ TcDecayArgs args) {
     using C = DecayCfg<DP>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     volatile int *abort = reinterpret_cast<volatile int *>(smem + C::OFF_TSLOT + 4);
     // neighbouring CTAs share their rows: column blocks and sweeps first, then segments, then heads
     int blk = blockIdx.x % args.blocks, k = 0;
@@ -154,38 +231,58 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
     const int rest = blockIdx.x / args.blocks, seg = rest % args.segs, bh = rest / args.segs;
     const int h = bh % args.H, b = bh / args.H, m0 = blk * kMB;
     const bool backwards = sw.backwards != 0, out = sw.has_out != 0;
+    if (args.sums && seg == (backwards ? 0 : args.segs - 1)) {   // nobody asks for that one
+        pdl_wait();
+        return;
+    }
+    // a state that leaves is exact; one that bf16 outputs alone see takes two parts of z
+    const int parts = sw.end != nullptr ? 3 : 2;
 
+    constexpr int kPair = 8;   // warps of a pair of groups
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *full = bar, *empty = full + C::NS, *p_full = empty + C::NS, *a_ready = p_full + 2, *xs_full = a_ready + 2,
-             *o_full = xs_full + 2, *o_free = o_full + 2, *zw_ready = o_free + 2, *tail_ready = zw_ready + 1,
-             *ds_full = tail_ready + 1, *ds_free = ds_full + 2, *snap_ready = ds_free + 2, *drain = snap_ready + 2;
+    uint64_t *x_full = bar, *x_empty = x_full + C::NS, *y_full = x_empty + C::NS, *y_empty = y_full + C::NS,
+             *z_full = y_empty + C::NS, *z_empty = z_full + C::NS;
+    uint64_t *p_full = z_empty + C::NS, *a_ready = p_full + 2, *xs_full = a_ready + 2, *o_full = xs_full + 2,
+             *o_free = o_full + 2, *zw_ready = o_free + 2, *tail_ready = zw_ready + 4, *half_ready = tail_ready + 1,
+             *half_free = half_ready + 1, *ds_full = half_free + 1, *ds_free = ds_full + 1, *snap_ready = ds_free + 1,
+             *drain = snap_ready + 2;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + C::OFF_TSLOT);
-    float *w = reinterpret_cast<float *>(smem + C::OFF_TAB) + 32, *colf = reinterpret_cast<float *>(smem + C::OFF_COL);
+    float *w = reinterpret_cast<float *>(smem + C::OFF_TAB), *colf = reinterpret_cast<float *>(smem + C::OFF_COL);
+    float *diag = reinterpret_cast<float *>(smem + C::OFF_DIAG) + 31;
     volatile int *flag = reinterpret_cast<volatile int *>(smem + C::OFF_FLAG);
     uint8_t *zw = smem + C::OFF_ZW;
     auto snap = [&](int j) { return smem + C::OFF_SNAP + (j % C::NSNAP) * C::SNAP; };
-    auto stage = [&](int it) { return smem + (it % C::NS) * C::STAGE; };
-    constexpr int OFF_Y = C::SUB * kTile, OFF_Z = 2 * C::SUB * kTile;
+    auto xtile = [&](int it) { return smem + C::OFF_X + (it % C::NS) * C::SUB * kTile; };
+    auto ytile = [&](int it) { return smem + C::OFF_Y + (it % C::NS) * C::SUB * kTile; };
+    auto ztile = [&](int it) { return smem + C::OFF_Z + (it % C::NS) * kTile; };
 
     pdl_launch_dependents();
     if (tid == 0) {
         *abort = (smem_u32(smem) & 1023u) ? 1 : 0;   // the swizzled layouts need a 1024-byte aligned base
         for (int s = 0; s < C::NS; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], out ? 3 : 1);       // increment MMAs; output MMAs; output rows stored
+            mbar_init(&x_full[s], 1);
+            mbar_init(&x_empty[s], 2);               // MMAs of P and of x S
+            mbar_init(&y_full[s], 1);
+            mbar_init(&y_empty[s], out ? 2 : 1);     // of the increment and of P
+            mbar_init(&z_full[s], 1);
+            mbar_init(&z_empty[s], out ? 2 : 1);     // of the increment and of A z
         }
+        // where a waiter may be a chunk behind, a barrier for each of two (or four, for
+        // the weighed z: up to NS chunks) chunks, so that none is two phases ahead of it
         for (int i = 0; i < 2; ++i) {
             mbar_init(&p_full[i], 1);
-            mbar_init(&a_ready[i], kGrp);
+            mbar_init(&a_ready[i], kPair);
             mbar_init(&xs_full[i], 1);
             mbar_init(&o_full[i], 1);
-            mbar_init(&o_free[i], kGrp);
-            mbar_init(&ds_full[i], 1);
-            mbar_init(&ds_free[i], kGrp);
-            mbar_init(&snap_ready[i], kGrp);
+            mbar_init(&o_free[i], kPair);
+            mbar_init(&snap_ready[i], kPair);
         }
-        mbar_init(zw_ready, kGrp);
-        mbar_init(tail_ready, kGrp);
+        for (int i = 0; i < 4; ++i) mbar_init(&zw_ready[i], kPair);
+        mbar_init(half_ready, kPair);
+        mbar_init(half_free, 1);
+        mbar_init(ds_full, 1);
+        mbar_init(ds_free, kPair);
+        mbar_init(tail_ready, kPair);
         mbar_init(drain, 3);
         fence_mbar_init();
     }
@@ -193,237 +290,292 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
+    if (tid == 32) {
+        prefetch_tmap(&sw.y);
+        prefetch_tmap(&sw.z);
+        if (out) prefetch_tmap(&sw.x);
+    }
     tc_fence_before();
     pdl_wait_cta();   // from here on the previous launch's writes are visible
     tc_fence_after();
-    const uint32_t tmem = *tslot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);
 
     const float g = args.log_decay[h];
     const int len = args.lens ? max(0, min(args.N, args.lens[b])) : args.N;
     const int first = seg * args.seg_tokens;
-    const int tokens = max(0, min(len - first, args.seg_tokens));
+    const int tokens = __shfl_sync(0xffffffffu, max(0, min(len - first, args.seg_tokens)), 0);
     const int n = (tokens + kC - 1) / kC;                       // chunks
     const int tail = tokens - (n - 1) * kC;                     // tokens of the last one
     auto chunk_of = [&](int it) { return backwards ? n - 1 - it : it; };
     auto rows_of = [&](int it) { return chunk_of(it) == n - 1 ? tail : kC; };
-    for (int i = tid; i < C::TAB; i += kDecayThreads) {
-        const int e = i - 32;   // a^0 is 1 also where g is -infinity
-        w[e] = e < 0 ? 0.f : e == 0 ? 1.f : expf(g * (float)e);
+    auto decayed = [&](int e) { return e == 0 ? 1.f : expf(g * (float)e); };   // a^0 is 1 also where g is -infinity
+    // warp 0 goes on to the loads
+    if (tid >= 32 && tid <= 32 + kC) w[tid - 32] = decayed(tid - 32);
+    else if (tid >= 192 && tid < 224) colf[tid - 192] = decayed(backwards ? tid - 192 : 223 - tid);
+    else if (tid >= 224 && tid < 288) {
+        const int e = backwards ? tid - 224 - 31 : 31 - (tid - 224);   // hidden places: 0
+        diag[tid - 224 - 31] = e < 0 ? 0.f : decayed(e);
     }
-    if (tid < 32) {
-        const int e = backwards ? tid : 31 - tid;
-        colf[tid] = e == 0 ? 1.f : expf(g * (float)e);
-    }
-    __syncthreads();
+    if (warp > 0) asm volatile("bar.sync 2, 608;" ::: "memory");
 
     if (warp == 0) {
-        // ------------------------------------------------------ producer
+        // ------------------------------------------------------ loads
         if (lane == 0 && !*abort) {
-            prefetch_tmap(&sw.y);
-            prefetch_tmap(&sw.z);
-            if (out) prefetch_tmap(&sw.x);
-            int issued = 0;
+            int ny = 0, nx = 0, nz = 0;
             for (int it = 0; it < n; ++it) {
-                const int s = it % C::NS;
-                if (it >= C::NS && !wait_bar(&empty[s], (it / C::NS - 1) & 1, abort)) break;
-                uint8_t *st = stage(it);
-                const int t0 = first + chunk_of(it) * kC;
-                mbar_arrive_expect_tx(&full[s], ((out ? 2 : 1) * C::SUB + 1) * kTile);
+                const int s = it % C::NS, t0 = first + chunk_of(it) * kC;
+                const uint32_t again = (it / C::NS - 1) & 1;
+                if (it >= C::NS && !wait_one(&y_empty[s], again, abort)) break;
+                mbar_arrive_expect_tx(&y_full[s], C::SUB * kTile);
 #pragma unroll
-                for (int j = 0; j < C::SUB; ++j) {
-                    if (out) tma_load_4d(st + j * kTile, &sw.x, &full[s], j * 64, t0, h, b);
-                    tma_load_4d(st + OFF_Y + j * kTile, &sw.y, &full[s], j * 64, t0, h, b);
+                for (int j = 0; j < C::SUB; ++j) tma_load_4d(ytile(it) + j * kTile, &sw.y, &y_full[s], j * 64, t0, h, b);
+                ++ny;
+                if (out) {
+                    if (it >= C::NS && !wait_one(&x_empty[s], again, abort)) break;
+                    mbar_arrive_expect_tx(&x_full[s], C::SUB * kTile);
+#pragma unroll
+                    for (int j = 0; j < C::SUB; ++j)
+                        tma_load_4d(xtile(it) + j * kTile, &sw.x, &x_full[s], j * 64, t0, h, b);
+                    ++nx;
                 }
-                tma_load_4d(st + OFF_Z, &sw.z, &full[s], m0, t0, h, b);
-                ++issued;
+                if (it >= C::NS && !wait_one(&z_empty[s], again, abort)) break;
+                mbar_arrive_expect_tx(&z_full[s], kTile);
+                tma_load_4d(ztile(it), &sw.z, &z_full[s], m0, t0, h, b);
+                ++nz;
             }
-            if (*abort)   // let the copies in flight land before the CTA exits
-                for (int it = max(0, issued - C::NS); it < issued; ++it)
-                    mbar_wait_bounded(&full[it % C::NS], (it / C::NS) & 1, now_ns() + kWaitNs, nullptr);
+            if (*abort) {   // let the copies in flight land before the CTA exits
+                auto land = [&](uint64_t *full, int issued) {
+                    for (int it = max(0, issued - C::NS); it < issued; ++it)
+                        mbar_wait_bounded(&full[it % C::NS], (it / C::NS) & 1, now_ns() + kWaitNs, nullptr);
+                };
+                land(y_full, ny);
+                land(x_full, nx);
+                land(z_full, nz);
+            }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ scores: P = x y^T
-        if (lane == 0 && !*abort && out) {
+        if (out) {
             constexpr uint32_t ID = idesc_bf16(128, kC, 0, 0);
             for (int it = 0; it < n; ++it) {
                 const int s = it % C::NS, pb = it & 1;
-                if (!wait_bar(&full[s], (it / C::NS) & 1, abort)) break;
-                if (rows_of(it) < kC && !wait_bar(tail_ready, 0, abort)) break;   // rows past the end are zeros now
-                if (it >= 2 && !wait_bar(&o_free[pb], (it / 2 - 1) & 1, abort)) break;
+                const uint32_t turn = (it / C::NS) & 1;
+                if (!wait_warp(&y_full[s], turn, abort) || !wait_warp(&x_full[s], turn, abort)) break;
+                if (rows_of(it) < kC && !wait_warp(tail_ready, 0, abort)) break;   // rows past the end are zeros now
+                // the scores of two chunks before were read
+                if (it >= 2 && !wait_warp(&o_full[pb], (it / 2 - 1) & 1, abort)) break;
                 tc_fence_after();
-                const uint32_t st = smem_u32(stage(it));
-                const uint64_t dx = kmajor_base(st), dy = kmajor_base(st + OFF_Y);
+                const uint64_t dx = kmajor_base(smem_u32(xtile(it))), dy = kmajor_base(smem_u32(ytile(it)));
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks)
-                    mma_f16_ss(tmem + C::col_p(pb), dx + kmajor_step(ks), dy + kmajor_step(ks), ID, ks > 0);
-                mma_commit(&p_full[pb]);
+                    for (int ks = 0; ks < DP / 16; ++ks)
+                        mma_f16_ss(tmem + C::col_p(pb), dx + kmajor_step(ks), dy + kmajor_step(ks), ID, ks > 0);
+                    mma_commit(&p_full[pb]);
+                    mma_commit(&x_empty[s]);
+                    mma_commit(&y_empty[s]);
+                }
             }
         }
-        if (lane == 0) mma_commit(drain);
+        if (elect_one()) mma_commit(drain);
+    } else if (warp == 3) {
+        // ------------------------------------------------------ increments: y^T (weighted z)
+        {
+            constexpr uint32_t ID_TWO = idesc_bf16(128, 2 * kMB, 1, 1), ID_ONE = idesc_bf16(128, kMB, 1, 1);
+            for (int it = 0; it < n; ++it) {
+                const int s = it % C::NS;
+                if (!wait_warp(&y_full[s], (it / C::NS) & 1, abort)) break;
+                if (it >= 1 && !wait_warp(ds_free, (it - 1) & 1, abort)) break;
+                // y^T read MN-major; 64 columns wide it is repeated (M-atom stride 0), so
+                // that lanes 64-127 hold a second copy.  The first two parts of z side by
+                // side are one operand, so that y^T is read once for them; the third is
+                // added to the second's products.  By halves of the rows, so that the first
+                // half's parts can be written anew while the second's are multiplied
+                const uint64_t dy = smem_desc(smem_u32(ytile(it)), DP == 64 ? 0 : kTile, 1024);
+                const uint64_t dz = smem_desc(smem_u32(zw), kTile, 1024);
+                const uint64_t dl = smem_desc(smem_u32(zw) + 2 * kTile, 0, 1024);
+                bool ok = true;
+#pragma unroll 1
+                for (int k0 = 0; k0 < kC / 16 && ok; k0 += kC / 32) {
+                    ok = k0 == 0 ? wait_warp(half_ready, it & 1, abort) : wait_warp(&zw_ready[it & 3], (it >> 2) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < kC / 32; ++i) {
+                            const uint64_t step = mnmajor_step(1) * (uint64_t)(k0 + i);
+                            mma_f16_ss(tmem + C::COL_DS, dy + step, dz + step, ID_TWO, k0 + i > 0);
+                        }
+                        if (parts == 3)
+#pragma unroll
+                            for (int i = 0; i < kC / 32; ++i) {
+                                const uint64_t step = mnmajor_step(1) * (uint64_t)(k0 + i);
+                                mma_f16_ss(tmem + C::COL_DS + kMB, dy + step, dl + step, ID_ONE, 1);
+                            }
+                        if (k0 == 0) mma_commit(half_free);
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    mma_commit(ds_full);
+                    mma_commit(&y_empty[s]);
+                    mma_commit(&z_empty[s]);
+                }
+            }
+        }
+        if (elect_one()) mma_commit(drain);
     } else if (warp == 2) {
         // ------------------------------------------------------ outputs: x S, A z
-        if (lane == 0 && !*abort && out) {
+        if (out) {
             constexpr uint32_t ID = idesc_bf16(128, kMB, 0, 1);
             for (int it = 0; it < n; ++it) {
                 const int s = it % C::NS, pb = it & 1;
-                if (!wait_bar(&full[s], (it / C::NS) & 1, abort)) break;
-                if (!wait_bar(&snap_ready[it & 1], (it >> 1) & 1, abort)) break;
-                if (it >= 2 && !wait_bar(&o_free[pb], (it / 2 - 1) & 1, abort)) break;
+                if (!wait_warp(&x_full[s], (it / C::NS) & 1, abort)) break;
+                if (!wait_warp(&snap_ready[it & 1], (it >> 1) & 1, abort)) break;
+                // the output rows of the chunk before have read x S and A z
+                if (it >= 1 && !wait_warp(&o_free[(it - 1) & 1], ((it - 1) >> 1) & 1, abort)) break;
                 tc_fence_after();
-                const uint32_t st = smem_u32(stage(it));
-                const uint64_t dx = kmajor_base(st), ds = smem_desc(smem_u32(snap(it)), 0, 1024);
+                const uint64_t dx = kmajor_base(smem_u32(xtile(it))), ds = smem_desc(smem_u32(snap(it)), 0, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks)
-                    mma_f16_ss(tmem + C::col_xs(pb), dx + kmajor_step(ks), ds + mnmajor_step(ks), ID, ks > 0);
-                mma_commit(&xs_full[pb]);
-                if (!wait_bar(&a_ready[pb], (it >> 1) & 1, abort)) break;
+                    for (int ks = 0; ks < DP / 16; ++ks)
+                        mma_f16_ss(tmem + C::COL_XS, dx + kmajor_step(ks), ds + mnmajor_step(ks), ID, ks > 0);
+                    mma_commit(&xs_full[pb]);
+                    mma_commit(&x_empty[s]);
+                }
+                // z has no value left that is not finite, and the scores are decayed
+                if (!wait_warp(&z_full[s], (it / C::NS) & 1, abort)) break;
+                if (!wait_warp(&zw_ready[it & 3], (it >> 2) & 1, abort)) break;
+                if (!wait_warp(&a_ready[pb], (it >> 1) & 1, abort)) break;
                 tc_fence_after();
-                const uint64_t dz = smem_desc(st + OFF_Z, 0, 1024);
-#pragma unroll
-                for (int ks = 0; ks < kC / 16; ++ks)
-                    mma_f16_ts(tmem + C::col_az(pb), tmem + C::col_p(pb) + ks * 8, dz + mnmajor_step(ks), ID, ks > 0);
-                mma_commit(&o_full[pb]);
-                mma_commit(&empty[s]);
-            }
-        }
-        if (lane == 0) mma_commit(drain);
-    } else if (warp == 3) {
-        // ------------------------------------------------------ increments: y^T (weighted z)
-        if (lane == 0 && !*abort) {
-            constexpr uint32_t ID = idesc_bf16(128, kMB, 1, 1);
-            for (int it = 0; it < n; ++it) {
-                const int s = it % C::NS, db = it & 1;
-                if (!wait_bar(&full[s], (it / C::NS) & 1, abort)) break;
-                if (!wait_bar(zw_ready, it & 1, abort)) break;
-                if (it >= 2 && !wait_bar(&ds_free[db], (it / 2 - 1) & 1, abort)) break;
-                tc_fence_after();
-                // y^T read MN-major; 64 columns wide it is repeated (M-atom stride 0), so
-                // that lanes 64-127 hold a second copy
-                const uint64_t dy = smem_desc(smem_u32(stage(it)) + OFF_Y, DP == 64 ? 0 : kTile, 1024);
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    const uint64_t dz = smem_desc(smem_u32(zw) + part * kTile, 0, 1024);
+                const uint64_t dz = smem_desc(smem_u32(ztile(it)), 0, 1024);
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < kC / 16; ++ks)
-                        mma_f16_ss(tmem + C::col_ds(db), dy + mnmajor_step(ks), dz + mnmajor_step(ks), ID,
-                                   part > 0 || ks > 0);
+                        mma_f16_ts(tmem + C::COL_AZ, tmem + C::col_p(pb) + (ks / 4) * 64 + (ks % 4) * 8, dz + mnmajor_step(ks), ID,
+                                   ks > 0);
+                    mma_commit(&o_full[pb]);
+                    mma_commit(&z_empty[s]);
                 }
-                mma_commit(&ds_full[db]);
-                mma_commit(&empty[s]);
             }
         }
-        if (lane == 0) mma_commit(drain);
-    } else if (warp < 8) {
-        // ------------------------------------------------------ scores: decayed, masked, bf16
-        const int q4 = warp & 3, r = 32 * q4 + lane;
+        if (elect_one()) mma_commit(drain);
+    } else if (warp < 12) {
+        // ------------------------------------------------------ scores, output rows
+        const int q4 = warp & 3, r = 32 * q4 + lane, grp = warp >= 8;
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
         const float4 *col4 = reinterpret_cast<const float4 *>(colf);
-        for (int it = 0; it < (out ? n : 0); ++it) {
+        const float2 intra2 = make_float2(sw.c_intra, sw.c_intra);
+        __nv_bfloat16 *rows_out = static_cast<__nv_bfloat16 *>(sw.rows.data) + b * sw.rows.sb + h * sw.rows.sh + m0 + 32 * grp;
+        const int cols = sw.M - m0 - 32 * grp;
+        // scores of columns 64 grp..64 grp + 63, decayed, masked, rounded to bf16: over the
+        // first half of P's own columns, which this thread alone reads
+        auto scores = [&](int it) {
             const int pb = it & 1;
-            if (wait_bar_warp(&p_full[pb], (it >> 1) & 1, abort)) {
+            if (wait_warp(&p_full[pb], (it >> 1) & 1, abort)) {
                 tc_fence_after();
+                const uint32_t tp = tmem + lane_off + C::col_p(pb) + 64 * grp;
 #pragma unroll 1
-                for (int c0 = 0; c0 < kC; c0 += 32) {
-                    uint32_t a[16];
-                    if (backwards ? c0 < 32 * q4 : c0 > 32 * q4) {   // hidden from every row of this warp
+                for (int i = 0; i < 64; i += 16) {
+                    const int c0 = 64 * grp + i, block = c0 >> 5;
+                    uint32_t x[16], a[8];
+                    if (backwards ? block < q4 : block > q4) {   // hidden from every row of this warp
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) a[j] = 0u;
+                        for (int j = 0; j < 8; ++j) a[j] = 0u;
                     } else {
-                        float x[32];
-                        tmem_ld32f(tmem + lane_off + C::col_p(pb) + c0, x);
-                        if (c0 == 32 * q4) {
-                            const float *wr = backwards ? w - lane : w + lane;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float f = backwards ? wr[j] : wr[-j];
-                                x[j] = (backwards ? j >= lane : j <= lane) ? x[j] * f : 0.f;
-                            }
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) a[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
-                        } else {
+                        tmem_ld16(tp + i, x);
+                        if (block != q4) {
                             // a^(distance) = a^(row to the block's near edge) a^(edge to column): no power grows
-                            const float rf = backwards ? w[c0 - r] : w[r - c0 - 31];
+                            const float rf = backwards ? w[32 * block - r] : w[r - 32 * block - 31];
                             const float2 rf2 = make_float2(rf, rf);
+                            const float4 *f4 = col4 + (i & 16) / 4;
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float4 f = col4[j];
-                                const float2 u = mul_pair(make_float2(x[4 * j], x[4 * j + 1]),
-                                                          mul_pair(make_float2(f.x, f.y), rf2));
-                                const float2 v = mul_pair(make_float2(x[4 * j + 2], x[4 * j + 3]),
-                                                          mul_pair(make_float2(f.z, f.w), rf2));
-                                a[2 * j] = pack_bf16x2(u.x, u.y);
-                                a[2 * j + 1] = pack_bf16x2(v.x, v.y);
+                            for (int j = 0; j < 4; ++j) {
+                                const float4 f = f4[j];
+                                const float2 t = mul_pair(pair_at(x, 4 * j), mul_pair(make_float2(f.x, f.y), rf2));
+                                const float2 u = mul_pair(pair_at(x, 4 * j + 2), mul_pair(make_float2(f.z, f.w), rf2));
+                                a[2 * j] = pack_bf16x2(t.x, t.y);
+                                a[2 * j + 1] = pack_bf16x2(u.x, u.y);
+                            }
+                        } else {
+                            // a select hides what is behind the row's own column (0 times a score
+                            // that is not finite is NaN)
+                            const float *f = diag + (c0 - r);
+                            const int k = backwards ? r - c0 : c0 - r;
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; j += 2) {
+                                const float u = __uint_as_float(x[j]) * f[j], v = __uint_as_float(x[j + 1]) * f[j + 1];
+                                a[j / 2] = pack_bf16x2(backwards ? (j >= k ? u : 0.f) : (j <= -k ? u : 0.f),
+                                                       backwards ? (j + 1 >= k ? v : 0.f) : (j + 1 <= -k ? v : 0.f));
                             }
                         }
                     }
-                    tmem_st16(tmem + lane_off + C::col_p(pb) + c0 / 2, a);
+                    tmem_st8(tp + i / 2, a);
                 }
                 tmem_wait_st();
             }
             tc_fence_before();
-            mbar_arrive(&a_ready[pb]);
-        }
-    } else if (warp < 12) {
-        // ------------------------------------------------------ z weighed, in three bf16 parts
-        const int r = tid - 256;
-        for (int it = 0; it < n; ++it) {
-            const int s = it % C::NS, rows = rows_of(it);
-            bool ok = wait_bar_warp(&full[s], (it / C::NS) & 1, abort);
-            // the last increment has read the parts
-            if (it > 0) ok = ok && wait_bar_warp(&ds_full[(it - 1) & 1], ((it - 1) >> 1) & 1, abort);
+            arrive_warp(&a_ready[pb]);
+        };
+        // output columns 32 grp..32 grp + 31
+        auto output = [&](int it) {
+            const int pb = it & 1, rows = rows_of(it), t = first + chunk_of(it) * kC + r;
+            const bool ok = wait_warp(&o_full[pb], (it >> 1) & 1, abort);
+            uint32_t hit = 0u;
             if (ok) {
-                uint8_t *st = stage(it), *zt = st + OFF_Z;
-                if (rows < kC) {   // rows past the end: nothing, whatever they hold
-                    if (r >= rows) {
-                        for (int c = 0; c < 64; c += 8) {
-                            *reinterpret_cast<uint4 *>(zt + sw128_offset(r, c)) = make_uint4(0u, 0u, 0u, 0u);
-                            for (int j = 0; j < C::SUB; ++j)
-                                *reinterpret_cast<uint4 *>(st + OFF_Y + j * kTile + sw128_offset(r, c)) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                }
-                const float wr = r < rows ? w[backwards ? r + 1 : rows - 1 - r] : 0.f;
-                uint32_t most = 0u;
-#pragma unroll 2
-                for (int c = 0; c < 64; c += 8) {
-                    const uint32_t off = sw128_offset(r, c);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(zt + off);
-                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t hi[4], mid[4], lo[4];
+                tc_fence_after();
+                const volatile int *f = flag + it % C::NBAD * 16;
+                if (__builtin_expect(__any_sync(0xffffffffu, f[lane & 15]), 0))
+                    hit = seen_bad(r, grp, smem + C::OFF_BAD + it % C::NBAD * 256, f, backwards);
+                const float by = r < rows ? sw.c_inter * w[backwards ? rows - 1 - r : r + 1] : 0.f;
+                const float2 by2 = make_float2(by, by);
+                const uint32_t at = tmem + lane_off + 32 * grp;
+                __nv_bfloat16 *row = rows_out + (long long)t * sw.rows.sn;
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t az[16], xs[16], o[8];
+                    tmem_ld16(at + C::COL_AZ + c, az);
+                    tmem_ld16(at + C::COL_XS + c, xs);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        most = __vmaxu2(most, in[i] & 0x7fff7fffu);
-                        float2 f = mul_pair(get_pair(in[i]), make_float2(wr, wr));
-                        hi[i] = put_pair(f);
-                        float2 e = get_pair(hi[i]);
-                        f = make_float2(f.x - e.x, f.y - e.y);
-                        mid[i] = put_pair(f);
-                        e = get_pair(mid[i]);
-                        lo[i] = put_pair(make_float2(f.x - e.x, f.y - e.y));
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 v = fma_pair(pair_at(az, 2 * i), intra2, mul_pair(pair_at(xs, 2 * i), by2));
+                        o[i] = pack_bf16x2(v.x, v.y);
                     }
-                    *reinterpret_cast<uint4 *>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(zw + kTile + off) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    *reinterpret_cast<uint4 *>(zw + 2 * kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (__builtin_expect(r >= rows || hit, 0)) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)   // zeros past the length, NaN where a value of z that is not finite is seen
+                            o[i] = r >= rows ? 0u
+                                             : o[i] | (hit >> (c + 2 * i) & 1u ? 0x7fffu : 0u) |
+                                                   (hit >> (c + 2 * i + 1) & 1u ? 0x7fff0000u : 0u);
+                    }
+                    if (t < args.N)
+                        store16(row + c, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), cols - c);
                 }
-                const bool bad = (most & 0xffffu) >= 0x7f80u || (most >> 16) >= 0x7f80u;
-                const bool any = __any_sync(0xffffffffu, bad);
-                if (lane == 0) flag[(it & 3) * 4 + (warp & 3)] = any;
-                __threadfence_block();
             }
-            fence_proxy_async();
-            if (rows < kC) mbar_arrive(tail_ready);
-            mbar_arrive(zw_ready);
+            tc_fence_before();
+            arrive_warp(&o_free[pb]);
+        };
+        if (out) {
+            for (int it = 0; it <= n; ++it) {
+                if (it < n) scores(it);
+                if (it > 0) output(it - 1);
+            }
+            // the chunks past the length: zeros
+            const uint4 zeros = make_uint4(0u, 0u, 0u, 0u);
+            for (int t = first + n * kC + r; t < min(first + args.seg_tokens, args.N); t += kC)
+                for (int c = 0; c < 32; c += 16) store16(rows_out + (long long)t * sw.rows.sn + c, zeros, zeros, cols - c);
         }
     } else {
-        // ------------------------------------------------------ state and output rows
-        // DP = 64: thread (q4, lane) keeps row 32 (q4 & 1) + lane of the state, columns
-        // 32 (q4 / 2) on; DP = 128: row 32 q4 + lane, all columns
-        constexpr int NC = DP == 64 ? 32 : 64;
-        const int q4 = warp & 3, r = 32 * q4 + lane;
+        // ------------------------------------------------------ weighted z, state
+        // The state lies in registers: DP = 64: thread (grp, q4, lane) keeps columns
+        // 32 (q4 / 2) + 16 grp on of row 32 (q4 & 1) + lane; DP = 128: columns 32 grp on
+        // of row 32 q4 + lane
+        constexpr int NC = DP == 64 ? 16 : 32;
+        const int q4 = warp & 3, r = 32 * q4 + lane, grp = warp >= 16;
         const uint32_t lane_off = (uint32_t)(32 * q4) << 16;
-        const int d = DP == 64 ? 32 * (q4 & 1) + lane : r, cb = DP == 64 ? 32 * (q4 >> 1) : 0;
-        const bool leader = tid == 384;
+        const int d = DP == 64 ? 32 * (q4 & 1) + lane : r, cb = DP == 64 ? 32 * (q4 >> 1) + 16 * grp : 32 * grp;
         const int D = sw.D, M = sw.M;
         const size_t DM = (size_t)D * M;
         float sv[NC];
@@ -447,91 +599,117 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
             for (int j = 0; j < NC; ++j) sv[j] = start && d < D && m0 + cb + j < M ? *state_at(start, j) : 0.f;
         }
         auto put_snap = [&](int it) {
+            // the snapshot that this one replaces has been read by its chunk's x S
+            const int old = it - C::NSNAP;
+            if (old >= 0) wait_warp(&xs_full[old & 1], (old >> 1) & 1, abort);
 #pragma unroll
-            for (int j = 0; j < NC; j += 32) store_snap32<DP>(snap(it), d, cb + j, sv + j);
+            for (int j = 0; j < NC; j += 8) {
+                uint4 v;
+                v.x = pack_bf16x2(sv[j], sv[j + 1]);
+                v.y = pack_bf16x2(sv[j + 2], sv[j + 3]);
+                v.z = pack_bf16x2(sv[j + 4], sv[j + 5]);
+                v.w = pack_bf16x2(sv[j + 6], sv[j + 7]);
+                *reinterpret_cast<uint4 *>(snap(it) + sw128_offset(d, cb + j)) = v;
+            }
             fence_proxy_async();
-            mbar_arrive(&snap_ready[it & 1]);
+            arrive_warp(&snap_ready[it & 1]);
+        };
+        // z of chunk it: the half of its rows from 64 on or before, by four pieces of 16
+        // columns a row (the parts go where the MMAs have read the last chunk's)
+        const int zr = (tid - 384) & 63, zc = 16 * ((tid - 384) >> 6);
+        auto weigh = [&](int it, int half, bool ok) {
+            const int rows = rows_of(it), row = 64 * half + zr;
+            uint8_t *zt = ztile(it);
+            if (ok) {
+                const float wr = row < rows ? w[backwards ? row + 1 : rows - 1 - row] : 0.f;
+                const float2 wr2 = make_float2(wr, wr), minus = make_float2(-1.f, -1.f);
+                float2 check = make_float2(0.f, 0.f);   // NaN where a value is not finite
+#pragma unroll 1
+                for (int c = zc; c < zc + 16; c += 8) {
+                    const uint32_t off = sw128_offset(row, c);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(zt + off);
+                    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // the leading 8 bits of each value, cut off, three times: 24 bits, all there are
+                        float2 f = mul_pair(get_pair(in[j]), wr2);
+                        hi[j] = top_pair(f);
+                        f = fma_pair(get_pair(hi[j]), minus, f);
+                        check = add_pair(check, f);
+                        mid[j] = top_pair(f);
+                        lo[j] = top_pair(fma_pair(get_pair(mid[j]), minus, f));
+                    }
+                    *reinterpret_cast<uint4 *>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(zw + kTile + off) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                    if (parts == 3)
+                        *reinterpret_cast<uint4 *>(zw + 2 * kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+                const int slot = it % C::NBAD * 16 + 8 * half + (warp - 12);
+                const float all = check.x + check.y;
+                const bool any = __any_sync(0xffffffffu, !(fabsf(all) < __int_as_float(0x7f800000)));
+                if (__builtin_expect(any, 0)) take_out(zt, row, zc, smem + C::OFF_BAD + slot * 16, backwards);
+                if (lane == 0) flag[slot] = any;
+            }
+            fence_proxy_async();
+            arrive_warp(half ? &zw_ready[it & 3] : half_ready);
+        };
+        // a sequence's last chunk: rows past the end are nothing, whatever they hold
+        auto end_rows = [&](int it) {
+            const int rows = rows_of(it);
+            const bool ok = wait_warp(&y_full[it % C::NS], (it / C::NS) & 1, abort);
+            if (ok && r >= rows) {
+                uint8_t *zt = ztile(it), *yt = ytile(it) + (DP == 64 ? 0 : grp * kTile);
+                for (int c = 0; c < 32; c += 8)
+                    *reinterpret_cast<uint4 *>(zt + sw128_offset(r, 32 * grp + c)) = make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < DP / 2; c += 8)
+                    *reinterpret_cast<uint4 *>(yt + sw128_offset(r, (DP == 64 ? 32 * grp : 0) + c)) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+            arrive_warp(tail_ready);
+            asm volatile("bar.sync 1, 256;" ::: "memory");   // other warps read these rows
+            return ok;
         };
         if (out) put_snap(0);
-        const float2 kept_whole = kept(g, kC), kept_tail = kept(g, tail);
-        for (int it = 0; it < n; ++it) {
-            const int db = it & 1, pb = it & 1, rows = rows_of(it);
-            bool ok = wait_bar_warp(&ds_full[db], (it >> 1) & 1, abort);
-            if (ok) {
-                tc_fence_after();
-                const float2 a = rows == kC ? kept_whole : kept_tail;
-#pragma unroll
-                for (int j = 0; j < NC; j += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(tmem + lane_off + C::col_ds(db) + cb + j, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sv[j + i] = fmaf(sw.c_state, __uint_as_float(v[i]), keep(a, sv[j + i]));
-                }
+        const float2 kept_whole = kept(g, kC), kept_tail = kept(g, tail), c2 = make_float2(sw.c_state, sw.c_state);
+        for (int it = 0; it <= n; ++it) {
+            bool ok = true;
+            if (it < n) {
+                ok = wait_warp(&z_full[it % C::NS], (it / C::NS) & 1, abort);
+                if (rows_of(it) < kC) ok = end_rows(it) && ok;
+                if (it > 0) ok = wait_warp(half_free, (it - 1) & 1, abort) && ok;
+                weigh(it, 0, ok);
             }
-            tc_fence_before();
-            mbar_arrive(&ds_free[db]);
-            if (!out) continue;
-            // the snapshot of chunk it - 1 was read before its output rows were, with
-            // room for one alone chunk it's has to be read first
-            if (C::NSNAP == 1) ok = ok && wait_bar_warp(&xs_full[pb], (it >> 1) & 1, abort);
-            if (it + 1 < n) put_snap(it + 1);
-            ok = ok && wait_bar_warp(&o_full[pb], (it >> 1) & 1, abort);
-            uint8_t *st = stage(it);   // x is dead: its first sub-tile takes the output rows
-            if (ok) {
-                tc_fence_after();
-                const volatile int *f = flag + (it & 3) * 4;
-                const bool by_hand = f[0] | f[1] | f[2] | f[3];
-                const float inter = sw.c_inter * w[r < rows ? (backwards ? rows - 1 - r : r + 1) : 0];
-                if (by_hand) {
-                    row_by_hand<DP>(st, st + OFF_Y, st + OFF_Z, w, tmem + lane_off + C::col_xs(pb), r, rows, backwards,
-                                    sw.c_intra, inter);
-                } else {
+            if (it > 0) {   // the increment of the chunk before
+                ok = wait_warp(ds_full, (it - 1) & 1, abort) && ok;
+                if (ok) {
+                    tc_fence_after();
+                    const float2 a = rows_of(it - 1) == kC ? kept_whole : kept_tail;
+                    const uint32_t tds = tmem + lane_off + C::COL_DS + cb;
 #pragma unroll
-                    for (int c0 = 0; c0 < kMB; c0 += 16) {
-                        uint32_t az[16], xs[16], o[8];
-                        tmem_ld16(tmem + lane_off + C::col_az(pb) + c0, az);
-                        tmem_ld16(tmem + lane_off + C::col_xs(pb) + c0, xs);
+                    for (int j = 0; j < NC; j += 16) {
+                        uint32_t v[16], u[16];
+                        tmem_ld16(tds + j, v);
+                        tmem_ld16(tds + kMB + j, u);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float u = fmaf(sw.c_intra, __uint_as_float(az[2 * i]), inter * __uint_as_float(xs[2 * i]));
-                            const float v =
-                                fmaf(sw.c_intra, __uint_as_float(az[2 * i + 1]), inter * __uint_as_float(xs[2 * i + 1]));
-                            o[i] = r < rows ? pack_bf16x2(u, v) : 0u;
+                        for (int i = 0; i < 16; i += 2) {
+                            const float2 e = add_pair(pair_at(v, i), pair_at(u, i));
+                            float2 s2 = make_float2(sv[j + i], sv[j + i + 1]);
+                            s2 = fma_pair(make_float2(a.y, a.y), s2, mul_pair(make_float2(a.x, a.x), s2));
+                            s2 = fma_pair(c2, e, s2);
+                            sv[j + i] = s2.x, sv[j + i + 1] = s2.y;
                         }
-                        *reinterpret_cast<uint4 *>(st + sw128_offset(r, c0)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(st + sw128_offset(r, c0 + 8)) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
                 }
+                tc_fence_before();
+                arrive_warp(ds_free);
             }
-            tc_fence_before();
-            mbar_arrive(&o_free[pb]);
-            fence_proxy_async();
-            state_sync();
-            if (leader) {
-                if (ok) {
-                    tma_store_4d(&sw.out, st, m0, first + chunk_of(it) * kC, h, b);
-                    tma_store_commit();
-                }
-                tma_store_wait_read0();
-                mbar_arrive(&empty[it % C::NS]);
-            }
+            if (it == n) break;
+            // z before the snapshot: its increment is what the next round waits for
+            weigh(it, 1, ok);
+            if (it > 0 && out) put_snap(it);
         }
-        // chunks past the length: rows of zeros (no load is on its way any more)
-        const int chunks = (min(first + args.seg_tokens, args.N) - first + kC - 1) / kC;
-        if (out && n < chunks) {
-            state_sync();   // the leader's last store has read its tile
-            for (int c = 0; c < 64; c += 8) *reinterpret_cast<uint4 *>(smem + sw128_offset(r, c)) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async();
-            state_sync();
-            if (leader && !*abort) {
-                for (int c = n; c < chunks; ++c) tma_store_4d(&sw.out, smem, m0, first + c * kC, h, b);
-                tma_store_commit();
-            }
-        }
-        if (leader && out) tma_store_wait_all0();
         // the state leaves where the sequence's last segment (backwards: its first) ends
         const int last = max(0, (len + args.seg_tokens - 1) / args.seg_tokens - 1);
         if (sw.end && !*abort && (args.sums || seg == (backwards ? 0 : last))) {
@@ -609,8 +787,8 @@ cudaError_t tc_decay(const DecayLaunch &l) {
         const DecaySweep &s = l.sweep[i];
         TcSweep &t = a.sweep[i];
         if (!map_of(&t.y, s.y, s.D, l) || !map_of(&t.z, s.z, s.M, l)) return cudaErrorInvalidValue;
-        if (s.out.data && (!map_of(&t.x, s.x, s.D, l) || !map_of(&t.out, s.out, s.M, l))) return cudaErrorInvalidValue;
-        t.start = s.start, t.end = s.end, t.D = s.D, t.M = s.M, t.blocks = (s.M + kMB - 1) / kMB;
+        if (s.out.data && !map_of(&t.x, s.x, s.D, l)) return cudaErrorInvalidValue;
+        t.rows = s.out, t.start = s.start, t.end = s.end, t.D = s.D, t.M = s.M, t.blocks = (s.M + kMB - 1) / kMB;
         t.transposed = s.transposed, t.backwards = s.backwards, t.has_out = s.out.data != nullptr;
         t.c_intra = s.c_intra, t.c_inter = s.c_inter, t.c_state = s.c_state;
         a.blocks += t.blocks;
