@@ -575,7 +575,7 @@ typedef struct {
  *      keys.  qo may be q and ko may be k (same strides): in place.
  *   norm 0: n = x (wq and wk have to be NULL); else wq, wk: D fp32 values each,
  *      or NULL (1).  eps >= 0.
- *   D even, 2 <= D <= 256 (else LA_ERR_UNSUPPORTED).
+ *   D even, 2 <= D <= 256, B N < 2^31 - 2^20 (else LA_ERR_UNSUPPORTED).
  * All arithmetic is fp32, y is rounded once.
  */
 la_status la_qk_rotate_forward(la_view q, la_view k, la_view qo, la_view ko, const float *wq, const float *wk,

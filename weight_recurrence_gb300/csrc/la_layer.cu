@@ -138,7 +138,7 @@ bool any_same(const void *a, std::initializer_list<const void *> others) {
 la_status check_qk(const la_qk_shape &s) {
     if (s.B < 0 || s.N < 0 || s.Hq < 0 || s.Hk < 0 || s.D < 1 || !dtype_ok(s.dtype)) return LA_ERR_INVALID_ARG;
     if (s.D > kRotateMaxD || s.D % 2) return LA_ERR_UNSUPPORTED;
-    if ((__int128)s.B * s.N > (1LL << 34)) return LA_ERR_UNSUPPORTED;
+    if ((long long)s.B * s.N > 0x7fffffff - (1 << 20)) return LA_ERR_UNSUPPORTED;   // tokens are counted in 32 bits
     return LA_OK;
 }
 

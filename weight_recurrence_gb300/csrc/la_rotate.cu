@@ -58,9 +58,8 @@ __device__ __forceinline__ unsigned long long turns(float f) {
     return bits >> 31 ? 0ull - t : t;
 }
 
-// How a lane's four pairs lie in a head's row: kHalf, kAdjacent: four
-// neighbouring pairs by 8 or 16 byte accesses; kAny: pairs a warp apart by
-// single values.
+// How a lane's V pairs lie in a head's row: kHalf, kAdjacent: V neighbouring pairs
+// by 16 byte pieces; kAny: pairs a warp apart by single values.
 enum Layout { kHalf, kAdjacent, kAny };
 
 // Channels of pair p: rotated pairs first, the channels behind them as pairs
@@ -70,20 +69,28 @@ __device__ __forceinline__ int second_of(int p, int P, int D, bool half) {
     return half ? (p < P ? p + P : p + D / 2) : 2 * p + 1;
 }
 
-// A lane's share of a row as it lies in memory: eight values.
-template <typename T, Layout L> struct Raw {
-    uint4 w[sizeof(T) == 4 ? 2 : 1];
+// A lane's share of a row as it lies in memory: 2V values.
+template <typename T, Layout L, int V> struct Raw {
+    uint4 w[2 * V * sizeof(T) / 16];
 };
-template <typename T> struct Raw<T, kAny> {
-    T v[8];
+template <typename T, int V> struct Raw<T, kAny, V> {
+    T v[2 * V];
+};
+// The first and the second values of its pairs, two pairs to a float2.
+template <int V> struct Pairs {
+    float2 a[V / 2], b[V / 2];
 };
 
-template <typename T, Layout L>
-__device__ __forceinline__ Raw<T, L> load_raw(const T *row, int lane, int P, int D, bool half) {
-    Raw<T, L> r;
+template <int V, Layout L> __device__ __forceinline__ int pair_of_lane(int lane, int i) {
+    return L == kAny ? lane + 32 * i : V * lane + i;
+}
+
+template <typename T, Layout L, int V>
+__device__ __forceinline__ Raw<T, L, V> load_raw(const T *row, int lane, int P, int D, bool half) {
+    Raw<T, L, V> r;
     if constexpr (L == kAny) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < V; i++) {
             const int p = lane + 32 * i;
             r.v[2 * i] = r.v[2 * i + 1] = from_f32<T>(0.f);
             if (p < D / 2) {
@@ -92,81 +99,85 @@ __device__ __forceinline__ Raw<T, L> load_raw(const T *row, int lane, int P, int
             }
         }
     } else {
-        const int p = 4 * lane;
+        static_assert(V * sizeof(T) == 16, "a piece is V values");
+        const int p = V * lane;
         const bool in = p < D / 2;
-        if constexpr (L == kAdjacent) {
-            const uint4 *s = reinterpret_cast<const uint4 *>(row + 2 * p);
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) / 2; i++) r.w[i] = in ? s[i] : make_uint4(0, 0, 0, 0);
-        } else if constexpr (sizeof(T) == 4) {
-            r.w[0] = in ? *reinterpret_cast<const uint4 *>(row + first_of(p, P, true)) : make_uint4(0, 0, 0, 0);
-            r.w[1] = in ? *reinterpret_cast<const uint4 *>(row + second_of(p, P, D, true)) : make_uint4(0, 0, 0, 0);
-        } else {
-            const uint2 z = make_uint2(0, 0);
-            const uint2 a = in ? *reinterpret_cast<const uint2 *>(row + first_of(p, P, true)) : z;
-            const uint2 b = in ? *reinterpret_cast<const uint2 *>(row + second_of(p, P, D, true)) : z;
-            r.w[0] = make_uint4(a.x, a.y, b.x, b.y);
-        }
+        const T *x = row + (L == kHalf ? first_of(p, P, true) : 2 * p);
+        const T *y = L == kHalf ? row + second_of(p, P, D, true) : x + V;
+        r.w[0] = in ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0);
+        r.w[1] = in ? *reinterpret_cast<const uint4 *>(y) : make_uint4(0, 0, 0, 0);
     }
     return r;
 }
 
-// pair i of the lane's four, in fp32
-template <typename T, Layout L> __device__ __forceinline__ float2 pair_of(const Raw<T, L> &r, int i) {
-    if constexpr (L == kAny) {
-        return make_float2(to_f32(r.v[2 * i]), to_f32(r.v[2 * i + 1]));
-    } else if constexpr (sizeof(T) == 4) {
-        if constexpr (L == kAdjacent) {
-            const uint4 q = r.w[i / 2];
-            return i % 2 ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
-                         : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
-        } else {
-            const unsigned a = i == 0 ? r.w[0].x : i == 1 ? r.w[0].y : i == 2 ? r.w[0].z : r.w[0].w;
-            const unsigned b = i == 0 ? r.w[1].x : i == 1 ? r.w[1].y : i == 2 ? r.w[1].z : r.w[1].w;
-            return make_float2(__uint_as_float(a), __uint_as_float(b));
-        }
-    } else {
-        const uint4 q = r.w[0];
-        if constexpr (L == kAdjacent) {
-            return get_pair(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
-        } else {
-            const float2 a = get_pair(i < 2 ? q.x : q.y), b = get_pair(i < 2 ? q.z : q.w);
-            return i % 2 ? make_float2(a.y, b.y) : make_float2(a.x, b.x);
-        }
-    }
+__device__ __forceinline__ float2 floats(unsigned x, unsigned y) {
+    return make_float2(__uint_as_float(x), __uint_as_float(y));
 }
 
-template <typename T, Layout L>
-__device__ __forceinline__ void store_pairs(T *row, const float2 (&v)[4], int lane, int P, int D, bool half) {
+template <typename T, Layout L, int V> __device__ __forceinline__ Pairs<V> pairs_of(const Raw<T, L, V> &r) {
+    Pairs<V> o;
     if constexpr (L == kAny) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int i = 0; i < V / 2; i++) {
+            o.a[i] = make_float2(to_f32(r.v[4 * i]), to_f32(r.v[4 * i + 2]));
+            o.b[i] = make_float2(to_f32(r.v[4 * i + 1]), to_f32(r.v[4 * i + 3]));
+        }
+    } else {
+        const uint4 x = r.w[0], y = r.w[1];
+        if constexpr (sizeof(T) == 4) {
+            if constexpr (L == kHalf) {
+                o.a[0] = floats(x.x, x.y), o.a[1] = floats(x.z, x.w);
+                o.b[0] = floats(y.x, y.y), o.b[1] = floats(y.z, y.w);
+            } else {
+                o.a[0] = floats(x.x, x.z), o.b[0] = floats(x.y, x.w);
+                o.a[1] = floats(y.x, y.z), o.b[1] = floats(y.y, y.w);
+            }
+        } else if constexpr (L == kHalf) {
+            o.a[0] = get_pair(x.x), o.a[1] = get_pair(x.y), o.a[2] = get_pair(x.z), o.a[3] = get_pair(x.w);
+            o.b[0] = get_pair(y.x), o.b[1] = get_pair(y.y), o.b[2] = get_pair(y.z), o.b[3] = get_pair(y.w);
+        } else {   // a word holds a pair
+            o.a[0] = floats(x.x << 16, x.y << 16), o.b[0] = floats(x.x & 0xffff0000u, x.y & 0xffff0000u);
+            o.a[1] = floats(x.z << 16, x.w << 16), o.b[1] = floats(x.z & 0xffff0000u, x.w & 0xffff0000u);
+            o.a[2] = floats(y.x << 16, y.y << 16), o.b[2] = floats(y.x & 0xffff0000u, y.y & 0xffff0000u);
+            o.a[3] = floats(y.z << 16, y.w << 16), o.b[3] = floats(y.z & 0xffff0000u, y.w & 0xffff0000u);
+        }
+    }
+    return o;
+}
+
+template <typename T, Layout L, int V>
+__device__ __forceinline__ void store_pairs(T *row, const Pairs<V> &v, int lane, int P, int D, bool half) {
+    if constexpr (L == kAny) {
+#pragma unroll
+        for (int i = 0; i < V; i++) {
             const int p = lane + 32 * i;
             if (p < D / 2) {
-                row[first_of(p, P, half)] = from_f32<T>(v[i].x);
-                row[second_of(p, P, D, half)] = from_f32<T>(v[i].y);
+                row[first_of(p, P, half)] = from_f32<T>(i % 2 ? v.a[i / 2].y : v.a[i / 2].x);
+                row[second_of(p, P, D, half)] = from_f32<T>(i % 2 ? v.b[i / 2].y : v.b[i / 2].x);
             }
         }
     } else {
-        const int p = 4 * lane;
+        const int p = V * lane;
         if (p >= D / 2) return;
+        T *x = row + (L == kHalf ? first_of(p, P, true) : 2 * p);
+        T *y = L == kHalf ? row + second_of(p, P, D, true) : x + V;
         if constexpr (sizeof(T) == 4) {
-            if constexpr (L == kAdjacent) {
-                float4 *d = reinterpret_cast<float4 *>(row + 2 * p);
-                d[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-                d[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+            if constexpr (L == kHalf) {
+                *reinterpret_cast<float4 *>(x) = make_float4(v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y);
+                *reinterpret_cast<float4 *>(y) = make_float4(v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y);
             } else {
-                *reinterpret_cast<float4 *>(row + first_of(p, P, true)) = make_float4(v[0].x, v[1].x, v[2].x, v[3].x);
-                *reinterpret_cast<float4 *>(row + second_of(p, P, D, true)) = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+                *reinterpret_cast<float4 *>(x) = make_float4(v.a[0].x, v.b[0].x, v.a[0].y, v.b[0].y);
+                *reinterpret_cast<float4 *>(y) = make_float4(v.a[1].x, v.b[1].x, v.a[1].y, v.b[1].y);
             }
-        } else if constexpr (L == kAdjacent) {
-            *reinterpret_cast<uint4 *>(row + 2 * p) =
-                make_uint4(put_pair(v[0]), put_pair(v[1]), put_pair(v[2]), put_pair(v[3]));
+        } else if constexpr (L == kHalf) {
+            *reinterpret_cast<uint4 *>(x) = make_uint4(put_pair(v.a[0]), put_pair(v.a[1]), put_pair(v.a[2]), put_pair(v.a[3]));
+            *reinterpret_cast<uint4 *>(y) = make_uint4(put_pair(v.b[0]), put_pair(v.b[1]), put_pair(v.b[2]), put_pair(v.b[3]));
         } else {
-            *reinterpret_cast<uint2 *>(row + first_of(p, P, true)) =
-                make_uint2(put_pair(make_float2(v[0].x, v[1].x)), put_pair(make_float2(v[2].x, v[3].x)));
-            *reinterpret_cast<uint2 *>(row + second_of(p, P, D, true)) =
-                make_uint2(put_pair(make_float2(v[0].y, v[1].y)), put_pair(make_float2(v[2].y, v[3].y)));
+            auto word = [&](int i) {
+                return i % 2 ? put_pair(make_float2(v.a[i / 2].y, v.b[i / 2].y)) : put_pair(make_float2(v.a[i / 2].x, v.b[i / 2].x));
+            };
+            *reinterpret_cast<uint4 *>(x) = make_uint4(word(0), word(1), word(2), word(3));
+            *reinterpret_cast<uint4 *>(y) = make_uint4(word(4), word(5), word(6), word(7));
         }
     }
 }
@@ -177,137 +188,158 @@ template <int G> __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// cos and sin of the lane's four pairs for the token's positions
-template <int G, Layout L>
-__device__ __forceinline__ void angles(const RotArgs &a, int lane, long long at, const unsigned long long (&turn)[4],
-                                       const float (&bad)[4], float2 (&cs)[4]) {
-    const int p0 = a.pos[at];
+// cos and sin of the lane's pairs for the token's positions.  With fp32 data by
+// sincospi (2 ulp), with bf16 data by the SFU's, 2^-21 off within a turn.
+template <typename T, int V, Layout L>
+__device__ __forceinline__ void angles(const RotArgs &a, int lane, long long at, const unsigned long long *turn,
+                                       unsigned bad, float2 (&cs)[V / 2], float2 (&sn)[V / 2]) {
+    const int p0 = a.P > 0 ? a.pos[at] : 0;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int p = L == kAny ? lane + 32 * i : 4 * lane + i;
-        cs[i] = make_float2(1.f, 0.f);
+    for (int i = 0; i < V; i++) {
+        const int p = pair_of_lane<V, L>(lane, i);
+        float c = 1.f, s = 0.f;
         if (p < a.P) {
             const int x = a.by_axis ? a.pos[at + a.axes[p] * a.sa] : p0;
-            const unsigned long long u = (unsigned long long)(long long)x * turn[i];
+            const unsigned long long u = (unsigned long long)(long long)x * turn[p];
             const float half_turns = (float)(int)((u + 0x80000000ull) >> 32) * 0x1p-31f;
-            float s, c;
-            sincospif(half_turns, &s, &c);
-            cs[i] = make_float2(c + bad[i], s + bad[i]);
+            if constexpr (sizeof(T) == 4) {
+                sincospif(half_turns, &s, &c);
+            } else {
+                s = __sinf(half_turns * 3.14159265f);
+                c = __cosf(half_turns * 3.14159265f);
+            }
+            if (bad >> i & 1) s = c = __int_as_float(0x7fffffff);
         }
+        (i % 2 ? cs[i / 2].y : cs[i / 2].x) = c;
+        (i % 2 ? sn[i / 2].y : sn[i / 2].x) = s;
     }
 }
 
-__device__ __forceinline__ float2 turned(float2 v, float2 cs) {
-    return make_float2(v.x * cs.x - v.y * cs.y, v.y * cs.x + v.x * cs.y);
-}
-__device__ __forceinline__ float2 turned_back(float2 v, float2 cs) {
-    return make_float2(v.x * cs.x + v.y * cs.y, v.y * cs.x - v.x * cs.y);
-}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
 
 // G lanes to a token; BWD: the gradients; NORM: with the norm.  U heads are on
 // their way at a time.
-template <typename T, int G, Layout L, bool BWD, bool NORM>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
-    constexpr int U = BWD ? 2 : 4;
+template <typename T, int V, int G, Layout L, bool BWD, bool NORM>
+__global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_constant__ RotArgs a) {
+    constexpr int U = BWD ? 2 : 4, E = V / 2;
     const int lane = threadIdx.x % G, D = a.D, P = a.P;
     const bool half = L == kHalf || (L == kAny && a.half);
-    const long long groups = (long long)gridDim.x * (kThreads / G);
-    const long long tokens = (long long)a.B * a.N, items = tokens * a.splits;
-    unsigned long long turn[4];
-    float bad[4];
-    float2 w[2][4], dw[2][4];
+    const unsigned groups = gridDim.x * (kThreads / G), tokens = (unsigned)a.B * a.N, items = tokens * a.splits;
+    const float mean = 1.f / (float)D;
+    __shared__ unsigned long long turn[kMaxPairs];   // of every pair, a position
+    unsigned bad = 0;
+    float2 dwa[BWD && NORM ? E : 1], dwb[BWD && NORM ? E : 1];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int p = L == kAny ? lane + 32 * i : 4 * lane + i;
+    for (int i = 0; i < V; i++) {
+        const int p = pair_of_lane<V, L>(lane, i);
         const float f = p < P ? a.freq[p] : 0.f;
-        turn[i] = turns(f);
-        bad[i] = f - f;
-#pragma unroll
-        for (int s = 0; s < 2; s++) {
-            dw[s][i] = make_float2(0.f, 0.f);
-            w[s][i] = NORM && a.w[s] && p < D / 2
-                          ? make_float2(a.w[s][first_of(p, P, half)], a.w[s][second_of(p, P, D, half)])
-                          : make_float2(1.f, 1.f);
-        }
+        bad |= (f - f != 0.f ? 1u : 0u) << i;
     }
-    // every group of a warp walks the same number of times: the sums' shuffles take whole warps
-    const long long first = (long long)blockIdx.x * (kThreads / G) + threadIdx.x / G;
-    const long long warp_first = (long long)blockIdx.x * (kThreads / G) + threadIdx.x / 32 * (32 / G);
-    for (long long it = first, wit = warp_first; wit < items; it += groups, wit += groups) {
+#pragma unroll
+    for (int i = 0; i < (BWD && NORM ? E : 1); i++) dwa[i] = dwb[i] = both(0.f);
+    if (threadIdx.x < P) turn[threadIdx.x] = turns(a.freq[threadIdx.x]);
+    __syncthreads();
+    // every group of a warp walks the same number of times: the sums' shuffles take whole
+    // warps (at most 2^31 items, so nothing below wraps)
+    const unsigned first = blockIdx.x * (kThreads / G) + threadIdx.x / G;
+    const unsigned warp_first = blockIdx.x * (kThreads / G) + threadIdx.x / 32 * (32 / G);
+    for (unsigned it = first, wit = warp_first; wit < items; it += groups, wit += groups) {
         const bool live = it < items;
-        const long long token = live ? it % tokens : 0;
-        const int split = live ? (int)(it / tokens) : 0;
-        const long long b = token / a.N, n = token - b * a.N;
-        float2 cs[4];
-        if (P > 0) {
-            angles<G, L>(a, lane, b * a.sb + n * a.sn, turn, bad, cs);
-        } else {
+        const unsigned split = live ? it / tokens : 0u, token = live ? it - split * tokens : 0u;
+        const unsigned bu = token / a.N;
+        const long long b = bu, n = token - bu * a.N;
+        float2 cs[E], sn[E];
+        angles<T, V, L>(a, lane, b * a.sb + n * a.sn, turn, bad, cs, sn);
+        // queries and keys; backward each by CTAs of its own, whose threads have room for one
+        // side's sums
 #pragma unroll
-            for (int i = 0; i < 4; i++) cs[i] = make_float2(1.f, 0.f);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; s++) {
+        for (int side = 0; side < (BWD ? 1 : 2); side++) {
+            const int s = BWD ? blockIdx.y : side;
             const T *x = static_cast<const T *>(a.x[s]) + b * a.xb[s] + n * a.xn[s];
             const T *dy = BWD ? static_cast<const T *>(a.dy[s]) + b * a.db[s] + n * a.dn[s] : nullptr;
             T *y = static_cast<T *>(a.y[s]) + b * a.yb[s] + n * a.yn[s];
             const int H = a.H[s];
+            // the weights of the lane's channels
+            float2 wa[NORM ? E : 1], wb[NORM ? E : 1];
+            if constexpr (NORM) {
+#pragma unroll
+                for (int i = 0; i < E; i++) {
+                    wa[i] = wb[i] = both(1.f);
+                    if (a.w[s]) {
+                        const int p = pair_of_lane<V, L>(lane, 2 * i), q = pair_of_lane<V, L>(lane, 2 * i + 1);
+                        if (p < D / 2) wa[i].x = a.w[s][first_of(p, P, half)], wb[i].x = a.w[s][second_of(p, P, D, half)];
+                        if (q < D / 2) wa[i].y = a.w[s][first_of(q, P, half)], wb[i].y = a.w[s][second_of(q, P, D, half)];
+                    }
+                }
+            }
+#pragma unroll 1
             for (int h0 = 0; h0 < H; h0 += U * a.splits) {
-                Raw<T, L> rx[U], rd[U];
+                Raw<T, L, V> rx[U], rd[U];
 #pragma unroll
                 for (int j = 0; j < U; j++) {
-                    const int h = h0 + j * a.splits + split;
-                    const bool on = live && h < H;
+                    const int h = h0 + j * a.splits + (int)split;
                     // a head that is not there: the row's own start, read and not used
-                    const int hh = on ? h : 0;
-                    if (NORM || !BWD) rx[j] = load_raw<T, L>(x + hh * a.xh[s], lane, P, D, half);
-                    if (BWD) rd[j] = load_raw<T, L>(dy + hh * a.dh[s], lane, P, D, half);
+                    const int hh = live && h < H ? h : 0;
+                    if (NORM || !BWD) rx[j] = load_raw<T, L, V>(x + hh * a.xh[s], lane, P, D, half);
+                    if (BWD) rd[j] = load_raw<T, L, V>(dy + hh * a.dh[s], lane, P, D, half);
                 }
 #pragma unroll
                 for (int j = 0; j < U; j++) {
-                    const int h = h0 + j * a.splits + split;
+                    const int h = h0 + j * a.splits + (int)split;
                     const bool on = live && h < H;
-                    float2 v[4], o[4];
+                    Pairs<V> v, o;
                     float rstd = 1.f;
-                    if (NORM || !BWD) {
-                        float sum = 0.f;
+                    if (NORM || !BWD) v = pairs_of<T, L, V>(rx[j]);
+                    if constexpr (NORM) {
+                        float2 sum = both(0.f);
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            v[i] = pair_of(rx[j], i);
-                            sum = fmaf(v[i].x, v[i].x, fmaf(v[i].y, v[i].y, sum));
-                        }
-                        if (NORM) rstd = 1.f / sqrtf(group_sum<G>(sum) / (float)D + a.eps);
+                        for (int i = 0; i < E; i++)
+                            sum = fma_pair(v.a[i], v.a[i], fma_pair(v.b[i], v.b[i], sum));
+                        rstd = rsqrtf(fmaf(group_sum<G>(sum.x + sum.y), mean, a.eps));
                     }
                     if constexpr (!BWD) {
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            if (NORM) v[i] = make_float2(v[i].x * rstd * w[s][i].x, v[i].y * rstd * w[s][i].y);
-                            o[i] = turned(v[i], cs[i]);
-                        }
-                    } else if constexpr (!NORM) {
-#pragma unroll
-                        for (int i = 0; i < 4; i++) o[i] = turned_back(pair_of(rd[j], i), cs[i]);
-                    } else {
-                        float2 u[4];
-                        float dot = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            u[i] = turned_back(pair_of(rd[j], i), cs[i]);
-                            v[i].x *= rstd;
-                            v[i].y *= rstd;
-                            if (on) {
-                                dw[s][i].x = fmaf(u[i].x, v[i].x, dw[s][i].x);
-                                dw[s][i].y = fmaf(u[i].y, v[i].y, dw[s][i].y);
+                        for (int i = 0; i < E; i++) {
+                            if (NORM) {
+                                v.a[i] = mul_pair(mul_pair(v.a[i], both(rstd)), wa[i]);
+                                v.b[i] = mul_pair(mul_pair(v.b[i], both(rstd)), wb[i]);
                             }
-                            u[i].x *= w[s][i].x;
-                            u[i].y *= w[s][i].y;
-                            dot = fmaf(u[i].x, v[i].x, fmaf(u[i].y, v[i].y, dot));
+                            o.a[i] = fma_pair(v.a[i], cs[i], neg(mul_pair(v.b[i], sn[i])));
+                            o.b[i] = fma_pair(v.b[i], cs[i], mul_pair(v.a[i], sn[i]));
                         }
-                        dot = group_sum<G>(dot) / (float)D;
+                    } else {
+                        const Pairs<V> d = pairs_of<T, L, V>(rd[j]);
+                        Pairs<V> u;
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            o[i] = make_float2(rstd * (u[i].x - v[i].x * dot), rstd * (u[i].y - v[i].y * dot));
+                        for (int i = 0; i < E; i++) {   // turned back
+                            u.a[i] = fma_pair(d.a[i], cs[i], mul_pair(d.b[i], sn[i]));
+                            u.b[i] = fma_pair(d.b[i], cs[i], neg(mul_pair(d.a[i], sn[i])));
+                        }
+                        if constexpr (!NORM) {
+                            o = u;
+                        } else {
+                            const float2 r = both(rstd);
+                            float2 dot2 = both(0.f);
+#pragma unroll
+                            for (int i = 0; i < E; i++) {
+                                v.a[i] = mul_pair(v.a[i], r), v.b[i] = mul_pair(v.b[i], r);
+                                if (on) {   // a head that is not there adds nothing
+                                    dwa[i] = fma_pair(u.a[i], v.a[i], dwa[i]);
+                                    dwb[i] = fma_pair(u.b[i], v.b[i], dwb[i]);
+                                }
+                                u.a[i] = mul_pair(u.a[i], wa[i]), u.b[i] = mul_pair(u.b[i], wb[i]);
+                                dot2 = fma_pair(u.a[i], v.a[i], fma_pair(u.b[i], v.b[i], dot2));
+                            }
+                            const float2 dot = both(-group_sum<G>(dot2.x + dot2.y) * mean);
+#pragma unroll
+                            for (int i = 0; i < E; i++) {
+                                o.a[i] = mul_pair(r, fma_pair(v.a[i], dot, u.a[i]));
+                                o.b[i] = mul_pair(r, fma_pair(v.b[i], dot, u.b[i]));
+                            }
+                        }
                     }
-                    if (on) store_pairs<T, L>(y + h * a.yh[s], o, lane, P, D, half);
+                    if (on) store_pairs<T, L, V>(y + h * a.yh[s], o, lane, P, D, half);
                 }
             }
         }
@@ -315,23 +347,21 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotArgs a) {
     if constexpr (BWD && NORM) {
         if (a.ws == nullptr) return;
         // the groups' sums of this CTA, added in the groups' order
-        extern __shared__ float sums[];   // [groups][2][D]
-        float *mine = sums + (size_t)(threadIdx.x / G) * 2 * D;
+        extern __shared__ float sums[];   // [groups][D]
+        float *mine = sums + (size_t)(threadIdx.x / G) * D;
 #pragma unroll
-        for (int s = 0; s < 2; s++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int p = L == kAny ? lane + 32 * i : 4 * lane + i;
-                if (p < D / 2) {
-                    mine[s * D + first_of(p, P, half)] = dw[s][i].x;
-                    mine[s * D + second_of(p, P, D, half)] = dw[s][i].y;
-                }
+        for (int i = 0; i < V; i++) {
+            const int p = pair_of_lane<V, L>(lane, i);
+            if (p < D / 2) {
+                mine[first_of(p, P, half)] = i % 2 ? dwa[i / 2].y : dwa[i / 2].x;
+                mine[second_of(p, P, D, half)] = i % 2 ? dwb[i / 2].y : dwb[i / 2].x;
             }
+        }
         __syncthreads();
-        for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
+        for (int c = threadIdx.x; c < D; c += kThreads) {
             float t = 0.f;
-            for (int g = 0; g < kThreads / G; g++) t += sums[(size_t)g * 2 * D + c];
-            a.ws[(size_t)blockIdx.x * 2 * D + c] = t;
+            for (int g = 0; g < kThreads / G; g++) t += sums[(size_t)g * D + c];
+            a.ws[((size_t)blockIdx.x * 2 + blockIdx.y) * D + c] = t;
         }
     }
 }
@@ -354,29 +384,40 @@ __global__ void __launch_bounds__(256) weight_sums_kernel(const float *ws, int n
 }
 
 constexpr int kSms = 152;
-constexpr int kBwdCtas = kSms * 4;   // their sums are written: few, that stay
+constexpr int kBwdCtas = kSms * 2;   // for each of queries and keys; their sums are written: few, that stay
 
 bool on_boundary(const void *p, long long b, long long h, long long n, size_t bytes) {
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(b * bytes) | (uintptr_t)(h * bytes) |
                              (uintptr_t)(n * bytes)) & 15) == 0;
 }
 
-template <typename T, int G, Layout L, bool BWD> cudaError_t launch(const RotArgs &a, int ctas, bool norm, cudaStream_t st) {
-    const size_t smem = BWD && norm && a.ws ? (size_t)(kThreads / G) * 2 * a.D * sizeof(float) : 0;
-    if (norm) rotate_kernel<T, G, L, BWD, true><<<ctas, kThreads, smem, st>>>(a);
-    else rotate_kernel<T, G, L, BWD, false><<<ctas, kThreads, smem, st>>>(a);
+template <typename T, int V, int G, Layout L, bool BWD>
+cudaError_t launch(const RotArgs &a, int ctas, bool norm, cudaStream_t st) {
+    const size_t smem = BWD && norm && a.ws ? (size_t)(kThreads / G) * a.D * sizeof(float) : 0;
+    const dim3 grid(ctas, BWD ? 2 : 1);
+    if (norm) rotate_kernel<T, V, G, L, BWD, true><<<grid, kThreads, smem, st>>>(a);
+    else rotate_kernel<T, V, G, L, BWD, false><<<grid, kThreads, smem, st>>>(a);
     count_launches(1);
     return cudaGetLastError();
 }
 
-template <typename T, bool BWD> cudaError_t pick(const RotArgs &a, int G, Layout l, int ctas, bool norm, cudaStream_t st) {
-    if (l == kAny) return launch<T, 32, kAny, BWD>(a, ctas, norm, st);
-    if (l == kHalf) {
-        if (G == 8) return launch<T, 8, kHalf, BWD>(a, ctas, norm, st);
-        return G == 16 ? launch<T, 16, kHalf, BWD>(a, ctas, norm, st) : launch<T, 32, kHalf, BWD>(a, ctas, norm, st);
-    }
-    if (G == 8) return launch<T, 8, kAdjacent, BWD>(a, ctas, norm, st);
-    return G == 16 ? launch<T, 16, kAdjacent, BWD>(a, ctas, norm, st) : launch<T, 32, kAdjacent, BWD>(a, ctas, norm, st);
+// Lanes to a token where rows are taken by pieces of V values: what D takes, rounded up.
+template <typename T> int lanes_of(int D) {
+    constexpr int V = 16 / sizeof(T), least = 32 / V;   // 4 (bf16) or 8 (fp32) lanes: D = 64
+    return D <= 64 ? least : D <= 128 ? 2 * least : 4 * least;
+}
+
+template <typename T, Layout L, bool BWD> cudaError_t pick_lanes(const RotArgs &a, int ctas, bool norm, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T), least = 32 / V;
+    const int G = lanes_of<T>(a.D);
+    if (G == least) return launch<T, V, least, L, BWD>(a, ctas, norm, st);
+    return G == 2 * least ? launch<T, V, 2 * least, L, BWD>(a, ctas, norm, st) : launch<T, V, 4 * least, L, BWD>(a, ctas, norm, st);
+}
+
+template <typename T, bool BWD> cudaError_t pick(const RotArgs &a, Layout l, int ctas, bool norm, cudaStream_t st) {
+    if (l == kHalf) return pick_lanes<T, kHalf, BWD>(a, ctas, norm, st);
+    if (l == kAdjacent) return pick_lanes<T, kAdjacent, BWD>(a, ctas, norm, st);
+    return a.D <= 128 ? launch<T, 2, 32, kAny, BWD>(a, ctas, norm, st) : launch<T, 4, 32, kAny, BWD>(a, ctas, norm, st);
 }
 
 cudaError_t rotate(const RotateProblem &p, bool bwd) {
@@ -384,7 +425,8 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
     const bool half = p.rot.pairs == LA_PAIRS_HALF;
     const la_view x[2] = {p.q, p.k}, y[2] = {p.qo, p.ko}, dy[2] = {p.dqo, p.dko};
     const size_t size = p.s.dtype == LA_DTYPE_F32 ? 4 : 2;
-    bool wide = p.s.D % 8 == 0 && (!half || p.rot.P % 4 == 0);
+    const int V = 16 / (int)size;
+    bool wide = p.s.D % (2 * V) == 0 && (!half || p.rot.P % V == 0);
     for (int s = 0; s < 2; s++) {
         a.H[s] = s ? p.s.Hk : p.s.Hq;
         a.x[s] = x[s].data, a.y[s] = y[s].data, a.dy[s] = dy[s].data;
@@ -406,7 +448,7 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
     // 16 byte pieces where every row allows them, else single values, 32 lanes to a token
     const Layout l = !wide ? kAny : half ? kHalf : kAdjacent;
     a.half = half;
-    const int G = l == kAny || p.s.D > 128 ? 32 : p.s.D > 64 ? 16 : 8;
+    const int G = l == kAny ? 32 : size == 4 ? lanes_of<float>(p.s.D) : lanes_of<__nv_bfloat16>(p.s.D);
     const long long tokens = (long long)p.s.B * p.s.N, per = kThreads / G;
     // a token's heads are shared by as many groups as it takes to fill the SMs
     const int heads = std::max(p.s.Hq, p.s.Hk);
@@ -417,10 +459,10 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
     a.ws = sums ? static_cast<float *>(p.ws) : nullptr;
     const long long ctas = std::min((tokens * splits + per - 1) / per, bwd && p.norm ? (long long)kBwdCtas : 1LL << 30);
     const bool f32 = p.s.dtype == LA_DTYPE_F32;
-    cudaError_t e = bwd ? (f32 ? pick<float, true>(a, G, l, (int)ctas, p.norm, p.stream)
-                               : pick<__nv_bfloat16, true>(a, G, l, (int)ctas, p.norm, p.stream))
-                        : (f32 ? pick<float, false>(a, G, l, (int)ctas, p.norm, p.stream)
-                               : pick<__nv_bfloat16, false>(a, G, l, (int)ctas, p.norm, p.stream));
+    cudaError_t e = bwd ? (f32 ? pick<float, true>(a, l, (int)ctas, p.norm, p.stream)
+                               : pick<__nv_bfloat16, true>(a, l, (int)ctas, p.norm, p.stream))
+                        : (f32 ? pick<float, false>(a, l, (int)ctas, p.norm, p.stream)
+                               : pick<__nv_bfloat16, false>(a, l, (int)ctas, p.norm, p.stream));
     if (e != cudaSuccess || !sums) return e;
     weight_sums_kernel<<<(2 * p.s.D + 31) / 32, 256, 0, p.stream>>>(a.ws, (int)ctas, p.s.D, p.dwq, p.dwk);
     count_launches(1);
