@@ -1,5 +1,5 @@
 // la_decay.cu - linear attention with a decay for each head: sweeps in fp32
-// arithmetic on CUDA cores (fp32 data, rows off 16 bytes), the scan of the
+// arithmetic on CUDA cores (fp32 data, bf16 rows off 16 bytes), the scan of the
 // segments' states, and the step of one token.
 #include <algorithm>
 
@@ -10,7 +10,7 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 32;      // tokens a chunk
+constexpr int kRows = 64;      // tokens a chunk
 constexpr int kCols = 64;      // columns of z that a CTA takes
 constexpr int kSms = 152;
 
@@ -23,15 +23,57 @@ __device__ __forceinline__ const T *row_of(const la_view &v, long long b, int h,
     return static_cast<const T *>(v.data) + b * v.sb + h * v.sh + t * v.sn;
 }
 
+// Shared memory of a CTA (floats): x and y [kRows][ld], z and the weighted z
+// [kRows][kCols], the scores [kRows][kRows + 4], the state [64 DT][kCols], decays.
+// Rows are 4 floats longer than a multiple of 4, so that eight rows' 16-byte pieces
+// lie in different banks.
+constexpr int row_floats(int D) { return (D + 3) / 4 * 4 + 4; }
+constexpr int kScores = kRows + 4;
 size_t sweep_smem(int D) {
-    return sizeof(float) * ((size_t)D * kCols + 2 * kRows * (D + 1) + kRows * kCols + kRows * (kRows + 1) + kRows + 1);
+    const int dt = D <= 64 ? 1 : 2;
+    return sizeof(float) * ((size_t)2 * kRows * row_floats(D) + 2 * kRows * kCols + kRows * kScores + 64 * dt * kCols + kRows + 4);
 }
 
-// One CTA walks over one segment of one head for up to kCols columns of z, chunk
-// by chunk, the state in shared memory.
+// Rows t0.. of a view into shared memory as fp32, columns c0..c0 + n - 1; zeros
+// behind `rows` rows and `n` columns (up to a multiple of 4).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sweep_kernel(const DecayLaunch l) {
-    extern __shared__ float sm[];
+__device__ __forceinline__ void load_rows(float *dst, int ld, const T *src, long long sn, int rows, int n, bool wide) {
+    const int pieces = (n + 3) / 4;
+    for (int i = threadIdx.x; i < kRows * pieces; i += kThreads) {
+        const int r = i / pieces, c = i % pieces * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows) {
+            const T *p = src + (long long)r * sn + c;
+            if constexpr (sizeof(T) == 4) {
+                if (wide) v = *reinterpret_cast<const float4 *>(p);
+            }
+            if (sizeof(T) != 4 || !wide) {
+                v.x = to_f32(p[0]);
+                if (c + 1 < n) v.y = to_f32(p[1]);
+                if (c + 2 < n) v.z = to_f32(p[2]);
+                if (c + 3 < n) v.w = to_f32(p[3]);
+            }
+        }
+        *reinterpret_cast<float4 *>(dst + r * ld + c) = v;
+    }
+}
+
+__device__ __forceinline__ float4 piece(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ void axpy(float4 &acc, float a, const float4 &v) {
+    acc.x = fmaf(a, v.x, acc.x), acc.y = fmaf(a, v.y, acc.y), acc.z = fmaf(a, v.z, acc.z), acc.w = fmaf(a, v.w, acc.w);
+}
+__device__ __forceinline__ float dot(const float4 &a, const float4 &b, float t) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, t))));
+}
+
+// One CTA walks over one segment of one head for up to kCols columns of z, in chunks
+// of kRows tokens.  Every product is taken by tiles of 4 x 4 in registers: threads
+// (ti, tj) of 16 x 16.  The state lies in registers too (rows 4 ti.. and, DT = 2,
+// 64 + 4 ti.., columns 4 tj..) with a copy in shared memory for x S.  Bound by the
+// FMA units: 4 D + 2 kRows of them a token and column.
+template <typename T, int DT>
+__global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const __grid_constant__ DecayLaunch l) {
+    extern __shared__ __align__(16) float sm[];
     int y = blockIdx.y, k = 0;
     for (; k + 1 < l.sweeps; k++) {
         const int blocks = (l.sweep[k].M + kCols - 1) / kCols;
@@ -39,86 +81,198 @@ __global__ void __launch_bounds__(kThreads) sweep_kernel(const DecayLaunch l) {
         y -= blocks;
     }
     const DecaySweep &s = l.sweep[k];
-    const int D = s.D, M = s.M, m0 = y * kCols, cols = min(kCols, M - m0), ld = D + 1;
-    float *S = sm, *X = S + D * kCols, *Y = X + kRows * ld, *Z = Y + kRows * ld, *A = Z + kRows * kCols;
-    float *w = A + kRows * (kRows + 1);   // decays by 0..kRows tokens
+    const int D = s.D, M = s.M, m0 = y * kCols, cols = min(kCols, M - m0), ld = row_floats(D), Dp = (D + 3) / 4 * 4;
+    float *X = sm, *Y = X + kRows * ld, *Z = Y + kRows * ld, *Zw = Z + kRows * kCols, *A = Zw + kRows * kCols;
+    float *S = A + kRows * kScores, *w = S + 64 * DT * kCols;   // w: decays by 0..kRows tokens
     const int seg = blockIdx.x % l.segs, bh = blockIdx.x / l.segs, b = bh / l.H, h = bh % l.H, tid = threadIdx.x;
+    const int ti = tid / 16, tj = tid % 16;
     if (l.sums && seg == (s.backwards ? 0 : l.segs - 1)) return;   // nobody asks for that one
     const float g = l.log_decay[h];
     const int len = l.lens ? max(0, min(l.N, l.lens[b])) : l.N;
     const int first = seg * l.seg_tokens;
     const int n = max(0, min(len - first, l.seg_tokens)), chunks = (n + kRows - 1) / kRows;
     const size_t DM = (size_t)D * M;
+    const bool back = s.backwards != 0;
     const float *start = l.sums || s.start == nullptr ? nullptr
-                                                      : s.start + (l.starts ? (size_t)bh * l.segs + seg : bh) * DM;
+                                                      : s.start + (l.starts ? (size_t)bh * l.segs + seg : (size_t)bh) * DM;
     auto at = [&](int d, int m) { return s.transposed ? (size_t)m * D + d : (size_t)d * M + m; };
-    for (int i = tid; i < D * kCols; i += kThreads) {
-        const int d = i / kCols, m = i % kCols;
-        S[i] = start && m < cols ? start[at(d, m0 + m)] : 0.f;
-    }
+    float4 sv[DT][4];   // rows 64 u + 4 ti + i, columns 4 tj..
+#pragma unroll
+    for (int u = 0; u < DT; u++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int d = 64 * u + 4 * ti + i, m = m0 + 4 * tj;
+            auto get = [&](int j) { return start && d < D && 4 * tj + j < cols ? start[at(d, m + j)] : 0.f; };
+            sv[u][i] = make_float4(get(0), get(1), get(2), get(3));
+        }
+    auto put_state = [&] {
+#pragma unroll
+        for (int u = 0; u < DT; u++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) *reinterpret_cast<float4 *>(S + (64 * u + 4 * ti + i) * kCols + 4 * tj) = sv[u][i];
+    };
+    put_state();
     if (tid <= kRows) w[tid] = decayed(g, tid);
     T *out = static_cast<T *>(s.out.data);
-    if (out) out += b * s.out.sb + h * s.out.sh;
+    if (out) out += b * s.out.sb + h * s.out.sh + m0;
+    // rows by 16 bytes where every one lies on them
+    auto on16 = [&](const la_view &v, int c) {
+        return sizeof(T) == 4 && c % 4 == 0 && ((reinterpret_cast<uintptr_t>(v.data) & 15) | (v.sb & 3) | (v.sh & 3) | (v.sn & 3)) == 0;
+    };
+    const bool xw = on16(s.x, D), yw = on16(s.y, D), zw = on16(s.z, cols), ow = on16(s.out, cols);
     for (int it = 0; it < chunks; it++) {
-        const int c = s.backwards ? chunks - 1 - it : it;
-        const int t0 = first + c * kRows, rows = min(kRows, n - c * kRows);
+        const int c = back ? chunks - 1 - it : it, t0 = first + c * kRows, rows = min(kRows, n - c * kRows);
         __syncthreads();
-        for (int i = tid; i < kRows * D; i += kThreads) {
-            const int r = i / D, d = i % D;
-            X[r * ld + d] = out && r < rows ? to_f32(row_of<T>(s.x, b, h, t0 + r)[d]) : 0.f;
-            Y[r * ld + d] = r < rows ? to_f32(row_of<T>(s.y, b, h, t0 + r)[d]) : 0.f;
-        }
-        for (int i = tid; i < kRows * kCols; i += kThreads) {
-            const int r = i / kCols, m = i % kCols;
-            Z[i] = r < rows && m < cols ? to_f32(row_of<T>(s.z, b, h, t0 + r)[m0 + m]) : 0.f;
-        }
+        if (out) load_rows(X, ld, row_of<T>(s.x, b, h, t0), s.x.sn, rows, D, xw);
+        load_rows(Y, ld, row_of<T>(s.y, b, h, t0), s.y.sn, rows, D, yw);
+        load_rows(Z, kCols, row_of<T>(s.z, b, h, t0) + m0, s.z.sn, rows, cols, zw);
         __syncthreads();
+        for (int i = tid; i < kRows * kCols / 4; i += kThreads) {   // z weighed for the state
+            const int r = i / (kCols / 4);
+            const float by = r < rows ? w[back ? r + 1 : rows - 1 - r] : 0.f;
+            const float4 v = piece(Z + 4 * i);
+            *reinterpret_cast<float4 *>(Zw + 4 * i) = make_float4(by * v.x, by * v.y, by * v.z, by * v.w);
+        }
         if (out) {
-            for (int i = tid; i < kRows * kRows; i += kThreads) {
-                const int r = i / kRows, j = i % kRows, e = s.backwards ? j - r : r - j;
-                float t = 0.f;
-                if (e >= 0 && r < rows && j < rows) {
-                    for (int d = 0; d < D; d++) t = fmaf(X[r * ld + d], Y[j * ld + d], t);
-                    t *= w[e];
+            // scores: the 136 tiles on and below the diagonal (backwards: above), decayed
+            if (tid < 136) {
+                int pi = (int)((sqrtf(8.f * tid + 1.f) - 1.f) * 0.5f);
+                while (pi * (pi + 1) / 2 > tid) pi--;
+                while ((pi + 1) * (pi + 2) / 2 <= tid) pi++;
+                const int pj = tid - pi * (pi + 1) / 2;
+                const int i0 = 4 * (back ? pj : pi), j0 = 4 * (back ? pi : pj);
+                float p[4][4] = {};
+                for (int d = 0; d < Dp; d += 4) {
+                    float4 x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) x[i] = piece(X + (i0 + i) * ld + d);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const float4 v = piece(Y + (j0 + j) * ld + d);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) p[i][j] = dot(x[i], v, p[i][j]);
+                    }
                 }
-                A[r * (kRows + 1) + j] = t;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    float q[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int e = back ? j0 + j - i0 - i : i0 + i - j0 - j;
+                        q[j] = e >= 0 ? p[i][j] * w[e] : 0.f;
+                    }
+                    *reinterpret_cast<float4 *>(A + (i0 + i) * kScores + j0) = make_float4(q[0], q[1], q[2], q[3]);
+                }
             }
             __syncthreads();
-            for (int i = tid; i < rows * kCols; i += kThreads) {
-                const int r = i / kCols, m = i % kCols;
-                if (m >= cols) continue;
-                float intra = 0.f, inter = 0.f;
-                const int j0 = s.backwards ? r : 0, j1 = s.backwards ? rows : r + 1;
-                for (int j = j0; j < j1; j++) intra = fmaf(A[r * (kRows + 1) + j], Z[j * kCols + m], intra);
-                for (int d = 0; d < D; d++) inter = fmaf(X[r * ld + d], S[d * kCols + m], inter);
-                const float by = w[s.backwards ? rows - 1 - r : r + 1];
-                out[(long long)(t0 + r) * s.out.sn + m0 + m] =
-                    from_f32<T>(fmaf(s.c_intra, intra, s.c_inter * by * inter));
+            // output rows 4 ti.., columns 4 tj..: x S, then the scores' part
+            float4 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int d = 0; d < Dp; d += 4) {
+                float4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) v[j] = piece(S + (d + j) * kCols + 4 * tj);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float4 x = piece(X + (4 * ti + i) * ld + d);
+                    axpy(o[i], x.x, v[0]), axpy(o[i], x.y, v[1]), axpy(o[i], x.z, v[2]), axpy(o[i], x.w, v[3]);
+                }
             }
-            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = 4 * ti + i;
+                const float by = r < rows ? s.c_inter * w[back ? rows - 1 - r : r + 1] : 0.f;
+                o[i] = make_float4(by * o[i].x, by * o[i].y, by * o[i].z, by * o[i].w);
+            }
+            float4 q[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int j_first = back ? 4 * ti + 4 : 0, j_end = back ? (rows + 3) / 4 * 4 : 4 * ti;
+            for (int j = j_first; j < j_end; j += 4) {
+                float4 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[e] = piece(Z + (j + e) * kCols + 4 * tj);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float4 a = piece(A + (4 * ti + i) * kScores + j);
+                    axpy(q[i], a.x, v[0]), axpy(q[i], a.y, v[1]), axpy(q[i], a.z, v[2]), axpy(q[i], a.w, v[3]);
+                }
+            }
+            // the tile on the diagonal: hidden tokens are left out, whatever they hold
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float4 v = piece(Z + (4 * ti + e) * kCols + 4 * tj);
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (back ? e >= i : e <= i) axpy(q[i], A[(4 * ti + i) * kScores + 4 * ti + e], v);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int r = 4 * ti + i;
+                if (r >= rows) continue;
+                axpy(o[i], s.c_intra, q[i]);
+                T *p = out + (long long)(t0 + r) * s.out.sn + 4 * tj;
+                if constexpr (sizeof(T) == 4) {
+                    if (ow && 4 * tj < cols) {
+                        *reinterpret_cast<float4 *>(p) = o[i];
+                        continue;
+                    }
+                }
+                if (4 * tj < cols) p[0] = from_f32<T>(o[i].x);
+                if (4 * tj + 1 < cols) p[1] = from_f32<T>(o[i].y);
+                if (4 * tj + 2 < cols) p[2] = from_f32<T>(o[i].z);
+                if (4 * tj + 3 < cols) p[3] = from_f32<T>(o[i].w);
+            }
         }
+        __syncthreads();   // the weighed z; S has been read
         const float2 a = kept(g, rows);
-        for (int i = tid; i < D * kCols; i += kThreads) {
-            const int d = i / kCols, m = i % kCols;
-            float t = 0.f;
-            for (int r = 0; r < rows; r++)
-                t = fmaf(Y[r * ld + d] * w[s.backwards ? r + 1 : rows - 1 - r], Z[r * kCols + m], t);
-            S[i] = fmaf(s.c_state, t, keep(a, S[i]));
+        float4 inc[DT][4];
+#pragma unroll
+        for (int u = 0; u < DT; u++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) inc[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int r = 0; r < rows; r++) {
+            const float4 v = piece(Zw + r * kCols + 4 * tj);
+#pragma unroll
+            for (int u = 0; u < DT; u++) {
+                if (64 * u + 4 * ti >= Dp) continue;
+                const float4 d = piece(Y + r * ld + 64 * u + 4 * ti);
+                axpy(inc[u][0], d.x, v), axpy(inc[u][1], d.y, v), axpy(inc[u][2], d.z, v), axpy(inc[u][3], d.w, v);
+            }
         }
+#pragma unroll
+        for (int u = 0; u < DT; u++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float4 &t = sv[u][i];
+                const float4 &e = inc[u][i];
+                t = make_float4(fmaf(s.c_state, e.x, keep(a, t.x)), fmaf(s.c_state, e.y, keep(a, t.y)),
+                                fmaf(s.c_state, e.z, keep(a, t.z)), fmaf(s.c_state, e.w, keep(a, t.w)));
+            }
+        if (out) put_state();
     }
-    __syncthreads();
     // the state leaves where the sequence's last segment (backwards: its first) ends
     const int last = max(0, (len + l.seg_tokens - 1) / l.seg_tokens - 1);
-    if (s.end && (l.sums || seg == (s.backwards ? 0 : last))) {
-        float *end = s.end + (l.sums ? (size_t)bh * l.segs + seg : bh) * DM;
-        for (int i = tid; i < D * kCols; i += kThreads) {
-            const int d = i / kCols, m = i % kCols;
-            if (m < cols) end[at(d, m0 + m)] = S[i];
-        }
+    if (s.end && (l.sums || seg == (back ? 0 : last))) {
+        float *end = s.end + (l.sums ? (size_t)bh * l.segs + seg : (size_t)bh) * DM;
+#pragma unroll
+        for (int u = 0; u < DT; u++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int d = 64 * u + 4 * ti + i, m = m0 + 4 * tj;
+                const float v[4] = {sv[u][i].x, sv[u][i].y, sv[u][i].z, sv[u][i].w};
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (d < D && 4 * tj + j < cols) end[at(d, m + j)] = v[j];
+            }
     }
     if (out)   // rows past the length
-        for (int t = first + n; t < min(first + l.seg_tokens, l.N); t++)
-            for (int m = tid; m < cols; m += kThreads) out[(long long)t * s.out.sn + m0 + m] = from_f32<T>(0.f);
+        for (int i = tid; i < (min(first + l.seg_tokens, l.N) - first - n) * kCols; i += kThreads) {
+            const int t = first + n + i / kCols, m = i % kCols;
+            if (m < cols) out[(long long)t * s.out.sn + m] = from_f32<T>(0.f);
+        }
 }
 
 // Sums of the segments [B*H][segs][DM] become the states at their starts (for
@@ -254,44 +408,58 @@ struct Cut {
     int segs, tokens;
 };
 
-// Segments of a sequence.  `ctas` walk over the whole sequences side by side, one to
-// an SM; cut, there are `segs` times as many, which have first to find the states at
-// their starts: `sums` CTAs a segment, then a scan that moves `states` bytes a segment.
-// In chunks of 128 tokens (about 2.1 us): a CTA's start and end cost six, a chunk's sums
-// 0.9, a scan's launch two.  16 heads of 65536 tokens, D = M = 128: 4 segments 519 us,
-// 19 566; 16 heads of 16384, backward: 1 segment 278 us, 3 303.
-Cut cut_of(long long ctas, long long sums, double states, int N) {
-    const long long chunks = ((long long)N + 127) / 128;
+// What a walk costs, in chunks of 128 tokens: a CTA's start and end, a chunk's sums
+// alone, a scan's launch; the chunk's time; CTAs that an SM holds.
+struct Cost {
+    double start, sums, scan, us;
+    int slots;
+};
+// tensor cores (bf16) and FMA units
+constexpr Cost kTensor = {6.0, 0.9, 2.0, 2.1, 1}, kFma64 = {0.5, 0.4, 0.4, 13.0, 2}, kFma128 = {0.5, 0.4, 0.4, 20.0, 1};
+
+// Segments of a sequence.  `ctas` walk over the whole sequences side by side; cut,
+// there are `segs` times as many, which have first to find the states at their
+// starts: `sums` CTAs a segment, then a scan that moves `states` bytes a segment.
+// Tensor cores, 16 heads of 65536 tokens, D = M = 128: 4 segments 519 us, 19 566; 16
+// heads of 16384, backward: 1 segment 278 us, 3 303.
+Cut cut_of(long long ctas, long long sums, double states, int N, const Cost &cost) {
+    const long long chunks = ((long long)N + 127) / 128, slots = (long long)kSms * cost.slots;
     long long best = 1;
     double least = 0;
-    for (long long segs = 1; segs <= std::min<long long>(chunks, 4 * kSms) && (segs == 1 || ctas * segs <= 4 * kSms); segs++) {
+    for (long long segs = 1; segs <= std::min(chunks, 4 * slots) && (segs == 1 || ctas * segs <= 4 * slots); segs++) {
         const long long per = (chunks + segs - 1) / segs;
         if (segs > 1 && (chunks + per - 1) / per != segs) continue;   // the same as fewer
-        auto waves = [&](long long n) { return (n + kSms - 1) / kSms; };
-        double cost = waves(ctas * segs) * (per + 6.0);
-        if (segs > 1) cost += waves(sums * (segs - 1)) * (0.9 * per + 6) + 2 + segs * states / (6.5e6 * 2.1);
-        if (segs == 1 || cost < least) best = segs, least = cost;
+        auto waves = [&](long long n) { return (n + slots - 1) / slots; };
+        double t = waves(ctas * segs) * (per + cost.start);
+        if (segs > 1)
+            t += waves(sums * (segs - 1)) * (cost.sums * per + cost.start) + cost.scan + segs * states / (6.5e6 * cost.us);
+        if (segs == 1 || t < least) best = segs, least = t;
     }
     const long long per = (chunks + best - 1) / best;
     return {(int)best, best == 1 ? std::max(N, 1) : (int)(per * 128)};
 }
 int blocks_of(int w) { return (w + kCols - 1) / kCols; }
-Cut cut_of(int B, int H, int N, int D, int M, bool backward) {
+Cut cut_of(int B, int H, int N, int D, int M, la_dtype dtype, bool backward) {
     const long long heads = (long long)B * H, d = blocks_of(D), m = blocks_of(M);
     const double states = 16.0 * heads * D * M;   // written, scanned, read
-    return backward ? cut_of(heads * (2 * d + m), heads * 2 * m, 2 * states, N) : cut_of(heads * m, heads * m, states, N);
+    const Cost &cost = dtype == LA_DTYPE_BF16 ? kTensor : std::max(D, backward ? M : D) <= 64 ? kFma64 : kFma128;
+    return backward ? cut_of(heads * (2 * d + m), heads * 2 * m, 2 * states, N, cost)
+                    : cut_of(heads * m, heads * m, states, N, cost);
+}
+
+template <typename T, int DT> cudaError_t simt_launch(const DecayLaunch &l, int blocks, int D) {
+    cudaError_t e = cudaFuncSetAttribute(sweep_kernel<T, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sweep_smem(64 * DT));
+    if (e != cudaSuccess) return e;
+    sweep_kernel<T, DT><<<dim3((unsigned)((long long)l.B * l.H * l.segs), blocks), kThreads, sweep_smem(D), l.stream>>>(l);
+    count_launches(1);
+    return cudaGetLastError();
 }
 
 template <typename T> cudaError_t simt_decay(const DecayLaunch &l) {
     int blocks = 0, D = 0;
     for (int i = 0; i < l.sweeps; i++) blocks += blocks_of(l.sweep[i].M), D = std::max(D, l.sweep[i].D);
-    const size_t smem = sweep_smem(D);
-    cudaError_t e = cudaFuncSetAttribute(sweep_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sweep_smem(kDecayMaxD));
-    if (e != cudaSuccess) return e;
-    sweep_kernel<T><<<dim3((unsigned)((long long)l.B * l.H * l.segs), blocks), kThreads, smem, l.stream>>>(l);
-    count_launches(1);
-    return cudaGetLastError();
+    return D <= 64 ? simt_launch<T, 1>(l, blocks, D) : simt_launch<T, 2>(l, blocks, D);
 }
 
 cudaError_t run(const DecayLaunch &l, la_dtype dtype) {
@@ -316,13 +484,13 @@ DecayLaunch launch_of(const DecayProblem &p, const Cut &cut) {
 }  // namespace
 
 size_t decay_ws_bytes(const la_shape &s, bool backward) {
-    const Cut c = cut_of(s.B, s.H, s.N, s.D, s.M, backward);
+    const Cut c = cut_of(s.B, s.H, s.N, s.D, s.M, s.dtype, backward);
     if (c.segs == 1) return 0;
     return (size_t)s.B * s.H * c.segs * s.D * s.M * sizeof(float) * (backward ? 2 : 1);
 }
 
 cudaError_t decay_forward(const DecayProblem &p) {
-    DecayLaunch l = launch_of(p, cut_of(p.B, p.H, p.N, p.D, p.M, false));
+    DecayLaunch l = launch_of(p, cut_of(p.B, p.H, p.N, p.D, p.M, p.dtype, false));
     const la_view none{nullptr, 0, 0, 0};
     l.sweeps = 1;
     DecaySweep &s = l.sweep[0];
@@ -343,7 +511,7 @@ cudaError_t decay_forward(const DecayProblem &p) {
 }
 
 cudaError_t decay_backward(const DecayProblem &p) {
-    DecayLaunch l = launch_of(p, cut_of(p.B, p.H, p.N, p.D, p.M, true));
+    DecayLaunch l = launch_of(p, cut_of(p.B, p.H, p.N, p.D, p.M, p.dtype, true));
     const la_view none{nullptr, 0, 0, 0};
     const int DM = p.D * p.M;
     const float *S0 = p.S0, *dSN = p.dSN;
