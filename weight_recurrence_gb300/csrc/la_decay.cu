@@ -23,39 +23,46 @@ __device__ __forceinline__ const T *row_of(const la_view &v, long long b, int h,
     return static_cast<const T *>(v.data) + b * v.sb + h * v.sh + t * v.sn;
 }
 
-// Shared memory of a CTA (floats): x and y [kRows][ld], z and the weighted z
+// Shared memory of a CTA (floats): x and y [kRows][64 DT], z and the weighted z
 // [kRows][kCols], the scores [kRows][kRows + 4], the state [64 DT][kCols], decays.
-// Rows are 4 floats longer than a multiple of 4, so that eight rows' 16-byte pieces
-// lie in different banks.
-constexpr int row_floats(int D) { return (D + 3) / 4 * 4 + 4; }
 constexpr int kScores = kRows + 4;
-size_t sweep_smem(int D) {
-    const int dt = D <= 64 ? 1 : 2;
-    return sizeof(float) * ((size_t)2 * kRows * row_floats(D) + 2 * kRows * kCols + kRows * kScores + 64 * dt * kCols + kRows + 4);
+constexpr size_t sweep_smem(int dt) {
+    return sizeof(float) * ((size_t)2 * kRows * 64 * dt + 2 * kRows * kCols + kRows * kScores + 64 * dt * kCols + kRows + 4);
 }
 
-// Rows t0.. of a view into shared memory as fp32, columns c0..c0 + n - 1; zeros
-// behind `rows` rows and `n` columns (up to a multiple of 4).
-template <typename T>
-__device__ __forceinline__ void load_rows(float *dst, int ld, const T *src, long long sn, int rows, int n, bool wide) {
-    const int pieces = (n + 3) / 4;
-    for (int i = threadIdx.x; i < kRows * pieces; i += kThreads) {
-        const int r = i / pieces, c = i % pieces * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
+// Where the 16-byte piece p of row r of x or y lies: threads read rows 4 apart at the
+// same time, so each four rows turn the pieces' order by one.
+template <int DT> __device__ __forceinline__ int place(int r, int p) { return r * 64 * DT + 4 * (p ^ (r >> 2 & 7)); }
+
+// A thread's share of kRows rows of up to 64 U columns: pieces of four values, 16
+// threads to a row.  Zeros behind `rows` rows and `n` columns.
+template <typename T, int U>
+__device__ __forceinline__ void fetch(float4 (&v)[4 * U], const T *src, long long sn, int rows, int n, bool wide) {
+    const int c0 = threadIdx.x % 16 * 4, r0 = threadIdx.x / 16;
+#pragma unroll
+    for (int i = 0; i < 4 * U; i++) {
+        const int r = r0 + 16 * (i % 4), c = c0 + 64 * (i / 4);
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && c < n) {
             const T *p = src + (long long)r * sn + c;
             if constexpr (sizeof(T) == 4) {
-                if (wide) v = *reinterpret_cast<const float4 *>(p);
+                if (wide) {
+                    v[i] = *reinterpret_cast<const float4 *>(p);
+                    continue;
+                }
             }
-            if (sizeof(T) != 4 || !wide) {
-                v.x = to_f32(p[0]);
-                if (c + 1 < n) v.y = to_f32(p[1]);
-                if (c + 2 < n) v.z = to_f32(p[2]);
-                if (c + 3 < n) v.w = to_f32(p[3]);
-            }
+            v[i].x = to_f32(p[0]);
+            if (c + 1 < n) v[i].y = to_f32(p[1]);
+            if (c + 2 < n) v[i].z = to_f32(p[2]);
+            if (c + 3 < n) v[i].w = to_f32(p[3]);
         }
-        *reinterpret_cast<float4 *>(dst + r * ld + c) = v;
     }
+}
+template <int DT> __device__ __forceinline__ void put_rows(float *dst, const float4 (&v)[4 * DT]) {
+    const int p0 = threadIdx.x % 16, r0 = threadIdx.x / 16;
+#pragma unroll
+    for (int i = 0; i < 4 * DT; i++)
+        *reinterpret_cast<float4 *>(dst + place<DT>(r0 + 16 * (i % 4), p0 + 16 * (i / 4))) = v[i];
 }
 
 __device__ __forceinline__ float4 piece(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -81,8 +88,8 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
         y -= blocks;
     }
     const DecaySweep &s = l.sweep[k];
-    const int D = s.D, M = s.M, m0 = y * kCols, cols = min(kCols, M - m0), ld = row_floats(D), Dp = (D + 3) / 4 * 4;
-    float *X = sm, *Y = X + kRows * ld, *Z = Y + kRows * ld, *Zw = Z + kRows * kCols, *A = Zw + kRows * kCols;
+    const int D = s.D, M = s.M, m0 = y * kCols, cols = min(kCols, M - m0), Dp = (D + 3) / 4 * 4;
+    float *X = sm, *Y = X + kRows * 64 * DT, *Z = Y + kRows * 64 * DT, *Zw = Z + kRows * kCols, *A = Zw + kRows * kCols;
     float *S = A + kRows * kScores, *w = S + 64 * DT * kCols;   // w: decays by 0..kRows tokens
     const int seg = blockIdx.x % l.segs, bh = blockIdx.x / l.segs, b = bh / l.H, h = bh % l.H, tid = threadIdx.x;
     const int ti = tid / 16, tj = tid % 16;
@@ -113,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
     };
     put_state();
     if (tid <= kRows) w[tid] = decayed(g, tid);
+    __syncthreads();
     T *out = static_cast<T *>(s.out.data);
     if (out) out += b * s.out.sb + h * s.out.sh + m0;
     // rows by 16 bytes where every one lies on them
@@ -122,16 +130,23 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
     const bool xw = on16(s.x, D), yw = on16(s.y, D), zw = on16(s.z, cols), ow = on16(s.out, cols);
     for (int it = 0; it < chunks; it++) {
         const int c = back ? chunks - 1 - it : it, t0 = first + c * kRows, rows = min(kRows, n - c * kRows);
-        __syncthreads();
-        if (out) load_rows(X, ld, row_of<T>(s.x, b, h, t0), s.x.sn, rows, D, xw);
-        load_rows(Y, ld, row_of<T>(s.y, b, h, t0), s.y.sn, rows, D, yw);
-        load_rows(Z, kCols, row_of<T>(s.z, b, h, t0) + m0, s.z.sn, rows, cols, zw);
-        __syncthreads();
-        for (int i = tid; i < kRows * kCols / 4; i += kThreads) {   // z weighed for the state
-            const int r = i / (kCols / 4);
-            const float by = r < rows ? w[back ? r + 1 : rows - 1 - r] : 0.f;
-            const float4 v = piece(Z + 4 * i);
-            *reinterpret_cast<float4 *>(Zw + 4 * i) = make_float4(by * v.x, by * v.y, by * v.z, by * v.w);
+        {
+            // all of the chunk's loads on their way, then into shared memory
+            float4 vx[4 * DT], vy[4 * DT], vz[4];
+            if (out) fetch<T, DT>(vx, row_of<T>(s.x, b, h, t0), s.x.sn, rows, D, xw);
+            fetch<T, DT>(vy, row_of<T>(s.y, b, h, t0), s.y.sn, rows, D, yw);
+            fetch<T, 1>(vz, row_of<T>(s.z, b, h, t0) + m0, s.z.sn, rows, cols, zw);
+            __syncthreads();   // the last chunk's have been read
+            if (out) put_rows<DT>(X, vx);
+            put_rows<DT>(Y, vy);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {   // z, and z weighed for the state
+                const int r = ti + 16 * i;
+                const float by = r < rows ? w[back ? r + 1 : rows - 1 - r] : 0.f;
+                *reinterpret_cast<float4 *>(Z + r * kCols + 4 * tj) = vz[i];
+                *reinterpret_cast<float4 *>(Zw + r * kCols + 4 * tj) = make_float4(by * vz[i].x, by * vz[i].y, by * vz[i].z, by * vz[i].w);
+            }
+            __syncthreads();
         }
         if (out) {
             // scores: the 136 tiles on and below the diagonal (backwards: above), decayed
@@ -145,10 +160,10 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
                 for (int d = 0; d < Dp; d += 4) {
                     float4 x[4];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) x[i] = piece(X + (i0 + i) * ld + d);
+                    for (int i = 0; i < 4; i++) x[i] = piece(X + place<DT>(i0 + i, d / 4));
 #pragma unroll
                     for (int j = 0; j < 4; j++) {
-                        const float4 v = piece(Y + (j0 + j) * ld + d);
+                        const float4 v = piece(Y + place<DT>(j0 + j, d / 4));
 #pragma unroll
                         for (int i = 0; i < 4; i++) p[i][j] = dot(x[i], v, p[i][j]);
                     }
@@ -175,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
                 for (int j = 0; j < 4; j++) v[j] = piece(S + (d + j) * kCols + 4 * tj);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    const float4 x = piece(X + (4 * ti + i) * ld + d);
+                    const float4 x = piece(X + place<DT>(4 * ti + i, d / 4));
                     axpy(o[i], x.x, v[0]), axpy(o[i], x.y, v[1]), axpy(o[i], x.z, v[2]), axpy(o[i], x.w, v[3]);
                 }
             }
@@ -238,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
 #pragma unroll
             for (int u = 0; u < DT; u++) {
                 if (64 * u + 4 * ti >= Dp) continue;
-                const float4 d = piece(Y + r * ld + 64 * u + 4 * ti);
+                const float4 d = piece(Y + place<DT>(r, 16 * u + ti));
                 axpy(inc[u][0], d.x, v), axpy(inc[u][1], d.y, v), axpy(inc[u][2], d.z, v), axpy(inc[u][3], d.w, v);
             }
         }
@@ -447,11 +462,11 @@ Cut cut_of(int B, int H, int N, int D, int M, la_dtype dtype, bool backward) {
                     : cut_of(heads * m, heads * m, states, N, cost);
 }
 
-template <typename T, int DT> cudaError_t simt_launch(const DecayLaunch &l, int blocks, int D) {
+template <typename T, int DT> cudaError_t simt_launch(const DecayLaunch &l, int blocks) {
     cudaError_t e = cudaFuncSetAttribute(sweep_kernel<T, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sweep_smem(64 * DT));
+                                         (int)sweep_smem(DT));
     if (e != cudaSuccess) return e;
-    sweep_kernel<T, DT><<<dim3((unsigned)((long long)l.B * l.H * l.segs), blocks), kThreads, sweep_smem(D), l.stream>>>(l);
+    sweep_kernel<T, DT><<<dim3((unsigned)((long long)l.B * l.H * l.segs), blocks), kThreads, sweep_smem(DT), l.stream>>>(l);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -459,7 +474,7 @@ template <typename T, int DT> cudaError_t simt_launch(const DecayLaunch &l, int 
 template <typename T> cudaError_t simt_decay(const DecayLaunch &l) {
     int blocks = 0, D = 0;
     for (int i = 0; i < l.sweeps; i++) blocks += blocks_of(l.sweep[i].M), D = std::max(D, l.sweep[i].D);
-    return D <= 64 ? simt_launch<T, 1>(l, blocks, D) : simt_launch<T, 2>(l, blocks, D);
+    return D <= 64 ? simt_launch<T, 1>(l, blocks) : simt_launch<T, 2>(l, blocks);
 }
 
 cudaError_t run(const DecayLaunch &l, la_dtype dtype) {
