@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
                 const int pj = tid - pi * (pi + 1) / 2;
                 const int i0 = 4 * (back ? pj : pi), j0 = 4 * (back ? pi : pj);
                 float p[4][4] = {};
+#pragma unroll 2
                 for (int d = 0; d < Dp; d += 4) {
                     float4 x[4];
 #pragma unroll
@@ -184,6 +185,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
             float4 o[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
             for (int d = 0; d < Dp; d += 4) {
                 float4 v[4];
 #pragma unroll
@@ -204,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
 #pragma unroll
             for (int i = 0; i < 4; i++) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             const int j_first = back ? 4 * ti + 4 : 0, j_end = back ? (rows + 3) / 4 * 4 : 4 * ti;
+#pragma unroll 2
             for (int j = j_first; j < j_end; j += 4) {
                 float4 v[4];
 #pragma unroll
@@ -247,14 +250,17 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
         for (int u = 0; u < DT; u++)
 #pragma unroll
             for (int i = 0; i < 4; i++) inc[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int r = 0; r < rows; r++) {
-            const float4 v = piece(Zw + r * kCols + 4 * tj);
+#pragma unroll 2
+        for (int r0 = 0; r0 < kRows; r0 += 4) {   // rows past the end are zeros
+            const int turn = r0 >> 2 & 7;
 #pragma unroll
-            for (int u = 0; u < DT; u++) {
-                if (64 * u + 4 * ti >= Dp) continue;
-                const float4 d = piece(Y + place<DT>(r, 16 * u + ti));
-                axpy(inc[u][0], d.x, v), axpy(inc[u][1], d.y, v), axpy(inc[u][2], d.z, v), axpy(inc[u][3], d.w, v);
+            for (int r = r0; r < r0 + 4; r++) {
+                const float4 v = piece(Zw + r * kCols + 4 * tj);
+#pragma unroll
+                for (int u = 0; u < DT; u++) {
+                    const float4 d = piece(Y + r * 64 * DT + 4 * ((16 * u + ti) ^ turn));
+                    axpy(inc[u][0], d.x, v), axpy(inc[u][1], d.y, v), axpy(inc[u][2], d.z, v), axpy(inc[u][3], d.w, v);
+                }
             }
         }
 #pragma unroll
