@@ -502,21 +502,89 @@ DecayLaunch launch_of(const DecayProblem &p, const Cut &cut) {
     return l;
 }
 
+// ------------------------------------------------------------- rows off 16 bytes
+
+struct PackArgs {
+    la_view v[4];
+    uint4 *to[4];
+    int n[4];      // values of a row
+    int count, H, N;
+    long long rows;
+    const int *lens;
+};
+
+// Rows of n bf16 values to rows of whole 16-byte pieces, zeros behind; rows past a
+// length are left alone.  One tensor to a grid row.
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
+    const la_view &v = a.v[blockIdx.y];
+    const int n = a.n[blockIdx.y], pieces = (n + 7) / 8;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < a.rows * pieces; i += (long long)gridDim.x * 256) {
+        const long long row = i / pieces;
+        const int c = (int)(i - row * pieces) * 8, t = (int)(row % a.N);
+        const long long bh = row / a.N;
+        const int b = (int)(bh / a.H), h = (int)(bh % a.H);
+        if (a.lens && t >= a.lens[b]) continue;
+        const uint16_t *p = static_cast<const uint16_t *>(v.data) + b * v.sb + h * v.sh + t * v.sn + c;
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) o[j] = c + j < n ? p[j] : 0u;
+        a.to[blockIdx.y][i] = make_uint4(o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16);
+    }
+}
+
+// bf16 rows that are not a multiple of 16 bytes long (contiguous ones then lie off
+// those boundaries) are packed first where sequences are long: two passes of memory
+// more, and then the tensor cores (2 heads of 2379 tokens, D = 99, M = 118: 51 us with it,
+// 87 on FMA units; 18 heads of 2 tokens: 38 and 23).
+bool packs(int N, int D, int M, la_dtype dtype) { return dtype == LA_DTYPE_BF16 && N >= 64 && (D % 8 || M % 8); }
+size_t packed_bytes(int B, int H, int N, int n) { return ((size_t)B * H * N * ((n + 7) / 8) * 16 + 255) / 256 * 256; }
+
+// The problem's inputs packed at ws, its views turned to them.
+cudaError_t pack(DecayProblem &p, char *ws, bool backward) {
+    la_view *views[4] = {&p.k, &p.v, backward ? &p.dout : nullptr, backward || p.out.data ? &p.q : nullptr};
+    PackArgs a{};
+    a.H = p.H, a.N = p.N, a.lens = p.lens, a.rows = (long long)p.B * p.H * p.N;
+    long long most = 0;
+    for (int i = 0; i < 4; i++) {
+        if (views[i] == nullptr) continue;
+        const int n = i == 0 || i == 3 ? p.D : p.M, pieces = (n + 7) / 8;
+        a.v[a.count] = *views[i], a.to[a.count] = reinterpret_cast<uint4 *>(ws), a.n[a.count++] = n;
+        const long long row = pieces * 8;
+        *views[i] = {ws, row * p.N * p.H, row * p.N, row};
+        ws += packed_bytes(p.B, p.H, p.N, n);
+        most = std::max(most, a.rows * pieces);
+    }
+    const int ctas = (int)std::min<long long>((most + 255) / 256, kSms * 8);
+    pack_kernel<<<dim3(ctas, a.count), 256, 0, p.stream>>>(a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 size_t decay_ws_bytes(const la_shape &s, bool backward) {
     const Cut c = cut_of(s.B, s.H, s.N, s.D, s.M, s.dtype, backward);
-    if (c.segs == 1) return 0;
-    return (size_t)s.B * s.H * c.segs * s.D * s.M * sizeof(float) * (backward ? 2 : 1);
+    size_t bytes = 0;
+    if (c.segs > 1) bytes += (size_t)s.B * s.H * c.segs * s.D * s.M * sizeof(float) * (backward ? 2 : 1);
+    if (packs(s.N, s.D, s.M, s.dtype))
+        bytes = (bytes + 255) / 256 * 256 + 2 * packed_bytes(s.B, s.H, s.N, s.D) + (backward ? 2 : 1) * packed_bytes(s.B, s.H, s.N, s.M);
+    return bytes;
 }
 
-cudaError_t decay_forward(const DecayProblem &p) {
+cudaError_t decay_forward(const DecayProblem &given) {
+    DecayProblem p = given;
     DecayLaunch l = launch_of(p, cut_of(p.B, p.H, p.N, p.D, p.M, p.dtype, false));
     const la_view none{nullptr, 0, 0, 0};
+    float *ws = static_cast<float *>(p.ws);
+    if (p.out.data == nullptr) p.q = none;
+    if (packs(p.N, p.D, p.M, p.dtype)) {
+        const size_t states = l.segs > 1 ? (size_t)p.B * p.H * l.segs * p.D * p.M * sizeof(float) : 0;
+        const cudaError_t e = pack(p, static_cast<char *>(p.ws) + (states + 255) / 256 * 256, false);
+        if (e != cudaSuccess) return e;
+    }
     l.sweeps = 1;
     DecaySweep &s = l.sweep[0];
     s = {none, p.k, p.v, none, nullptr, nullptr, p.D, p.M, 0, 0, p.scale, p.scale, 1.f};
-    float *ws = static_cast<float *>(p.ws);
     if (l.segs > 1) {
         l.sums = 1;
         s.end = ws;
@@ -531,13 +599,19 @@ cudaError_t decay_forward(const DecayProblem &p) {
     return run(l, p.dtype);
 }
 
-cudaError_t decay_backward(const DecayProblem &p) {
+cudaError_t decay_backward(const DecayProblem &given) {
+    DecayProblem p = given;
     DecayLaunch l = launch_of(p, cut_of(p.B, p.H, p.N, p.D, p.M, p.dtype, true));
     const la_view none{nullptr, 0, 0, 0};
     const int DM = p.D * p.M;
     const float *S0 = p.S0, *dSN = p.dSN;
+    const size_t states = l.segs > 1 ? (size_t)p.B * p.H * l.segs * DM : 0;   // of one direction
+    if (packs(p.N, p.D, p.M, p.dtype)) {
+        const cudaError_t e = pack(p, static_cast<char *>(p.ws) + (2 * states * sizeof(float) + 255) / 256 * 256, true);
+        if (e != cudaSuccess) return e;
+    }
     if (l.segs > 1) {
-        float *wf = static_cast<float *>(p.ws), *wb = wf + (size_t)p.B * p.H * l.segs * DM;
+        float *wf = static_cast<float *>(p.ws), *wb = wf + states;
         l.sums = 1, l.sweeps = 2;
         l.sweep[0] = {none, p.k, p.v, none, nullptr, wf, p.D, p.M, 0, 0, 0.f, 0.f, 1.f};
         l.sweep[1] = {none, p.q, p.dout, none, nullptr, wb, p.D, p.M, 0, 1, 0.f, 0.f, p.scale};

@@ -1,5 +1,6 @@
 // la_tc_decay.cu - linear attention with a decay for each head on tensor cores
-// (tcgen05 + TMA): bf16 rows on 16-byte boundaries.
+// (tcgen05 + TMA): bf16 rows on 16-byte boundaries (the inputs'; outputs lie as they
+// may).
 //
 // One CTA walks over one segment of one head of one sweep (la_decay.h) for 64
 // columns of z, in chunks of C = 128 tokens.  With rows x_i, y_i, z_i of the
@@ -196,7 +197,7 @@ __device__ __noinline__ uint32_t seen_bad(int r, int grp, const uint8_t *note, c
     return hit;
 }
 
-// 16 output values to a row on 16 bytes, `cols` of them.
+// 16 output values to a row, `cols` of them.
 __device__ __noinline__ void store_some(__nv_bfloat16 *row, uint4 a, uint4 b, int cols) {
     for (int i = 0; i < min(cols, 16); i += 8) {
         const uint4 v = i == 0 ? a : b;
@@ -208,7 +209,7 @@ __device__ __noinline__ void store_some(__nv_bfloat16 *row, uint4 a, uint4 b, in
     }
 }
 __device__ __forceinline__ void store16(__nv_bfloat16 *row, uint4 a, uint4 b, int cols) {
-    if (cols < 16) {
+    if (cols < 16 || (reinterpret_cast<uintptr_t>(row) & 15)) {
         store_some(row, a, b, cols);
     } else if ((reinterpret_cast<uintptr_t>(row) & 31) == 0) {   // a whole 32-byte sector
         st_global_v8(row, a, b);
@@ -772,7 +773,7 @@ bool tc_decay_supported(const DecayLaunch &l, la_dtype dtype) {
     if (dtype != LA_DTYPE_BF16) return false;
     for (int i = 0; i < l.sweeps; i++) {
         const DecaySweep &s = l.sweep[i];
-        for (const la_view *v : {&s.x, &s.y, &s.z, &s.out})
+        for (const la_view *v : {&s.x, &s.y, &s.z})
             if (!mappable(*v, l.B, l.H, l.N)) return false;
     }
     return true;
