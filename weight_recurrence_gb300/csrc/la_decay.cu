@@ -156,28 +156,30 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
                 while ((pi + 1) * (pi + 2) / 2 <= tid) pi++;
                 const int pj = tid - pi * (pi + 1) / 2;
                 const int i0 = 4 * (back ? pj : pi), j0 = 4 * (back ? pi : pj);
-                float p[4][4] = {};
+                if (i0 < rows && j0 < rows) {
+                    float p[4][4] = {};
 #pragma unroll 2
-                for (int d = 0; d < Dp; d += 4) {
-                    float4 x[4];
+                    for (int d = 0; d < Dp; d += 4) {
+                        float4 x[4];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) x[i] = piece(X + place<DT>(i0 + i, d / 4));
+                        for (int i = 0; i < 4; i++) x[i] = piece(X + place<DT>(i0 + i, d / 4));
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const float4 v = piece(Y + place<DT>(j0 + j, d / 4));
+                        for (int j = 0; j < 4; j++) {
+                            const float4 v = piece(Y + place<DT>(j0 + j, d / 4));
 #pragma unroll
-                        for (int i = 0; i < 4; i++) p[i][j] = dot(x[i], v, p[i][j]);
+                            for (int i = 0; i < 4; i++) p[i][j] = dot(x[i], v, p[i][j]);
+                        }
                     }
-                }
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    float q[4];
+                    for (int i = 0; i < 4; i++) {
+                        float q[4];
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int e = back ? j0 + j - i0 - i : i0 + i - j0 - j;
-                        q[j] = e >= 0 ? p[i][j] * w[e] : 0.f;
+                        for (int j = 0; j < 4; j++) {
+                            const int e = back ? j0 + j - i0 - i : i0 + i - j0 - j;
+                            q[j] = e >= 0 ? p[i][j] * w[e] : 0.f;
+                        }
+                        *reinterpret_cast<float4 *>(A + (i0 + i) * kScores + j0) = make_float4(q[0], q[1], q[2], q[3]);
                     }
-                    *reinterpret_cast<float4 *>(A + (i0 + i) * kScores + j0) = make_float4(q[0], q[1], q[2], q[3]);
                 }
             }
             __syncthreads();
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
 #pragma unroll
             for (int i = 0; i < 4; i++) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-            for (int d = 0; d < Dp; d += 4) {
+            for (int d = 0; d < (4 * ti < rows ? Dp : 0); d += 4) {
                 float4 v[4];
 #pragma unroll
                 for (int j = 0; j < 4; j++) v[j] = piece(S + (d + j) * kCols + 4 * tj);
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
             float4 q[4];
 #pragma unroll
             for (int i = 0; i < 4; i++) q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int j_first = back ? 4 * ti + 4 : 0, j_end = back ? (rows + 3) / 4 * 4 : 4 * ti;
+            const int j_first = back ? 4 * ti + 4 : 0, j_end = back ? (rows + 3) / 4 * 4 : 4 * ti < rows ? 4 * ti : 0;
 #pragma unroll 2
             for (int j = j_first; j < j_end; j += 4) {
                 float4 v[4];
@@ -251,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
 #pragma unroll
             for (int i = 0; i < 4; i++) inc[u][i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-        for (int r0 = 0; r0 < kRows; r0 += 4) {   // rows past the end are zeros
+        for (int r0 = 0; r0 < rows; r0 += 4) {   // rows past the end are zeros
             const int turn = r0 >> 2 & 7;
 #pragma unroll
             for (int r = r0; r < r0 + 4; r++) {
