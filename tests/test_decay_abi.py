@@ -35,7 +35,8 @@ def _shape(B=2, H=4, N=8, D=16, M=16, dt=F32):
 
 BAD_SHAPES = [(dict(B=-1), INVALID), (dict(H=-1), INVALID), (dict(N=-1), INVALID), (dict(D=0), INVALID),
               (dict(M=0), INVALID), (dict(dt=2), INVALID), (dict(D=129), UNSUPPORTED), (dict(M=256), UNSUPPORTED),
-              (dict(B=1 << 16, H=1 << 13), UNSUPPORTED), (dict(N=0x7fffffff), UNSUPPORTED)]
+              (dict(B=1 << 16, H=1 << 13), UNSUPPORTED), (dict(N=0x7fffffff), UNSUPPORTED),
+              (dict(N=0x7fffffff - (1 << 20) + 1), UNSUPPORTED)]
 BAD_VIEWS = [_v(None), _v(0, off=2), _v(0, sb=-1), _v(0, sn=1 << 41)]
 
 
@@ -69,6 +70,15 @@ def test_decay_forward_refusals(lib):
     assert call(s=long, **views) == INVALID
     assert call(s=long, ws=_p(8), n=need - 1, **views) == INVALID
     assert call(s=long, ws=_p(8, 8), n=need, **views) == INVALID
+    # and bf16 rows that are not whole 16-byte pieces, for their packed copies
+    odd = _shape(N=100, D=33, dt=BF16)
+    need = lib.la_decay_workspace_bytes(odd, 0)
+    assert need >= 2 * 4 * 100 * (2 * 40 + 16) * 2 and lib.la_decay_workspace_bytes(odd, 1) >= need + 2 * 4 * 100 * 16 * 2
+    views = dict(q=_v(0, 1 << 20, 1 << 14, 40), k=_v(1, 1 << 20, 1 << 14, 40), v=_v(2, 1 << 20, 1 << 14, 40),
+                 out=_v(3, 1 << 20, 1 << 14, 40))
+    assert call(s=odd, **views) == INVALID
+    assert call(s=odd, ws=_p(8), n=need - 1, **views) == INVALID
+    assert call(s=odd, ws=_p(8, 8), n=need, **views) == INVALID
     none = _v(None)
     assert call(q=none, k=none, v=none, out=none, g=None, s=_shape(B=0)) == OK
     assert call(q=none, k=none, v=none, out=none, s=_shape(N=0), S0=_p(6), SN=_p(6)) == OK
@@ -205,6 +215,8 @@ def test_binding_refuses_decay_arguments(lib):
         with pytest.raises(TypeError):
             f(**a)
     b = la.la_decay_backward
+    with pytest.raises(RuntimeError):       # no truth value
+        f(q, k, v, g, want_out=torch.zeros(2))
     for bad in [dict(dout=q), dict(dq=v), dict(dv=q), dict(dSN=S[:1]), dict(dS0=S[..., :4])]:
         with pytest.raises(ValueError):
             b(**dict(dict(q=q, k=k, v=v, dout=v, log_decay=g), **bad))
@@ -226,7 +238,7 @@ def test_binding_refuses_rotation_arguments(lib):
         with pytest.raises(ValueError):
             f(**dict(base, **bad))
     for bad in [dict(pos=pos.long()), dict(freq=freq.double()), dict(wq=w.bfloat16()), dict(k=k.bfloat16()),
-                dict(q=q.half(), k=k.half()), dict(eps="x")]:
+                dict(q=q.half(), k=k.half()), dict(eps="x"), dict(axes=8)]:
         with pytest.raises(TypeError):
             f(**dict(base, **bad))
     b = la.la_qk_rotate_backward
@@ -235,6 +247,14 @@ def test_binding_refuses_rotation_arguments(lib):
                 dict(k=None, dko=None, dwk=w)]:
         with pytest.raises(ValueError):
             b(**dict(base, **bad))
+
+
+def test_axes_are_numbers_whatever_holds_them():
+    want = bytes((0, 1, 2, 1))
+    for axes in ((0, 1, 2, 1), [0, 1, 2, 1], want, bytearray(want), torch.tensor([0, 1, 2, 1]),
+                 torch.tensor([0, 1, 2, 1]).numpy()):
+        assert la._axes_bytes(axes) == want
+    assert la._axes_bytes(None) is None
 
 
 def test_views_reach_the_library_as_they_are(lib):

@@ -292,10 +292,8 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
             }
     }
     if (out)   // rows past the length
-        for (int i = tid; i < (min(first + l.seg_tokens, l.N) - first - n) * kCols; i += kThreads) {
-            const int t = first + n + i / kCols, m = i % kCols;
-            if (m < cols) out[(long long)t * s.out.sn + m] = from_f32<T>(0.f);
-        }
+        for (int t = first + n + ti / 4; t < min(first + l.seg_tokens, l.N); t += 4)
+            if (const int m = tid % kCols; m < cols) out[(long long)t * s.out.sn + m] = from_f32<T>(0.f);
 }
 
 // Sums of the segments [B*H][segs][DM] become the states at their starts (for

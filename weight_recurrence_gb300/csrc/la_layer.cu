@@ -119,7 +119,7 @@ la_status check_decay(const la_shape &s) {
     if (s.B < 0 || s.H < 0 || s.N < 0 || s.D < 1 || s.M < 1 || !dtype_ok(s.dtype)) return LA_ERR_INVALID_ARG;
     if (s.D > kDecayMaxD || s.M > kDecayMaxD) return LA_ERR_UNSUPPORTED;
     if ((__int128)s.B * s.H * 8 > 0x7fffffff) return LA_ERR_UNSUPPORTED;
-    if (s.N > 0x7fffffff - 256) return LA_ERR_UNSUPPORTED;
+    if (s.N > 0x7fffffff - (1 << 20)) return LA_ERR_UNSUPPORTED;   // so that segments end below 2^31
     return LA_OK;
 }
 

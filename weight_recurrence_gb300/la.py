@@ -587,7 +587,7 @@ def la_decay_forward(q, k, v, log_decay, scale=1.0, S0=None, SN=None, lens=None,
     state before the first token and after the last; SN may be S0.  lens: int32
     [B]; rows past a length are 0.  want_out=False: the state alone (q may be
     None).  Returns out."""
-    st, out = _bound().decay_forward(q, k, v, log_decay, scale, S0, SN, lens, out, want_out, _handle(stream))
+    st, out = _bound().decay_forward(q, k, v, log_decay, scale, S0, SN, lens, out, bool(want_out), _handle(stream))
     _check(st, "la_decay_forward")
     return out
 
@@ -619,7 +619,8 @@ def _pairs_code(pairs: str) -> int:
 
 
 def _axes_bytes(axes):
-    return None if axes is None else bytes(axes)
+    # (bytes() of an integer or of an array would be something else)
+    return axes if axes is None else bytes(axes if isinstance(axes, (bytes, tuple, list)) else [int(i) for i in axes])
 
 
 def la_qk_rotate_forward(q, k, pos, freq, wq=None, wk=None, eps=1e-6, norm=True, pairs="half", axes=None, qo=None,
