@@ -481,7 +481,8 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
  *       = scale (sum over j <= i of a^(i-j) (q_i.k_j) v_j + a^(i+1) q_i^T S_0)
  * q and k enter as they are (no feature map, no denominator).
  *   q, k: [B,H,N,D]; v, out: [B,H,N,M], views of dtype s.dtype; any
- *      1 <= D, M <= 128 (larger: LA_ERR_UNSUPPORTED).
+ *      1 <= D, M <= 128 (larger: LA_ERR_UNSUPPORTED, as 8 B H >= 2^31 and
+      N >= 2^31 - 2^20).  Inputs may repeat heads or sequences (stride 0).
  *   log_decay: H fp32 values on the device; 0 forgets nothing, -infinity
  *      keeps the token itself alone; above 0 the state grows.
  *   S0, SN: [B,H,D,M] contiguous fp32, the state before the first token
@@ -494,11 +495,13 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
  *   workspace: la_decay_workspace_bytes(s, 0) bytes.
  * A token's NaN and infinities make what sees them not finite, as token by
  * token does; rows that do not see it are what they are without it.
- * bf16 rows on 16-byte boundaries (base and strides) run on tensor cores,
- * their outputs the sums of bf16 products with the masked scores and the state
- * rounded to bf16 once; the state itself takes the products of the rows as
- * they are, its weights by three bf16 parts, in fp32.  fp32 data, and bf16
- * off those boundaries, run fp32 arithmetic.
+ * bf16 inputs whose rows lie on 16-byte boundaries (base and strides; outputs
+ * may lie anywhere) run on tensor cores, their outputs the sums of bf16
+ * products with the masked scores and the state rounded to bf16 once; a state
+ * that leaves takes the products of the rows as they are, its weights by three
+ * bf16 parts (two where outputs alone see it), in fp32.  So do bf16 inputs with
+ * D or M no multiple of 8 from N = 64 on, packed into the workspace first.
+ * fp32 data, and any other bf16, run fp32 arithmetic.
  */
 la_status la_decay_forward(la_view q, la_view k, la_view v, la_view out, const float *log_decay, const int *lens,
                            la_shape s, float scale, const float *S0, float *SN, void *workspace, size_t ws_bytes,
@@ -507,8 +510,9 @@ la_status la_decay_forward(la_view q, la_view k, la_view v, la_view out, const f
 /*
  * Bytes of device workspace la_decay_forward (backward = 0) or
  * la_decay_backward (1) needs: the states at the segments' starts where few
- * heads are cut into segments (0: none, NULL is accepted).  (size_t)-1 for an
- * invalid shape.
+ * heads are cut into segments, and the packed inputs where bf16 rows are not
+ * whole 16-byte pieces (0: none, NULL is accepted).  (size_t)-1 for an invalid
+ * shape.
  */
 size_t la_decay_workspace_bytes(la_shape s, int backward);
 

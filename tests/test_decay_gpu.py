@@ -322,6 +322,48 @@ def test_repeated_inputs(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dims", [(0,), (1,), (0, 1)])
+@pytest.mark.parametrize("N", [1, 200, 900])
+def test_shared_inputs_are_their_copies(N, dims, dtype):
+    """q, k, v and dout repeated by views over the sequences, the heads or both, each by itself and all together: what
+    copies of them give, bit for bit, gradients of every head's own."""
+    ts = inputs(3, 2, N, 64, 64, dtype, seed=N)
+    rows, (S0, dSN, g) = ts[:4], ts[4:]
+
+    def shared(t):
+        for d in dims:
+            t = t[:1] if d == 0 else t[:, :1]
+        return t.expand(3, 2, -1, -1)
+    for which in ((0,), (1,), (2,), (3,), (0, 1), (0, 1, 2, 3)):
+        views = [shared(t) if i in which else t for i, t in enumerate(rows)]
+        q, k, v, dout = views
+        a = [la.la_decay_forward(q, k, v, g, S0=S0), *la.la_decay_backward(q, k, v, dout, g, S0=S0, dSN=dSN)]
+        q, k, v, dout = (t.contiguous() for t in views)
+        b = [la.la_decay_forward(q, k, v, g, S0=S0), *la.la_decay_backward(q, k, v, dout, g, S0=S0, dSN=dSN)]
+        assert all(torch.equal(x, y) for x, y in zip(a, b)), which
+
+
+@pytest.mark.parametrize("D,M", [(33, 64), (64, 33), (99, 118), (1, 1), (127, 128)])
+@pytest.mark.parametrize("N,lens", [(64, [64, 0]), (130, [129, 1]), (1500, [1500, 700])])
+def test_packed_rows(N, lens, D, M):
+    """bf16 rows that are not whole 16-byte pieces, from long sequences on; rows past a length hold NaN and are not
+    read."""
+    check(2, 1, N, D, M, torch.bfloat16, seed=D, lens=lens)
+    q, k, v, dout, S0, dSN, g = inputs(2, 1, N, D, M, torch.bfloat16, D)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+
+    def run():
+        SN, dS0 = torch.empty_like(S0), torch.empty_like(S0)
+        out = la.la_decay_forward(q, k, v, g, S0=S0, SN=SN, lens=ln)
+        return [out, SN, *la.la_decay_backward(q, k, v, dout, g, S0=S0, dSN=dSN, dS0=dS0, lens=ln), dS0]
+    want = run()
+    for b, n in enumerate(lens):
+        for t in (q, k, v, dout):
+            t[b, :, n:] = float("nan")
+    assert all(torch.equal(x, y) for x, y in zip(run(), want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_offsets_past_32_bits(dtype):
     """Sequences more than 2^31 values apart."""
     q, k, v, _, S0, _, g = inputs(2, 1, 140, 64, 64, dtype, seed=8)

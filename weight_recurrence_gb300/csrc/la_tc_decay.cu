@@ -52,6 +52,7 @@ struct TcSweep {
     float *end;
     int D, M, blocks;                      // blocks of kMB columns
     int transposed, backwards, has_out;
+    int shared;                            // bits 2 i (heads) and 2 i + 1 (sequences): all of x, y, z's are one
     float c_intra, c_inter, c_state;
 };
 
@@ -111,10 +112,8 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                  : "memory");
 }
 
-// A wait that sleeps in the barrier's hardware for up to about 20 us at a time: polls
-// without the time hint came back at once, and those of a dozen waiting warps were
-// three of four instructions that an SM issued (5000 -> 3500 clocks a chunk without
-// them).  Out of line but for the first try: the roles share one instruction cache.
+// A wait that may sleep in the barrier's hardware for up to about 20 us at a time.
+// Out of line but for the first try: the roles share one instruction cache.
 __device__ __forceinline__ bool try_wait_long(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -323,25 +322,27 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
         // ------------------------------------------------------ loads
         if (lane == 0 && !*abort) {
             int ny = 0, nx = 0, nz = 0;
+            const int hx = sw.shared & 1 ? 0 : h, bx = sw.shared & 2 ? 0 : b, hy = sw.shared & 4 ? 0 : h;
+            const int by = sw.shared & 8 ? 0 : b, hz = sw.shared & 16 ? 0 : h, bz = sw.shared & 32 ? 0 : b;
             for (int it = 0; it < n; ++it) {
                 const int s = it % C::NS, t0 = first + chunk_of(it) * kC;
                 const uint32_t again = (it / C::NS - 1) & 1;
                 if (it >= C::NS && !wait_one(&y_empty[s], again, abort)) break;
                 mbar_arrive_expect_tx(&y_full[s], C::SUB * kTile);
 #pragma unroll
-                for (int j = 0; j < C::SUB; ++j) tma_load_4d(ytile(it) + j * kTile, &sw.y, &y_full[s], j * 64, t0, h, b);
+                for (int j = 0; j < C::SUB; ++j) tma_load_4d(ytile(it) + j * kTile, &sw.y, &y_full[s], j * 64, t0, hy, by);
                 ++ny;
                 if (out) {
                     if (it >= C::NS && !wait_one(&x_empty[s], again, abort)) break;
                     mbar_arrive_expect_tx(&x_full[s], C::SUB * kTile);
 #pragma unroll
                     for (int j = 0; j < C::SUB; ++j)
-                        tma_load_4d(xtile(it) + j * kTile, &sw.x, &x_full[s], j * 64, t0, h, b);
+                        tma_load_4d(xtile(it) + j * kTile, &sw.x, &x_full[s], j * 64, t0, hx, bx);
                     ++nx;
                 }
                 if (it >= C::NS && !wait_one(&z_empty[s], again, abort)) break;
                 mbar_arrive_expect_tx(&z_full[s], kTile);
-                tma_load_4d(ztile(it), &sw.z, &z_full[s], m0, t0, h, b);
+                tma_load_4d(ztile(it), &sw.z, &z_full[s], m0, t0, hz, bz);
                 ++nz;
             }
             if (*abort) {   // let the copies in flight land before the CTA exits
@@ -737,21 +738,24 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
     if (tid == 0 && *abort) record_error(args.err, kErrTimeout);
 }
 
-// 16-byte rows: base and strides; dimensions of one do not move.
+// 16-byte rows: base and strides; dimensions of one do not move, and heads and
+// sequences may be one and the same (stride 0).
 bool mappable(const la_view &v, int B, int H, int N) {
     auto ok = [](long long stride, int n) { return n <= 1 || (stride % 8 == 0 && stride > 0 && stride < (1LL << 38)); };
-    return v.data == nullptr ||
-           ((reinterpret_cast<uintptr_t>(v.data) & 15) == 0 && ok(v.sb, B) && ok(v.sh, H) && ok(v.sn, N));
+    return v.data == nullptr || ((reinterpret_cast<uintptr_t>(v.data) & 15) == 0 && (v.sb == 0 || ok(v.sb, B)) &&
+                                 (v.sh == 0 || ok(v.sh, H)) && ok(v.sn, N));
 }
+int shared_by(const la_view &v) { return (v.sh == 0 ? 1 : 0) | (v.sb == 0 ? 2 : 0); }
 
 // Tensor map of [B][H][N][cols] with the view's strides, boxes of 64 columns x
 // 128 rows.  Columns and rows past the tensor read as zeros and are not written.
 bool map_of(CUtensorMap *m, const la_view &v, int cols, const DecayLaunch &l) {
     auto fn = encode_fn();
     if (!fn) return false;
+    const int H = v.sh == 0 ? 1 : l.H, B = v.sb == 0 ? 1 : l.B;
     auto bytes = [](long long stride, int n) { return (cuuint64_t)(n > 1 ? stride * 2 : 16); };
-    cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)l.N, (cuuint64_t)l.H, (cuuint64_t)l.B};
-    cuuint64_t strides[3] = {bytes(v.sn, l.N), bytes(v.sh, l.H), bytes(v.sb, l.B)};
+    cuuint64_t dims[4] = {(cuuint64_t)cols, (cuuint64_t)l.N, (cuuint64_t)H, (cuuint64_t)B};
+    cuuint64_t strides[3] = {bytes(v.sn, l.N), bytes(v.sh, H), bytes(v.sb, B)};
     cuuint32_t box[4] = {64, (cuuint32_t)kC, 1, 1}, step[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
@@ -791,6 +795,7 @@ cudaError_t tc_decay(const DecayLaunch &l) {
         if (s.out.data && !map_of(&t.x, s.x, s.D, l)) return cudaErrorInvalidValue;
         t.rows = s.out, t.start = s.start, t.end = s.end, t.D = s.D, t.M = s.M, t.blocks = (s.M + kMB - 1) / kMB;
         t.transposed = s.transposed, t.backwards = s.backwards, t.has_out = s.out.data != nullptr;
+        t.shared = shared_by(s.x) | shared_by(s.y) << 2 | shared_by(s.z) << 4;
         t.c_intra = s.c_intra, t.c_inter = s.c_inter, t.c_state = s.c_state;
         a.blocks += t.blocks;
         D = std::max(D, s.D);
