@@ -9,7 +9,15 @@
 // keeps one token: it works out the token's angles once, in registers, and then
 // walks over the heads, a head's pairs spread over the group, so that the sines
 // cost a token's share of the heads and no table is read.  Neighbouring groups
-// of a warp take neighbouring tokens, whose rows lie side by side.
+// of a warp take neighbouring tokens, whose rows lie side by side.  The next
+// heads' rows are on their way while some are worked on, the first ones while
+// the angles are, and the weights lie in shared memory, which leaves the
+// registers for it.  Measured (40 heads of 64 channels, 8 x 4096 tokens, bf16):
+// forward 57 us, 5.9 of the copy's 6.8 TB/s, backward 107 us, 4.7 (without the
+// rows ahead 71 and 122).  The bf16 backward is held back by its registers, one
+// head ahead: with two it spilled (154 us).  fp32 rows by pieces reach 6.4 TB/s
+// both ways; rows by single values are bound by their instructions (16384 tokens
+// of 32 heads of 66 channels, bf16: 87 and 166 us, 1.6 and 1.25 TB/s).
 #include <algorithm>
 #include <cstring>
 
@@ -21,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = kRotateMaxD / 2;
-constexpr int kMaxAxes = 8;
 
 struct RotArgs {
     const void *x[2], *dy[2];   // queries, keys
@@ -61,6 +68,10 @@ __device__ __forceinline__ unsigned long long turns(float f) {
 // How a lane's V pairs lie in a head's row: kHalf, kAdjacent: V neighbouring pairs
 // by 16 byte pieces; kAny: pairs a warp apart by single values.
 enum Layout { kHalf, kAdjacent, kAny };
+// CTAs that an SM holds: rows by pieces take the registers for their loads (three of
+// them an SM: 8 x 4096 tokens backward 107 -> 214 us, spilled), single values the
+// warps (3 x 1234 tokens of 12 heads of 90 channels, two: 15 and 27 us, so 11 and 23).
+constexpr int slots_of(Layout l, bool bwd) { return l != kAny ? 2 : bwd ? 3 : 4; }
 
 // Channels of pair p: rotated pairs first, the channels behind them as pairs
 // that do not turn.
@@ -218,16 +229,29 @@ __device__ __forceinline__ void angles(const RotArgs &a, int lane, long long at,
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
 
-// G lanes to a token; BWD: the gradients; NORM: with the norm.  U heads are on
-// their way at a time.
+// G lanes to a token; BWD: the gradients; NORM: with the norm.  U heads are worked on
+// while the next U are on their way.
 template <typename T, int V, int G, Layout L, bool BWD, bool NORM>
-__global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_constant__ RotArgs a) {
-    constexpr int U = BWD ? 2 : 4, E = V / 2;
+__global__ void __launch_bounds__(kThreads, slots_of(L, BWD)) rotate_kernel(const __grid_constant__ RotArgs a) {
+    constexpr int U = L == kAny ? (BWD ? 1 : 2) : BWD ? 8 / V : 4, E = V / 2;
     const int lane = threadIdx.x % G, D = a.D, P = a.P;
     const bool half = L == kHalf || (L == kAny && a.half);
     const unsigned groups = gridDim.x * (kThreads / G), tokens = (unsigned)a.B * a.N, items = tokens * a.splits;
     const float mean = 1.f / (float)D;
     __shared__ unsigned long long turn[kMaxPairs];   // of every pair, a position
+    // the weights, by lanes: first and second values of a lane's pairs, two pairs to a piece
+    __shared__ float4 weights[NORM ? 2 : 1][NORM ? E : 1][NORM ? G : 1];
+    if constexpr (NORM) {
+        for (int i = threadIdx.x; i < 2 * E * G; i += kThreads) {
+            const int s = i / (E * G), e = i / G % E, ln = i % G;
+            const int p = pair_of_lane<V, L>(ln, 2 * e), q = pair_of_lane<V, L>(ln, 2 * e + 1);
+            auto at = [&](int c) { return a.w[s] ? a.w[s][c] : 1.f; };
+            float4 v = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (p < D / 2) v.x = at(first_of(p, P, half)), v.z = at(second_of(p, P, D, half));
+            if (q < D / 2) v.y = at(first_of(q, P, half)), v.w = at(second_of(q, P, D, half));
+            weights[s][e][ln] = v;
+        }
+    }
     unsigned bad = 0;
     float2 dwa[BWD && NORM ? E : 1], dwb[BWD && NORM ? E : 1];
 #pragma unroll
@@ -249,98 +273,96 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
         const unsigned split = live ? it / tokens : 0u, token = live ? it - split * tokens : 0u;
         const unsigned bu = token / a.N;
         const long long b = bu, n = token - bu * a.N;
-        float2 cs[E], sn[E];
-        angles<T, V, L>(a, lane, b * a.sb + n * a.sn, turn, bad, cs, sn);
-        // queries and keys; backward each by CTAs of its own, whose threads have room for one
-        // side's sums
+        // forward a token's queries and then its keys; backward each by CTAs of its own, whose
+        // threads have room for one side's sums
+        const int s0 = BWD ? blockIdx.y : 0, H0 = a.H[s0], H = BWD ? H0 : H0 + a.H[1], step = U * a.splits;
+        const T *x0 = static_cast<const T *>(a.x[s0]) + b * a.xb[s0] + n * a.xn[s0];
+        const T *x1 = BWD ? static_cast<const T *>(a.dy[s0]) + b * a.db[s0] + n * a.dn[s0]
+                          : static_cast<const T *>(a.x[1]) + b * a.xb[1] + n * a.xn[1];
+        T *y0 = static_cast<T *>(a.y[s0]) + b * a.yb[s0] + n * a.yn[s0];
+        T *y1 = BWD ? nullptr : static_cast<T *>(a.y[1]) + b * a.yb[1] + n * a.yn[1];
+        Raw<T, L, V> nx[U], nd[U];
+        auto fetch = [&](int h0) {
 #pragma unroll
-        for (int side = 0; side < (BWD ? 1 : 2); side++) {
-            const int s = BWD ? blockIdx.y : side;
-            const T *x = static_cast<const T *>(a.x[s]) + b * a.xb[s] + n * a.xn[s];
-            const T *dy = BWD ? static_cast<const T *>(a.dy[s]) + b * a.db[s] + n * a.dn[s] : nullptr;
-            T *y = static_cast<T *>(a.y[s]) + b * a.yb[s] + n * a.yn[s];
-            const int H = a.H[s];
-            // the weights of the lane's channels
-            float2 wa[NORM ? E : 1], wb[NORM ? E : 1];
-            if constexpr (NORM) {
-#pragma unroll
-                for (int i = 0; i < E; i++) {
-                    wa[i] = wb[i] = both(1.f);
-                    if (a.w[s]) {
-                        const int p = pair_of_lane<V, L>(lane, 2 * i), q = pair_of_lane<V, L>(lane, 2 * i + 1);
-                        if (p < D / 2) wa[i].x = a.w[s][first_of(p, P, half)], wb[i].x = a.w[s][second_of(p, P, D, half)];
-                        if (q < D / 2) wa[i].y = a.w[s][first_of(q, P, half)], wb[i].y = a.w[s][second_of(q, P, D, half)];
-                    }
+            for (int j = 0; j < U; j++) {
+                const int h = h0 + j * a.splits + (int)split, hh = live && h < H ? h : 0;   // one that is not there: read, not used
+                if constexpr (BWD) {
+                    if (NORM) nx[j] = load_raw<T, L, V>(x0 + hh * a.xh[s0], lane, P, D, half);
+                    nd[j] = load_raw<T, L, V>(x1 + hh * a.dh[s0], lane, P, D, half);
+                } else {
+                    nx[j] = load_raw<T, L, V>(hh < H0 ? x0 + hh * a.xh[0] : x1 + (hh - H0) * a.xh[1], lane, P, D, half);
                 }
             }
+        };
+        if (H > 0) fetch(0);
+        float2 cs[E], sn[E];
+        angles<T, V, L>(a, lane, b * a.sb + n * a.sn, turn, bad, cs, sn);
 #pragma unroll 1
-            for (int h0 = 0; h0 < H; h0 += U * a.splits) {
-                Raw<T, L, V> rx[U], rd[U];
+        for (int h0 = 0; h0 < H; h0 += step) {
+            Raw<T, L, V> rx[U], rd[U];
 #pragma unroll
-                for (int j = 0; j < U; j++) {
-                    const int h = h0 + j * a.splits + (int)split;
-                    // a head that is not there: the row's own start, read and not used
-                    const int hh = live && h < H ? h : 0;
-                    if (NORM || !BWD) rx[j] = load_raw<T, L, V>(x + hh * a.xh[s], lane, P, D, half);
-                    if (BWD) rd[j] = load_raw<T, L, V>(dy + hh * a.dh[s], lane, P, D, half);
+            for (int j = 0; j < U; j++) rx[j] = nx[j], rd[j] = nd[j];
+            if (h0 + step < H) fetch(h0 + step);   // the next heads on their way
+#pragma unroll
+            for (int j = 0; j < U; j++) {
+                const int h = h0 + j * a.splits + (int)split;
+                const bool on = live && h < H;
+                const int s = BWD ? s0 : h >= H0;
+                Pairs<V> v, o;
+                float rstd = 1.f;
+                if (NORM || !BWD) v = pairs_of<T, L, V>(rx[j]);
+                if constexpr (NORM) {
+                    float2 sum = both(0.f);
+#pragma unroll
+                    for (int i = 0; i < E; i++)
+                        sum = fma_pair(v.a[i], v.a[i], fma_pair(v.b[i], v.b[i], sum));
+                    rstd = rsqrtf(fmaf(group_sum<G>(sum.x + sum.y), mean, a.eps));
                 }
+                if constexpr (!BWD) {
 #pragma unroll
-                for (int j = 0; j < U; j++) {
-                    const int h = h0 + j * a.splits + (int)split;
-                    const bool on = live && h < H;
-                    Pairs<V> v, o;
-                    float rstd = 1.f;
-                    if (NORM || !BWD) v = pairs_of<T, L, V>(rx[j]);
-                    if constexpr (NORM) {
-                        float2 sum = both(0.f);
-#pragma unroll
-                        for (int i = 0; i < E; i++)
-                            sum = fma_pair(v.a[i], v.a[i], fma_pair(v.b[i], v.b[i], sum));
-                        rstd = rsqrtf(fmaf(group_sum<G>(sum.x + sum.y), mean, a.eps));
+                    for (int i = 0; i < E; i++) {
+                        if constexpr (NORM) {
+                            const float4 w = weights[s][i][lane];
+                            v.a[i] = mul_pair(mul_pair(v.a[i], both(rstd)), make_float2(w.x, w.y));
+                            v.b[i] = mul_pair(mul_pair(v.b[i], both(rstd)), make_float2(w.z, w.w));
+                        }
+                        o.a[i] = fma_pair(v.a[i], cs[i], neg(mul_pair(v.b[i], sn[i])));
+                        o.b[i] = fma_pair(v.b[i], cs[i], mul_pair(v.a[i], sn[i]));
                     }
-                    if constexpr (!BWD) {
+                } else {
+                    const Pairs<V> d = pairs_of<T, L, V>(rd[j]);
+                    Pairs<V> u;
+#pragma unroll
+                    for (int i = 0; i < E; i++) {   // turned back
+                        u.a[i] = fma_pair(d.a[i], cs[i], mul_pair(d.b[i], sn[i]));
+                        u.b[i] = fma_pair(d.b[i], cs[i], neg(mul_pair(d.a[i], sn[i])));
+                    }
+                    if constexpr (!NORM) {
+                        o = u;
+                    } else {
+                        const float2 r = both(rstd);
+                        float2 dot2 = both(0.f);
 #pragma unroll
                         for (int i = 0; i < E; i++) {
-                            if (NORM) {
-                                v.a[i] = mul_pair(mul_pair(v.a[i], both(rstd)), wa[i]);
-                                v.b[i] = mul_pair(mul_pair(v.b[i], both(rstd)), wb[i]);
+                            v.a[i] = mul_pair(v.a[i], r), v.b[i] = mul_pair(v.b[i], r);
+                            if (on) {   // a head that is not there adds nothing
+                                dwa[i] = fma_pair(u.a[i], v.a[i], dwa[i]);
+                                dwb[i] = fma_pair(u.b[i], v.b[i], dwb[i]);
                             }
-                            o.a[i] = fma_pair(v.a[i], cs[i], neg(mul_pair(v.b[i], sn[i])));
-                            o.b[i] = fma_pair(v.b[i], cs[i], mul_pair(v.a[i], sn[i]));
+                            const float4 w = weights[s][i][lane];
+                            u.a[i] = mul_pair(u.a[i], make_float2(w.x, w.y));
+                            u.b[i] = mul_pair(u.b[i], make_float2(w.z, w.w));
+                            dot2 = fma_pair(u.a[i], v.a[i], fma_pair(u.b[i], v.b[i], dot2));
                         }
-                    } else {
-                        const Pairs<V> d = pairs_of<T, L, V>(rd[j]);
-                        Pairs<V> u;
+                        const float2 dot = both(-group_sum<G>(dot2.x + dot2.y) * mean);
 #pragma unroll
-                        for (int i = 0; i < E; i++) {   // turned back
-                            u.a[i] = fma_pair(d.a[i], cs[i], mul_pair(d.b[i], sn[i]));
-                            u.b[i] = fma_pair(d.b[i], cs[i], neg(mul_pair(d.a[i], sn[i])));
-                        }
-                        if constexpr (!NORM) {
-                            o = u;
-                        } else {
-                            const float2 r = both(rstd);
-                            float2 dot2 = both(0.f);
-#pragma unroll
-                            for (int i = 0; i < E; i++) {
-                                v.a[i] = mul_pair(v.a[i], r), v.b[i] = mul_pair(v.b[i], r);
-                                if (on) {   // a head that is not there adds nothing
-                                    dwa[i] = fma_pair(u.a[i], v.a[i], dwa[i]);
-                                    dwb[i] = fma_pair(u.b[i], v.b[i], dwb[i]);
-                                }
-                                u.a[i] = mul_pair(u.a[i], wa[i]), u.b[i] = mul_pair(u.b[i], wb[i]);
-                                dot2 = fma_pair(u.a[i], v.a[i], fma_pair(u.b[i], v.b[i], dot2));
-                            }
-                            const float2 dot = both(-group_sum<G>(dot2.x + dot2.y) * mean);
-#pragma unroll
-                            for (int i = 0; i < E; i++) {
-                                o.a[i] = mul_pair(r, fma_pair(v.a[i], dot, u.a[i]));
-                                o.b[i] = mul_pair(r, fma_pair(v.b[i], dot, u.b[i]));
-                            }
+                        for (int i = 0; i < E; i++) {
+                            o.a[i] = mul_pair(r, fma_pair(v.a[i], dot, u.a[i]));
+                            o.b[i] = mul_pair(r, fma_pair(v.b[i], dot, u.b[i]));
                         }
                     }
-                    if (on) store_pairs<T, L, V>(y + h * a.yh[s], o, lane, P, D, half);
                 }
+                if (on) store_pairs<T, L, V>(BWD || s == 0 ? y0 + h * a.yh[s0] : y1 + (h - H0) * a.yh[1], o, lane, P, D, half);
             }
         }
     }
@@ -366,18 +388,21 @@ __global__ void __launch_bounds__(kThreads, 2) rotate_kernel(const __grid_consta
     }
 }
 
-// Columns of the CTAs' sums [n][2D]: 32 columns to a CTA, rows over its 8 warps.
-__global__ void __launch_bounds__(256) weight_sums_kernel(const float *ws, int n, int D, float *dwq, float *dwk) {
-    __shared__ float part[8][33];
+// Columns of the CTAs' sums [n][2D]: 32 columns to a CTA, rows over its 32 warps, whose
+// loads are all on their way at once.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) weight_sums_kernel(const float *ws, int n, int D, float *dwq, float *dwk) {
+    __shared__ float part[kSumWarps][33];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     float t = 0.f;
     if (c < 2 * D)
-#pragma unroll 4
-        for (int r = warp; r < n; r += 8) t += ws[(size_t)r * 2 * D + c];
+#pragma unroll 10
+        for (int r = warp; r < n; r += kSumWarps) t += ws[(size_t)r * 2 * D + c];
     part[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && c < 2 * D) {
-        for (int i = 1; i < 8; i++) t += part[i][lane];
+#pragma unroll
+        for (int i = 1; i < kSumWarps; i++) t += part[i][lane];
         float *dst = c < D ? dwq : dwk;
         if (dst) dst[c < D ? c : c - D] = t;
     }
@@ -450,10 +475,11 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
     a.half = half;
     const int G = l == kAny ? 32 : size == 4 ? lanes_of<float>(p.s.D) : lanes_of<__nv_bfloat16>(p.s.D);
     const long long tokens = (long long)p.s.B * p.s.N, per = kThreads / G;
-    // a token's heads are shared by as many groups as it takes to fill the SMs
-    const int heads = std::max(p.s.Hq, p.s.Hk);
+    // a token's heads are shared by as many groups as fill the SMs at once, and no more
+    // (4096 tokens of 32 heads of 64: 9.4 and 16.7 us, with twice as many 11.8 and 21.3)
+    const int heads = bwd ? std::max(p.s.Hq, p.s.Hk) : p.s.Hq + p.s.Hk;
     long long splits = 1;
-    while (splits < heads && tokens * splits * 2 <= (long long)kSms * 4 * per) splits *= 2;
+    while (splits < heads && tokens * splits * 2 <= (long long)kSms * slots_of(l, bwd) / (bwd ? 2 : 1) * per) splits *= 2;
     a.splits = (int)splits;
     const bool sums = bwd && p.norm && (p.dwq || p.dwk);
     a.ws = sums ? static_cast<float *>(p.ws) : nullptr;
@@ -464,7 +490,7 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
                         : (f32 ? pick<float, false>(a, l, (int)ctas, p.norm, p.stream)
                                : pick<__nv_bfloat16, false>(a, l, (int)ctas, p.norm, p.stream));
     if (e != cudaSuccess || !sums) return e;
-    weight_sums_kernel<<<(2 * p.s.D + 31) / 32, 256, 0, p.stream>>>(a.ws, (int)ctas, p.s.D, p.dwq, p.dwk);
+    weight_sums_kernel<<<(2 * p.s.D + 31) / 32, 32 * kSumWarps, 0, p.stream>>>(a.ws, (int)ctas, p.s.D, p.dwq, p.dwk);
     count_launches(1);
     return cudaGetLastError();
 }
