@@ -501,7 +501,8 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
  * that leaves takes the products of the rows as they are, its weights by three
  * bf16 parts (two where outputs alone see it), in fp32.  So do bf16 inputs with
  * D or M no multiple of 8 from N = 64 on, packed into the workspace first.
- * fp32 data, and any other bf16, run fp32 arithmetic.
+ * fp32 data, any other bf16, and up to 16 tokens (8 of few heads) run fp32
+ * arithmetic.
  */
 la_status la_decay_forward(la_view q, la_view k, la_view v, la_view out, const float *log_decay, const int *lens,
                            la_shape s, float scale, const float *S0, float *SN, void *workspace, size_t ws_bytes,

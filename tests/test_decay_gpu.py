@@ -322,6 +322,26 @@ def test_repeated_inputs(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [1, 3, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("B,H,D,M", [(2, 2, 64, 64), (3, 60, 64, 64), (160, 4, 128, 128), (2, 160, 40, 72), (90, 2, 33, 7), (2, 3, 128, 66)])
+def test_a_few_tokens(B, H, D, M, N, dtype):
+    """Few tokens of few and of many heads, lengths from none to all of them, with the state in place, and the state
+    alone."""
+    lens = [(0, N, N // 2, 1)[b % 4] for b in range(B)]
+    q, k, v, _, S0, _, g = inputs(B, H, N, D, M, dtype, seed=N, layout="tokens")
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    S, alone = S0.clone(), torch.empty_like(S0)
+    out = la.la_decay_forward(q, k, v, g, 0.3, S0=S, SN=S, lens=ln)
+    assert la.la_decay_forward(None, k, v, g, 0.3, S0=S0, SN=alone, lens=ln, want_out=False) is None
+    qn, kn, vn, Sn, gn = (_np(t) for t in (q, k, v, S0, g))
+    ref, refS = decay.forward(qn, kn, vn, gn, 0.3, Sn, lens)
+    H_, HS = decay.forward(np.abs(qn), np.abs(kn), np.abs(vn), gn, 0.3, np.abs(Sn), lens)
+    _rows("out", out, ref, H_, _k(N, max(D, M)), dtype)
+    _close("SN", S, refS, _k(N, max(D, M)) * U * HS)
+    assert torch.equal(S, alone)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("dims", [(0,), (1,), (0, 1)])
 @pytest.mark.parametrize("N", [1, 200, 900])
 def test_shared_inputs_are_their_copies(N, dims, dtype):

@@ -1,10 +1,11 @@
 // la_decay.cu - linear attention with a decay for each head: sweeps in fp32
 // arithmetic on CUDA cores (fp32 data, short bf16 rows off 16 bytes), the scan of
-// the segments' states, the packing of long bf16 rows, and the step of one token.
+// the segments' states, the packing of long bf16 rows, and steps of one or a few tokens.
 #include <algorithm>
 
 #include "la_common.cuh"
 #include "la_decay.h"
+#include "la_pair.cuh"
 
 namespace la {
 namespace {
@@ -407,9 +408,10 @@ __global__ void __launch_bounds__(128) step_kernel(const StepArgs a) {
 template <typename T, int L, int VEC> cudaError_t step_of(const StepArgs &a, long long heads, cudaStream_t st) {
     constexpr int R = 128 / L;
     const int ctas = (int)(heads * a.blocks);
+    constexpr int most = kDecayMaxD / R;   // rows of a thread: 16, or 8 where there are 16 a pass
     if (a.D <= R * 4) step_kernel<T, L, 4, VEC><<<ctas, 128, 0, st>>>(a);
-    else if (a.D <= R * 8) step_kernel<T, L, 8, VEC><<<ctas, 128, 0, st>>>(a);
-    else step_kernel<T, L, 16, VEC><<<ctas, 128, 0, st>>>(a);
+    else if (most == 8 || a.D <= R * 8) step_kernel<T, L, 8, VEC><<<ctas, 128, 0, st>>>(a);
+    else step_kernel<T, L, most, VEC><<<ctas, 128, 0, st>>>(a);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -428,6 +430,153 @@ template <typename T> cudaError_t step(const DecayProblem &p) {
     }
     a.blocks = (p.M + 15) / 16;
     return step_of<T, 16, 1>(a, heads, p.stream);
+}
+
+// ------------------------------------------------------------- a few tokens
+
+constexpr int kShort = 16;     // tokens of a sequence up to which the walk goes token by token
+constexpr int kGroup = 4;      // tokens whose outputs are joined together
+
+struct ShortArgs {
+    la_view q, k, v, out;
+    const float *log_decay, *S0;
+    const int *lens;
+    float *SN;
+    int H, N, D, M, blocks;
+    float scale;
+};
+
+// The same as the step over up to kShort tokens, the state in registers from the first
+// to the last: it is read and written once, where chunks of 128 tokens would mostly
+// multiply zeros.  4096 heads of 64 x 64, 134 MB of states: one token 28 us, then 3 to 4 us
+// a token, four instructions for each two values of the state.
+template <typename T, int L, int K, int VEC>
+__global__ void __launch_bounds__(128) short_kernel(const ShortArgs a) {
+    constexpr int R = 128 / L, W = L * VEC;   // rows a pass, columns a CTA
+    __shared__ float2 kq[kShort][R * K];
+    __shared__ __align__(16) float vs[kShort][W], part[2][4][kGroup][W];
+    const int bh = blockIdx.x / a.blocks, blk = blockIdx.x % a.blocks, b = bh / a.H, h = bh % a.H, tid = threadIdx.x;
+    const int m0 = blk * W, col = tid % L * VEC, m = m0 + col, r = tid / L, cols = min(W, a.M - m0);
+    const int n = a.lens ? max(0, min(a.N, a.lens[b])) : a.N;
+    const size_t at = (size_t)bh * a.D * a.M + m;
+    const bool in = m < a.M, out = a.out.data != nullptr;
+    float s[K][VEC];
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+        const int d = r + k * R;
+#pragma unroll
+        for (int i = 0; i < VEC; i++) s[k][i] = 0.f;
+        if (a.S0 && in && d < a.D) {
+            const float *p = a.S0 + at + (size_t)d * a.M;
+            if constexpr (VEC == 4) {
+                const float4 t = *reinterpret_cast<const float4 *>(p);
+                s[k][0] = t.x, s[k][1] = t.y, s[k][2] = t.z, s[k][3] = t.w;
+            } else {
+                s[k][0] = *p;
+            }
+        }
+    }
+    const T *q = out ? row_of<T>(a.q, b, h, 0) : nullptr, *kk = row_of<T>(a.k, b, h, 0), *vv = row_of<T>(a.v, b, h, 0) + m0;
+    // rows behind the last token of a group add nothing (a row that is not there is 0)
+    const int groups = (n + kGroup - 1) / kGroup;
+    for (int i = tid; i < groups * kGroup * R * K; i += 128) {
+        const int t = i / (R * K), d = i % (R * K);
+        const bool is = t < n && d < a.D;
+        kq[t][d] = make_float2(is ? to_f32(kk[t * a.k.sn + d]) : 0.f, is && out ? to_f32(q[t * a.q.sn + d]) : 0.f);
+    }
+    for (int i = tid; i < groups * kGroup * W; i += 128) {
+        const int t = i / W, c = i % W;
+        vs[t][c] = t < n && c < cols ? to_f32(vv[t * a.v.sn + c]) : 0.f;
+    }
+    const float2 decay = kept(a.log_decay[h], 1);
+    T *y = out ? static_cast<T *>(a.out.data) + b * a.out.sb + h * a.out.sh + m0 : nullptr;
+    __syncthreads();
+    for (int g = 0; g < groups; g++) {
+        float acc[kGroup][VEC];
+#pragma unroll
+        for (int j = 0; j < kGroup; j++) {
+            const int t = g * kGroup + j;
+            float v[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; i++) v[i] = vs[t][col + i], acc[j][i] = 0.f;
+            if (t >= n) continue;
+#pragma unroll
+            for (int k = 0; k < K; k++) {
+                if (r + k * R >= a.D) continue;
+                const float2 x = kq[t][r + k * R];
+                if constexpr (VEC == 4) {
+                    const float2 kd = make_float2(x.x, x.x), qd = make_float2(x.y, x.y);
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        float2 t2 = make_float2(s[k][i], s[k][i + 1]);
+                        t2 = fma_pair(make_float2(decay.y, decay.y), t2, mul_pair(make_float2(decay.x, decay.x), t2));
+                        t2 = fma_pair(kd, make_float2(v[i], v[i + 1]), t2);
+                        const float2 o = fma_pair(qd, t2, make_float2(acc[j][i], acc[j][i + 1]));
+                        s[k][i] = t2.x, s[k][i + 1] = t2.y, acc[j][i] = o.x, acc[j][i + 1] = o.y;
+                    }
+                } else {
+                    s[k][0] = fmaf(x.x, v[0], keep(decay, s[k][0]));
+                    acc[j][0] = fmaf(x.y, s[k][0], acc[j][0]);
+                }
+            }
+        }
+        if (!out) continue;
+        // rows of the warp, then of the warps
+#pragma unroll
+        for (int j = 0; j < kGroup; j++)
+#pragma unroll
+            for (int i = 0; i < VEC; i++) {
+#pragma unroll
+                for (int o = L; o < 32; o *= 2) acc[j][i] += __shfl_xor_sync(0xffffffffu, acc[j][i], o);
+                if (tid % 32 < L) part[g & 1][tid / 32][j][col + i] = acc[j][i];
+            }
+        __syncthreads();
+        for (int i = tid; i < kGroup * W; i += 128) {
+            const int j = i / W, c = i % W, t = g * kGroup + j;
+            const float(&p)[4][kGroup][W] = part[g & 1];
+            if (t < n && c < cols)
+                y[t * a.out.sn + c] = from_f32<T>(a.scale * ((p[0][j][c] + p[1][j][c]) + (p[2][j][c] + p[3][j][c])));
+        }
+    }
+    if (a.SN && in)
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int d = r + k * R;
+            if (d >= a.D) continue;
+            float *p = a.SN + at + (size_t)d * a.M;
+            if constexpr (VEC == 4) *reinterpret_cast<float4 *>(p) = make_float4(s[k][0], s[k][1], s[k][2], s[k][3]);
+            else *p = s[k][0];
+        }
+    if (out)   // rows past the length
+        for (int i = tid; i < (a.N - n) * W; i += 128) {
+            const int t = n + i / W, c = i % W;
+            if (c < cols) y[t * a.out.sn + c] = from_f32<T>(0.f);
+        }
+}
+
+template <typename T, int L, int VEC> cudaError_t short_of(const ShortArgs &a, long long heads, cudaStream_t st) {
+    constexpr int R = 128 / L;
+    const int ctas = (int)(heads * a.blocks);
+    constexpr int most = kDecayMaxD / R;   // rows of a thread: 16, or 8 where there are 16 a pass
+    if (a.D <= R * 4) short_kernel<T, L, 4, VEC><<<ctas, 128, 0, st>>>(a);
+    else if (most == 8 || a.D <= R * 8) short_kernel<T, L, 8, VEC><<<ctas, 128, 0, st>>>(a);
+    else short_kernel<T, L, most, VEC><<<ctas, 128, 0, st>>>(a);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t short_forward(const DecayProblem &p) {
+    ShortArgs a{p.q, p.k, p.v, p.out, p.log_decay, p.S0, p.lens, p.SN, p.H, p.N, p.D, p.M, 1, p.scale};
+    const long long heads = (long long)p.B * p.H;
+    const bool wide = p.M % 4 == 0 && ((reinterpret_cast<uintptr_t>(p.SN) | reinterpret_cast<uintptr_t>(p.S0)) & 15) == 0;
+    a.blocks = (p.M + 63) / 64;
+    if (wide && heads * a.blocks >= kSms * 4) return short_of<T, 16, 4>(a, heads, p.stream);
+    if (wide) {   // few heads: columns over more CTAs
+        a.blocks = (p.M + 31) / 32;
+        return short_of<T, 8, 4>(a, heads, p.stream);
+    }
+    a.blocks = (p.M + 15) / 16;
+    return short_of<T, 16, 1>(a, heads, p.stream);
 }
 
 // ------------------------------------------------------------- segments
@@ -541,8 +690,9 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
 
 // bf16 rows that are not a multiple of 16 bytes long (contiguous ones then lie off
 // those boundaries) are packed first where sequences are long: two passes of memory
-// more, and then the tensor cores (2 heads of 2379 tokens, D = 99, M = 118: 51 us with it,
-// 87 on FMA units; 18 heads of 2 tokens: 38 and 23).
+// more, and then the tensor cores (2 heads of 2379 tokens, D = 99, M = 118: 43 us with it,
+// 87 on FMA units; 8 heads of 32 and of 64 tokens take 10.5 and 14.8 us there, 5.9 on
+// tensor cores without the packing).
 bool packs(int N, int D, int M, la_dtype dtype) { return dtype == LA_DTYPE_BF16 && N >= 64 && (D % 8 || M % 8); }
 size_t packed_bytes(int B, int H, int N, int n) { return ((size_t)B * H * N * ((n + 7) / 8) * 16 + 255) / 256 * 256; }
 
@@ -580,6 +730,10 @@ size_t decay_ws_bytes(const la_shape &s, bool backward) {
 
 cudaError_t decay_forward(const DecayProblem &given) {
     DecayProblem p = given;
+    // 4096 heads of 64 x 64, 4 and 16 tokens: 41 and 76 us (bf16), in chunks 177 and 178; 8
+    // heads, 8 and 16 tokens: 4.6 and 6.7 us, in chunks 5.9 on tensor cores, 8.8 and 9.1 else
+    const bool few = (long long)p.B * p.H * blocks_of(p.M) <= kSms;
+    if (p.N <= (few && p.dtype == LA_DTYPE_BF16 ? kShort / 2 : kShort)) return p.dtype == LA_DTYPE_F32 ? short_forward<float>(p) : short_forward<__nv_bfloat16>(p);
     DecayLaunch l = launch_of(p, cut_of(p.B, p.H, p.N, p.D, p.M, p.dtype, false));
     const la_view none{nullptr, 0, 0, 0};
     float *ws = static_cast<float *>(p.ws);
