@@ -101,13 +101,12 @@ template <int DP> struct DecayCfg {
     static constexpr int OFF_FLAG = OFF_DIAG + 64 * 4;     // [NBAD][2 halves][8 warps]
     static constexpr int OFF_BAD = OFF_FLAG + NBAD * 64;   // [NBAD][2][8][16 columns]: first or last row, a byte
     static constexpr int OFF_BAR = OFF_BAD + NBAD * 256;
-    static constexpr int NBARS = 6 * NS + 5 * 2 + 4 + 1 + 4 + 2 + 1;
+    static constexpr int NBARS = 6 * NS + 5 * 2 + 4 + 1 + 6 + 2 + 1;
     static constexpr int OFF_TSLOT = OFF_BAR + 8 * NBARS;
     static constexpr int SMEM = OFF_TSLOT + 16;
     static_assert(NBAD > NS && OFF_BAR % 8 == 0 && SMEM <= (int)kSmemMax, "shared memory budget");
     // TMEM: two buffers of P (128 columns; the scores as bf16 take the first half of
-    // each 64), x S and A z (64 each), and the increment of the state by the first part
-    // of z and by the others (64 each)
+    // each 64), x S and A z (64 each), and two of the state's increment (64 each)
     static __device__ __forceinline__ uint32_t col_p(int b) { return 128u * b; }
     static constexpr uint32_t COL_XS = 256, COL_AZ = 320, COL_DS = 384;
 };
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
              *z_full = y_empty + C::NS, *z_empty = z_full + C::NS;
     uint64_t *p_full = z_empty + C::NS, *a_ready = p_full + 2, *xs_full = a_ready + 2, *o_full = xs_full + 2,
              *o_free = o_full + 2, *zw_ready = o_free + 2, *tail_ready = zw_ready + 4, *half_ready = tail_ready + 1,
-             *half_free = half_ready + 1, *ds_full = half_free + 1, *ds_free = ds_full + 1, *snap_ready = ds_free + 1,
+             *half_free = half_ready + 1, *ds_full = half_free + 1, *ds_free = ds_full + 2, *snap_ready = ds_free + 2,
              *drain = snap_ready + 2;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(smem + C::OFF_TSLOT);
     float *w = reinterpret_cast<float *>(smem + C::OFF_TAB), *colf = reinterpret_cast<float *>(smem + C::OFF_COL);
@@ -290,12 +289,12 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
             mbar_init(&o_full[i], 1);
             mbar_init(&o_free[i], kPair);
             mbar_init(&snap_ready[i], kPair);
+            mbar_init(&ds_full[i], 1);
+            mbar_init(&ds_free[i], kPair);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&zw_ready[i], kPair);
         mbar_init(half_ready, kPair);
         mbar_init(half_free, 1);
-        mbar_init(ds_full, 1);
-        mbar_init(ds_free, kPair);
         mbar_init(tail_ready, kPair);
         mbar_init(drain, 3);
         fence_mbar_init();
@@ -396,19 +395,19 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
     } else if (warp == 3) {
         // ------------------------------------------------------ increments: y^T (weighted z)
         {
-            constexpr uint32_t ID_TWO = idesc_bf16(128, 2 * kMB, 1, 1), ID_ONE = idesc_bf16(128, kMB, 1, 1);
+            constexpr uint32_t ID = idesc_bf16(128, kMB, 1, 1);
             for (int it = 0; it < n; ++it) {
                 const int s = it % C::NS;
                 if (!wait_warp(&y_full[s], (it / C::NS) & 1, abort)) break;
-                if (it >= 1 && !wait_warp(ds_free, (it - 1) & 1, abort)) break;
+                // the increment of two chunks before has been added to the state
+                if (it >= 2 && !wait_warp(&ds_free[it & 1], (it / 2 - 1) & 1, abort)) break;
                 // y^T read MN-major; 64 columns wide it is repeated (M-atom stride 0), so
-                // that lanes 64-127 hold a second copy.  The first two parts of z side by
-                // side are one operand, so that y^T is read once for them; the third is
-                // added to the second's products.  By halves of the rows, so that the first
-                // half's parts can be written anew while the second's are multiplied
+                // that lanes 64-127 hold a second copy.  By halves of the rows, so that the
+                // first half's parts can be written anew while the second's are multiplied
                 const uint64_t dy = smem_desc(smem_u32(ytile(it)), DP == 64 ? 0 : kTile, 1024);
-                const uint64_t dz = smem_desc(smem_u32(zw), kTile, 1024);
-                const uint64_t dl = smem_desc(smem_u32(zw) + 2 * kTile, 0, 1024);
+                const uint64_t dz = smem_desc(smem_u32(zw), 0, 1024);
+                constexpr uint64_t part = kTile >> 4;
+                const uint32_t to = tmem + C::COL_DS + kMB * (it & 1);
                 bool ok = true;
 #pragma unroll 1
                 for (int k0 = 0; k0 < kC / 16 && ok; k0 += kC / 32) {
@@ -419,20 +418,21 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
 #pragma unroll
                         for (int i = 0; i < kC / 32; ++i) {
                             const uint64_t step = mnmajor_step(1) * (uint64_t)(k0 + i);
-                            mma_f16_ss(tmem + C::COL_DS, dy + step, dz + step, ID_TWO, k0 + i > 0);
+                            mma_f16_ss(to, dy + step, dz + step, ID, k0 + i > 0);
+                            mma_f16_ss(to, dy + step, dz + part + step, ID, 1);
                         }
                         if (parts == 3)
 #pragma unroll
                             for (int i = 0; i < kC / 32; ++i) {
                                 const uint64_t step = mnmajor_step(1) * (uint64_t)(k0 + i);
-                                mma_f16_ss(tmem + C::COL_DS + kMB, dy + step, dl + step, ID_ONE, 1);
+                                mma_f16_ss(to, dy + step, dz + 2 * part + step, ID, 1);
                             }
                         if (k0 == 0) mma_commit(half_free);
                     }
                 }
                 if (!ok) break;
                 if (elect_one()) {
-                    mma_commit(ds_full);
+                    mma_commit(&ds_full[it & 1]);
                     mma_commit(&y_empty[s]);
                     mma_commit(&z_empty[s]);
                 }
@@ -640,12 +640,13 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
                 const float wr = row < rows ? w[backwards ? row + 1 : rows - 1 - row] : 0.f;
                 const float2 wr2 = make_float2(wr, wr), minus = make_float2(-1.f, -1.f);
                 float2 check = make_float2(0.f, 0.f);   // NaN where a value is not finite
-#pragma unroll 1
+#pragma unroll
                 for (int c = zc; c < zc + 16; c += 8) {
                     const uint32_t off = sw128_offset(row, c);
                     const uint4 v = *reinterpret_cast<const uint4 *>(zt + off);
                     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t hi[4], mid[4], lo[4];
+                    uint32_t hi[4], mid[4];
+                    float2 rest[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         // the leading 8 bits of each value, cut off, three times: 24 bits, all there are
@@ -654,12 +655,16 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
                         f = fma_pair(get_pair(hi[j]), minus, f);
                         check = add_pair(check, f);
                         mid[j] = top_pair(f);
-                        lo[j] = top_pair(fma_pair(get_pair(mid[j]), minus, f));
+                        rest[j] = f;
                     }
                     *reinterpret_cast<uint4 *>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(zw + kTile + off) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                    if (parts == 3)
+                    if (parts == 3) {
+                        uint32_t lo[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) lo[j] = top_pair(fma_pair(get_pair(mid[j]), minus, rest[j]));
                         *reinterpret_cast<uint4 *>(zw + 2 * kTile + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
                 const int slot = it % C::NBAD * 16 + 8 * half + (warp - 12);
                 const float all = check.x + check.y;
@@ -697,20 +702,19 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
                 weigh(it, 0, ok);
             }
             if (it > 0) {   // the increment of the chunk before
-                ok = wait_warp(ds_full, (it - 1) & 1, abort) && ok;
+                ok = wait_warp(&ds_full[(it - 1) & 1], ((it - 1) >> 1) & 1, abort) && ok;
                 if (ok) {
                     tc_fence_after();
                     const float2 a = rows_of(it - 1) == kC ? kept_whole : kept_tail;
-                    const uint32_t tds = tmem + lane_off + C::COL_DS + cb;
+                    const uint32_t tds = tmem + lane_off + C::COL_DS + kMB * ((it - 1) & 1) + cb;
 #pragma unroll
                     for (int j = 0; j < NC; j += 16) {
-                        uint32_t v[16], u[16];
+                        uint32_t v[16];
                         tmem_ld16(tds + j, v);
-                        tmem_ld16(tds + kMB + j, u);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            const float2 e = add_pair(pair_at(v, i), pair_at(u, i));
+                            const float2 e = pair_at(v, i);
                             float2 s2 = make_float2(sv[j + i], sv[j + i + 1]);
                             s2 = fma_pair(make_float2(a.y, a.y), s2, mul_pair(make_float2(a.x, a.x), s2));
                             s2 = fma_pair(c2, e, s2);
@@ -719,7 +723,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
                     }
                 }
                 tc_fence_before();
-                arrive_warp(ds_free);
+                arrive_warp(&ds_free[(it - 1) & 1]);
             }
             if (it == n) break;
             // z before the snapshot: its increment is what the next round waits for
