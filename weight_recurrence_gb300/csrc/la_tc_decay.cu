@@ -33,14 +33,14 @@
 // columns would leave one chunk.  The CTAs of a head's column blocks and of the
 // backward's three sweeps are neighbours and share their rows through the L2.
 //
-// Measured: 128 heads of 4096 tokens, D = M = 64, forward 78 us (268 MB, 3.5 TB/s,
-// 110 TFLOP/s); 16 heads of 65536 tokens, D = M = 128, in 4 segments 502 us; the
-// backward's three sweeps of 128 heads of 2048 tokens 114 us.  A chunk takes about
-// 4400 clocks, of which HBM would need 2800 (all SMs at the copy's rate), the tensor
-// pipe 900, issue 2400: what bounds it is the chain from chunk to chunk (z weighed,
-// its increment multiplied, added to the state, the snapshot for the next x S), whose
-// links share the shared memory's bandwidth (about 300 KB a chunk), and a CTA's start
-// and end, which together take as long as six chunks.
+// Measured: 128 heads of 4096 tokens, D = M = 64, forward 76 us (272 MB, 3.6 TB/s,
+// 113 TFLOP/s); 16 heads of 65536 tokens, D = M = 128, in 4 segments 491 us; the
+// backward's three sweeps of 128 heads of 2048 tokens 105 us.  A chunk takes about
+// 3900 clocks, of which HBM would need 2800 (all SMs at the copy's rate), the tensor
+// pipe 850, issue 2100.  No unit is full: the weighing of z (14 us of 72 where it was
+// left out), the outputs (12), the scores (4) and the increments share the issue slots
+// and the shared memory's bandwidth (about 300 KB a chunk).  A CTA's start and end
+// take as long as six chunks.
 #include <algorithm>
 
 #include "la_common.cuh"
