@@ -597,8 +597,10 @@ constexpr Cost kTensor = {6.0, 0.9, 2.0, 2.1, 1}, kFma64 = {0.5, 0.4, 0.4, 13.0,
 // Segments of a sequence.  `ctas` walk over the whole sequences side by side; cut,
 // there are `segs` times as many, which have first to find the states at their
 // starts: `sums` CTAs a segment, then a scan that moves `states` bytes a segment.
-// Tensor cores, 16 heads of 65536 tokens, D = M = 128: 4 segments 519 us, 19 566; 16
-// heads of 16384, backward: 1 segment 278 us, 3 303.
+// Measured, us: tensor cores, 16 heads of 65536 tokens, D = M = 128: 9 segments (taken)
+// 490, 4 506, 8 540, 19 554, none 1087; backward of 16 heads of 16384: none (taken)
+// 264, 2 383, 3 290; 8 heads of 16384, D = M = 64: 19 (taken) 45, 4 126, none 262.
+// FMA units, 35 heads of 1537, D = M = 64: 8 (taken) 103, 4 118, none 248.
 Cut cut_of(long long ctas, long long sums, double states, int N, const Cost &cost) {
     const long long chunks = ((long long)N + 127) / 128, slots = (long long)kSms * cost.slots;
     long long best = 1;

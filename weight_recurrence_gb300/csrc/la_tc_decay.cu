@@ -34,7 +34,7 @@
 // backward's three sweeps are neighbours and share their rows through the L2.
 //
 // Measured: 128 heads of 4096 tokens, D = M = 64, forward 76 us (272 MB, 3.6 TB/s,
-// 113 TFLOP/s); 16 heads of 65536 tokens, D = M = 128, in 4 segments 491 us; the
+// 113 TFLOP/s); 16 heads of 65536 tokens, D = M = 128, in 9 segments 491 us; the
 // backward's three sweeps of 128 heads of 2048 tokens 105 us.  A chunk takes about
 // 3900 clocks, of which HBM would need 2800 (all SMs at the copy's rate), the tensor
 // pipe 850, issue 2100.  No unit is full: the weighing of z (14 us of 72 where it was
