@@ -342,6 +342,48 @@ def test_a_few_tokens(B, H, D, M, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [1, 5, 20, 200, 1100])
+def test_states_off_16_bytes(N, dtype):
+    """States that start on 4 bytes only, against states on 16: the same sums, at most in another order (fp32: below
+    1e-5 of the largest at these lengths)."""
+    q, k, v, dout, S0, dSN, g = inputs(1, 2, N, 64, 64, dtype, seed=N)
+
+    def off(t):
+        return torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)
+
+    def run(f):
+        a, b, SN, dS0 = f(S0), f(dSN), f(torch.zeros_like(S0)), f(torch.zeros_like(S0))
+        out = la.la_decay_forward(q, k, v, g, 0.2, S0=a, SN=SN)
+        grads = la.la_decay_backward(q, k, v, dout, g, 0.2, S0=a, dSN=b, dS0=dS0)
+        y = la.la_decay_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], a, g, 0.2)
+        return [out, SN, *grads, dS0, y, a]
+    assert off(S0).data_ptr() % 16 == 4
+    for x, y in zip(run(off), run(torch.clone)):
+        assert (x - y).abs().max() <= 2 * _half(x.dtype) * y.abs().max() + 1e-5 * y.abs().max()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N", [1, 3, 20])
+def test_many_sequences(N, dtype):
+    """More heads than a grid's second dimension holds."""
+    B = 70000
+    q, k, v, dout, S0, _, g = inputs(B, 1, N, 8, 8, dtype, seed=N)
+    SN = torch.empty_like(S0)
+    out = la.la_decay_forward(q, k, v, g, 0.5, S0=S0, SN=SN)
+    grads = la.la_decay_backward(q, k, v, dout, g, 0.5, S0=S0)
+    at = [0, 1, 303, 65535, 65536, B - 1]
+    qn, kn, vn, dn, Sn = (_np(t[at]) for t in (q, k, v, dout, S0))
+    ab = [np.abs(t) for t in (qn, kn, vn, dn, Sn)]
+    gn, K = _np(g), _k(N, 8)
+    ref, refS = decay.forward(qn, kn, vn, gn, 0.5, Sn)
+    H_, HS = decay.forward(*ab[:3], gn, 0.5, ab[4])
+    _rows("out", out[at], ref, H_, K, dtype)
+    _close("SN", SN[at], refS, K * U * HS)
+    for got, r, h in zip(grads, decay.backward(qn, kn, vn, dn, gn, 0.5, Sn), decay.backward(*ab[:4], gn, 0.5, ab[4])):
+        _rows("gradient", got[at], r, h, K, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("dims", [(0,), (1,), (0, 1)])
 @pytest.mark.parametrize("N", [1, 200, 900])
 def test_shared_inputs_are_their_copies(N, dims, dtype):

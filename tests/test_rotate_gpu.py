@@ -191,6 +191,33 @@ def test_in_place(D, P, pairs, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,N,Hq,Hk,D,P", [(1, 1, 37, 5, 64, 32), (2, 700, 24, 24, 64, 32), (3, 5, 1, 30, 128, 64), (4, 900, 9, 2, 66, 30)])
+def test_in_place_with_many_heads(B, N, Hq, Hk, D, P, dtype):
+    """Rows that are read ahead of the ones that are written over."""
+    q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(B, N, Hq, Hk, D, P, 1, dtype, 8, "tokens")
+    how = dict(wq=wq, wk=wk)
+    want = la.la_qk_rotate_forward(q, k, pos, freq, **how)
+    grads = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, **how)
+    got = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, dq=dqo, dk=dko, **how)
+    assert all(torch.equal(a, b) for a, b in zip(got, grads))
+    got = la.la_qk_rotate_forward(q, k, pos, freq, qo=q, ko=k, **how)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_no_query_heads(dtype):
+    q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(2, 33, 4, 3, 64, 32, 1, dtype, 9)
+    none = q[:, :0]
+    want = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk)
+    qo, ko = la.la_qk_rotate_forward(none, k, pos, freq, wq, wk)
+    assert qo.numel() == 0 and torch.equal(ko, want[1])
+    want = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk)
+    dq, dk, dwq, dwk = la.la_qk_rotate_backward(none, dko, none, k, pos, freq, wq, wk)
+    assert dq.numel() == 0 and torch.equal(dk, want[1]) and not dwq.any()
+    assert (dwk - want[3]).abs().max() <= 1e-5 * want[3].abs().max()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_rows_of_zeros_and_extremes(dtype):
     q, k, dqo, dko, pos, freq, _, wq, wk = inputs(1, 8, 2, 2, 64, 32, 1, dtype, 6)
     q[:, :, 3] = 0.0
