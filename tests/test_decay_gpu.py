@@ -341,6 +341,37 @@ def test_a_few_tokens(B, H, D, M, N, dtype):
     assert torch.equal(S, alone)
 
 
+@pytest.mark.parametrize("N,lens", [(1, None), (9, [9, 4]), (70, None), (300, [300, 131]), (900, None)])
+@pytest.mark.parametrize("D,M", [(64, 64), (24, 72)])
+def test_gradients_against_differences(N, lens, D, M):
+    """fp32.  The outputs and the last state are linear in each of q, k, v and S0: half the difference at x + d and
+    x - d, weighed with dout and dSN, is the gradient's product with d, but for the roundings of both sides (K u of the
+    majorants)."""
+    q, k, v, dout, S0, dSN, g = inputs(2, 2, N, D, M, torch.float32, seed=N)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=DEV)
+    dS0 = torch.empty_like(S0)
+    grads = la.la_decay_backward(q, k, v, dout, g, 0.3, S0=S0, dSN=dSN, dS0=dS0, lens=ln)
+    rng = torch.Generator().manual_seed(N + 1)
+    K = _k(N, max(D, M))
+    args = [q, k, v, S0]
+    for i, grad in enumerate((*grads, dS0)):
+        d = torch.randn(args[i].shape, generator=rng).to(DEV)
+        sides, bound = [], 0.0
+        for sign in (1.0, -1.0):
+            a = [t + sign * d if j == i else t for j, t in enumerate(args)]
+            SN = torch.empty_like(S0)
+            out = la.la_decay_forward(a[0], a[1], a[2], g, 0.3, S0=a[3], SN=SN, lens=ln)
+            sides.append((_np(dout) * _np(out)).sum() + (_np(dSN) * _np(SN)).sum())
+            H_, HS = decay.forward(*(np.abs(_np(t)) for t in a[:3]), _np(g), 0.3, np.abs(_np(a[3])), lens)
+            bound += (np.abs(_np(dout)) * H_).sum() + (np.abs(_np(dSN)) * HS).sum()
+        ab = [np.abs(_np(t)) for t in (q, k, v, dout, S0, dSN)]
+        h = decay.backward(*ab[:4], _np(g), 0.3, ab[4], ab[5], lens)[i]
+        bound += (np.abs(_np(d)) * h).sum()
+        off = abs((sides[0] - sides[1]) / 2 - (_np(grad) * _np(d)).sum())
+        # x + d is rounded too: once more u of every term
+        assert off <= (K + 2) * U * bound, (i, off, K * U * bound)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("N", [1, 5, 20, 200, 1100])
 def test_states_off_16_bytes(N, dtype):

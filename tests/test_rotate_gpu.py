@@ -204,6 +204,28 @@ def test_in_place_with_many_heads(B, N, Hq, Hk, D, P, dtype):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("pairs", PAIRS)
+@pytest.mark.parametrize("D,P", [(64, 32), (50, 13)])
+def test_gradients_against_differences(D, P, pairs):
+    """fp32, central differences along random directions.  With e = 2^-6 of a direction the cut third order term is of
+    the relative size e^2 (2.4e-4 of the product of norms); the roundings of outputs of size 1 are u / e of it (4e-6)."""
+    q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(2, 20, 3, 2, D, P, 1, torch.float32, 11)
+    wq, wk = (torch.ones(D, device=DEV) if w is None else w for w in (wq, wk))
+    grads = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk, pairs=pairs)
+    args, e = [q, k, wq, wk], 2.0 ** -6
+    rng = torch.Generator().manual_seed(3)
+    for i, grad in enumerate(grads):
+        d = torch.randn(args[i].shape, generator=rng).to(DEV)
+        sides = []
+        for sign in (e, -e):
+            a = [t + sign * d if j == i else t for j, t in enumerate(args)]
+            qo, ko = la.la_qk_rotate_forward(a[0], a[1], pos, freq, a[2], a[3], pairs=pairs)
+            sides.append(float((dqo.double() * qo.double()).sum() + (dko.double() * ko.double()).sum()))
+        want = float((grad.double() * d.double()).sum())
+        size = float((dqo if i % 2 == 0 else dko).double().norm()) * float(d.double().norm() if i < 2 else (d.double().norm() * (args[i - 2].numel() / D) ** 0.5))
+        assert abs((sides[0] - sides[1]) / (2 * e) - want) <= 1e-3 * size, (i, sides, want, size)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_no_query_heads(dtype):
     q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(2, 33, 4, 3, 64, 32, 1, dtype, 9)

@@ -83,8 +83,8 @@ __device__ __forceinline__ float dot(const float4 &a, const float4 &b, float t) 
 // memory 59 % (the backward of 128 heads of 1024 tokens, 64 channels: 384 us).
 // Tiles of 8 x 4 on half of the threads were slower (7 ragged sequences of 1537
 // tokens, 5 heads: 108 -> 128 us), and so were 512 threads above 64 channels (128
-// heads of 1024 tokens, 128 channels: 491 -> 555 us).  Tensor cores would need six bf16 products (or
-// three of tf32) in place of each of these to keep fp32's digits.
+// heads of 1024 tokens, 128 channels: 491 -> 555 us).  Tensor cores would need six
+// bf16 products (or three of tf32) in place of each of these to keep fp32's digits.
 template <typename T, int DT>
 __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const __grid_constant__ DecayLaunch l) {
     extern __shared__ __align__(16) float sm[];
