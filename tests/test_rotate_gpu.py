@@ -121,6 +121,31 @@ def test_widths(D, P, pairs, dtype):
     check(2, 9, 3, 2, D, P, dtype=dtype, pairs=pairs, seed=D + P)
 
 
+@pytest.mark.parametrize("pairs", PAIRS)
+@pytest.mark.parametrize("N", [1, 70])
+@pytest.mark.parametrize("D,P", [(8, 4), (24, 8), (24, 12), (40, 20), (72, 36), (72, 4), (104, 0), (136, 68), (248, 100), (48, 20)])
+def test_pieces_of_8_bytes(D, P, N, pairs):
+    """bf16 heads that are a multiple of 8 channels wide, not of 16."""
+    check(2, N, 5, 3, D, P, dtype=torch.bfloat16, pairs=pairs, seed=D + P, layout="tokens")
+
+
+@pytest.mark.parametrize("pairs", PAIRS)
+def test_rows_on_8_bytes(pairs):
+    """bf16 rows whose strides are a multiple of 8 bytes, not of 16."""
+    q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(2, 21, 3, 2, 64, 32, 1, torch.bfloat16, 12)
+    want = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk, pairs=pairs)
+    grads = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk, pairs=pairs)
+
+    def on8(t):
+        return torch.cat([t, t[..., :4]], dim=-1)[..., :-4]
+    q, k, dqo, dko = (on8(t) for t in (q, k, dqo, dko))
+    assert q.stride(-2) == 68
+    got = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk, pairs=pairs)
+    for a, b in zip((*got, *la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk, pairs=pairs)), (*want, *grads)):
+        tol = 2 * torch.finfo(a.dtype).eps if a.dtype == torch.bfloat16 else 1e-5   # sums in another order: a rounding apart
+        assert (a.double() - b.double()).abs().max() <= tol * b.double().abs().max()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("norm,weights", [(True, True), (True, False), (False, False)])
 @pytest.mark.parametrize("layout", ["heads", "tokens", "odd"])

@@ -13,11 +13,12 @@
 // heads' rows are on their way while some are worked on, the first ones while
 // the angles are, and the weights lie in shared memory, which leaves the
 // registers for it.  Measured (40 heads of 64 channels, 8 x 4096 tokens, bf16):
-// forward 57 us, 5.9 of the copy's 6.8 TB/s, backward 107 us, 4.7 (without the
-// rows ahead 71 and 122).  The bf16 backward is held back by its registers, one
-// head ahead: with two it spilled (154 us).  fp32 rows by pieces reach 6.4 TB/s
-// both ways; rows by single values are bound by their instructions (16384 tokens
-// of 32 heads of 66 channels, bf16: 87 and 166 us, 1.6 and 1.25 TB/s).
+// forward 57 us, 5.9 of the copy's 6.8 TB/s, backward 90 us, 5.6 (without the
+// rows ahead 71 and 122).  The bf16 backward takes pieces of 8 bytes, four heads
+// ahead: with 16 the weights' sums leave room for one (107 us).  fp32 rows reach
+// 6.4 TB/s both ways; rows by single values are bound by their instructions (16384
+// tokens of 32 heads of 66 channels, bf16: 87 and 169 us, 1.6 and 1.2 TB/s; of 72
+// channels, by 8 bytes, 51 and 77).
 #include <algorithm>
 #include <cstring>
 
@@ -66,10 +67,10 @@ __device__ __forceinline__ unsigned long long turns(float f) {
 }
 
 // How a lane's V pairs lie in a head's row: kHalf, kAdjacent: V neighbouring pairs
-// by 16 byte pieces; kAny: pairs a warp apart by single values.
+// by pieces of V values, 16 bytes or (bf16, V = 4) 8; kAny: pairs a warp apart by single values.
 enum Layout { kHalf, kAdjacent, kAny };
 // CTAs that an SM holds: rows by pieces take the registers for their loads (three of
-// them an SM: 8 x 4096 tokens backward 107 -> 214 us, spilled), single values the
+// them an SM: fp32 backward, 4 x 8192 tokens of 32 heads of 64, 126 -> 145 us), single values the
 // warps (3 x 1234 tokens of 12 heads of 90 channels, two: 15 and 27 us, so 11 and 23).
 constexpr int slots_of(Layout l, bool bwd) { return l != kAny ? 2 : bwd ? 3 : 4; }
 
@@ -81,8 +82,14 @@ __device__ __forceinline__ int second_of(int p, int P, int D, bool half) {
 }
 
 // A lane's share of a row as it lies in memory: 2V values.
+template <int bytes> struct Piece {
+    using type = uint4;
+};
+template <> struct Piece<8> {
+    using type = uint2;
+};
 template <typename T, Layout L, int V> struct Raw {
-    uint4 w[2 * V * sizeof(T) / 16];
+    typename Piece<V * sizeof(T)>::type w[2];
 };
 template <typename T, int V> struct Raw<T, kAny, V> {
     T v[2 * V];
@@ -110,13 +117,14 @@ __device__ __forceinline__ Raw<T, L, V> load_raw(const T *row, int lane, int P, 
             }
         }
     } else {
-        static_assert(V * sizeof(T) == 16, "a piece is V values");
+        static_assert(V * sizeof(T) == 16 || V * sizeof(T) == 8, "a piece is V values");
+        using piece = typename Piece<V * sizeof(T)>::type;
         const int p = V * lane;
         const bool in = p < D / 2;
         const T *x = row + (L == kHalf ? first_of(p, P, true) : 2 * p);
         const T *y = L == kHalf ? row + second_of(p, P, D, true) : x + V;
-        r.w[0] = in ? *reinterpret_cast<const uint4 *>(x) : make_uint4(0, 0, 0, 0);
-        r.w[1] = in ? *reinterpret_cast<const uint4 *>(y) : make_uint4(0, 0, 0, 0);
+        r.w[0] = in ? *reinterpret_cast<const piece *>(x) : piece{};
+        r.w[1] = in ? *reinterpret_cast<const piece *>(y) : piece{};
     }
     return r;
 }
@@ -134,8 +142,16 @@ template <typename T, Layout L, int V> __device__ __forceinline__ Pairs<V> pairs
             o.b[i] = make_float2(to_f32(r.v[4 * i + 1]), to_f32(r.v[4 * i + 3]));
         }
     } else {
-        const uint4 x = r.w[0], y = r.w[1];
-        if constexpr (sizeof(T) == 4) {
+        const auto x = r.w[0], y = r.w[1];
+        if constexpr (sizeof(T) * V == 8) {
+            if constexpr (L == kHalf) {
+                o.a[0] = get_pair(x.x), o.a[1] = get_pair(x.y);
+                o.b[0] = get_pair(y.x), o.b[1] = get_pair(y.y);
+            } else {
+                o.a[0] = floats(x.x << 16, x.y << 16), o.b[0] = floats(x.x & 0xffff0000u, x.y & 0xffff0000u);
+                o.a[1] = floats(y.x << 16, y.y << 16), o.b[1] = floats(y.x & 0xffff0000u, y.y & 0xffff0000u);
+            }
+        } else if constexpr (sizeof(T) == 4) {
             if constexpr (L == kHalf) {
                 o.a[0] = floats(x.x, x.y), o.a[1] = floats(x.z, x.w);
                 o.b[0] = floats(y.x, y.y), o.b[1] = floats(y.z, y.w);
@@ -172,7 +188,18 @@ __device__ __forceinline__ void store_pairs(T *row, const Pairs<V> &v, int lane,
         if (p >= D / 2) return;
         T *x = row + (L == kHalf ? first_of(p, P, true) : 2 * p);
         T *y = L == kHalf ? row + second_of(p, P, D, true) : x + V;
-        if constexpr (sizeof(T) == 4) {
+        [[maybe_unused]] auto word = [&](int i) {
+            return i % 2 ? put_pair(make_float2(v.a[i / 2].y, v.b[i / 2].y)) : put_pair(make_float2(v.a[i / 2].x, v.b[i / 2].x));
+        };
+        if constexpr (sizeof(T) * V == 8) {
+            if constexpr (L == kHalf) {
+                *reinterpret_cast<uint2 *>(x) = make_uint2(put_pair(v.a[0]), put_pair(v.a[1]));
+                *reinterpret_cast<uint2 *>(y) = make_uint2(put_pair(v.b[0]), put_pair(v.b[1]));
+            } else {
+                *reinterpret_cast<uint2 *>(x) = make_uint2(word(0), word(1));
+                *reinterpret_cast<uint2 *>(y) = make_uint2(word(2), word(3));
+            }
+        } else if constexpr (sizeof(T) == 4) {
             if constexpr (L == kHalf) {
                 *reinterpret_cast<float4 *>(x) = make_float4(v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y);
                 *reinterpret_cast<float4 *>(y) = make_float4(v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y);
@@ -184,9 +211,6 @@ __device__ __forceinline__ void store_pairs(T *row, const Pairs<V> &v, int lane,
             *reinterpret_cast<uint4 *>(x) = make_uint4(put_pair(v.a[0]), put_pair(v.a[1]), put_pair(v.a[2]), put_pair(v.a[3]));
             *reinterpret_cast<uint4 *>(y) = make_uint4(put_pair(v.b[0]), put_pair(v.b[1]), put_pair(v.b[2]), put_pair(v.b[3]));
         } else {
-            auto word = [&](int i) {
-                return i % 2 ? put_pair(make_float2(v.a[i / 2].y, v.b[i / 2].y)) : put_pair(make_float2(v.a[i / 2].x, v.b[i / 2].x));
-            };
             *reinterpret_cast<uint4 *>(x) = make_uint4(word(0), word(1), word(2), word(3));
             *reinterpret_cast<uint4 *>(y) = make_uint4(word(4), word(5), word(6), word(7));
         }
@@ -233,7 +257,7 @@ __device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y)
 // while the next U are on their way.
 template <typename T, int V, int G, Layout L, bool BWD, bool NORM>
 __global__ void __launch_bounds__(kThreads, slots_of(L, BWD)) rotate_kernel(const __grid_constant__ RotArgs a) {
-    constexpr int U = L == kAny ? (BWD ? 1 : 2) : BWD ? 8 / V : 4, E = V / 2;
+    constexpr int U = L == kAny ? (BWD ? 1 : 2) : BWD && sizeof(T) == 4 ? 2 : 4, E = V / 2;
     const int lane = threadIdx.x % G, D = a.D, P = a.P;
     const bool half = L == kHalf || (L == kAny && a.half);
     const unsigned groups = gridDim.x * (kThreads / G), tokens = (unsigned)a.B * a.N, items = tokens * a.splits;
@@ -411,9 +435,9 @@ __global__ void __launch_bounds__(32 * kSumWarps) weight_sums_kernel(const float
 constexpr int kSms = 152;
 constexpr int kBwdCtas = kSms * 2;   // for each of queries and keys; their sums are written: few, that stay
 
-bool on_boundary(const void *p, long long b, long long h, long long n, size_t bytes) {
+bool on_boundary(const void *p, long long b, long long h, long long n, size_t bytes, size_t piece) {
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(b * bytes) | (uintptr_t)(h * bytes) |
-                             (uintptr_t)(n * bytes)) & 15) == 0;
+                             (uintptr_t)(n * bytes)) & (piece - 1)) == 0;
 }
 
 template <typename T, int V, int G, Layout L, bool BWD>
@@ -427,22 +451,20 @@ cudaError_t launch(const RotArgs &a, int ctas, bool norm, cudaStream_t st) {
 }
 
 // Lanes to a token where rows are taken by pieces of V values: what D takes, rounded up.
-template <typename T> int lanes_of(int D) {
-    constexpr int V = 16 / sizeof(T), least = 32 / V;   // 4 (bf16) or 8 (fp32) lanes: D = 64
-    return D <= 64 ? least : D <= 128 ? 2 * least : 4 * least;
+int lanes_of(int D, int V) { return (D <= 64 ? 32 : D <= 128 ? 64 : 128) / V; }
+
+template <typename T, int V, Layout L, bool BWD>
+cudaError_t pick_lanes(const RotArgs &a, int ctas, bool norm, cudaStream_t st) {
+    constexpr int least = 32 / V;   // D = 64
+    if (a.D <= 64) return launch<T, V, least, L, BWD>(a, ctas, norm, st);
+    return a.D <= 128 ? launch<T, V, 2 * least, L, BWD>(a, ctas, norm, st) : launch<T, V, 4 * least, L, BWD>(a, ctas, norm, st);
 }
 
-template <typename T, Layout L, bool BWD> cudaError_t pick_lanes(const RotArgs &a, int ctas, bool norm, cudaStream_t st) {
-    constexpr int V = 16 / sizeof(T), least = 32 / V;
-    const int G = lanes_of<T>(a.D);
-    if (G == least) return launch<T, V, least, L, BWD>(a, ctas, norm, st);
-    return G == 2 * least ? launch<T, V, 2 * least, L, BWD>(a, ctas, norm, st) : launch<T, V, 4 * least, L, BWD>(a, ctas, norm, st);
-}
-
-template <typename T, bool BWD> cudaError_t pick(const RotArgs &a, Layout l, int ctas, bool norm, cudaStream_t st) {
-    if (l == kHalf) return pick_lanes<T, kHalf, BWD>(a, ctas, norm, st);
-    if (l == kAdjacent) return pick_lanes<T, kAdjacent, BWD>(a, ctas, norm, st);
-    return a.D <= 128 ? launch<T, 2, 32, kAny, BWD>(a, ctas, norm, st) : launch<T, 4, 32, kAny, BWD>(a, ctas, norm, st);
+template <typename T, bool BWD> cudaError_t pick(const RotArgs &a, Layout l, int V, int ctas, bool norm, cudaStream_t st) {
+    if (l == kAny) return a.D <= 128 ? launch<T, 2, 32, kAny, BWD>(a, ctas, norm, st) : launch<T, 4, 32, kAny, BWD>(a, ctas, norm, st);
+    if constexpr (sizeof(T) == 2 && !BWD)
+        if (V == 8) return l == kHalf ? pick_lanes<T, 8, kHalf, BWD>(a, ctas, norm, st) : pick_lanes<T, 8, kAdjacent, BWD>(a, ctas, norm, st);
+    return l == kHalf ? pick_lanes<T, 4, kHalf, BWD>(a, ctas, norm, st) : pick_lanes<T, 4, kAdjacent, BWD>(a, ctas, norm, st);
 }
 
 cudaError_t rotate(const RotateProblem &p, bool bwd) {
@@ -450,8 +472,12 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
     const bool half = p.rot.pairs == LA_PAIRS_HALF;
     const la_view x[2] = {p.q, p.k}, y[2] = {p.qo, p.ko}, dy[2] = {p.dqo, p.dko};
     const size_t size = p.s.dtype == LA_DTYPE_F32 ? 4 : 2;
-    const int V = 16 / (int)size;
-    bool wide = p.s.D % (2 * V) == 0 && (!half || p.rot.P % V == 0);
+    // pieces of 16 bytes where every row allows them; for bf16 else, and backward, of 8
+    bool wide[2];   // pieces of 16 and of 8 bytes
+    for (int i = 0; i < 2; i++) {
+        const int V = (16 >> i) / (int)size;
+        wide[i] = V >= 4 && p.s.D % (2 * V) == 0 && (!half || p.rot.P % V == 0);
+    }
     for (int s = 0; s < 2; s++) {
         a.H[s] = s ? p.s.Hk : p.s.Hq;
         a.x[s] = x[s].data, a.y[s] = y[s].data, a.dy[s] = dy[s].data;
@@ -460,9 +486,10 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
         a.db[s] = dy[s].sb, a.dh[s] = dy[s].sh, a.dn[s] = dy[s].sn;
         a.w[s] = s ? p.wk : p.wq;
         if (a.H[s] == 0) continue;
-        wide = wide && on_boundary(x[s].data, x[s].sb, x[s].sh, x[s].sn, size) &&
-               on_boundary(y[s].data, y[s].sb, y[s].sh, y[s].sn, size) &&
-               (!bwd || on_boundary(dy[s].data, dy[s].sb, dy[s].sh, dy[s].sn, size));
+        for (int i = 0; i < 2; i++)
+            wide[i] = wide[i] && on_boundary(x[s].data, x[s].sb, x[s].sh, x[s].sn, size, 16 >> i) &&
+                      on_boundary(y[s].data, y[s].sb, y[s].sh, y[s].sn, size, 16 >> i) &&
+                      (!bwd || on_boundary(dy[s].data, dy[s].sb, dy[s].sh, dy[s].sn, size, 16 >> i));
     }
     a.pos = p.rot.pos, a.sa = p.rot.sa, a.sb = p.rot.sb, a.sn = p.rot.sn, a.freq = p.rot.freq;
     a.B = p.s.B, a.N = p.s.N, a.D = p.s.D, a.P = p.rot.P, a.eps = p.eps;
@@ -470,10 +497,11 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
         memcpy(a.axes, p.rot.axes, p.rot.P);
         for (int i = 0; i < p.rot.P; i++) a.by_axis |= p.rot.axes[i] != 0;
     }
-    // 16 byte pieces where every row allows them, else single values, 32 lanes to a token
-    const Layout l = !wide ? kAny : half ? kHalf : kAdjacent;
+    // else single values, 32 lanes to a token
+    const Layout l = !wide[0] && !wide[1] ? kAny : half ? kHalf : kAdjacent;
+    const int V = size == 2 && wide[0] && !bwd ? 8 : 4;
     a.half = half;
-    const int G = l == kAny ? 32 : size == 4 ? lanes_of<float>(p.s.D) : lanes_of<__nv_bfloat16>(p.s.D);
+    const int G = l == kAny ? 32 : lanes_of(p.s.D, V);
     const long long tokens = (long long)p.s.B * p.s.N, per = kThreads / G;
     // a token's heads are shared by as many groups as fill the SMs at once, and no more
     // (4096 tokens of 32 heads of 64: 9.4 and 16.7 us, with twice as many 11.8 and 21.3)
@@ -485,10 +513,10 @@ cudaError_t rotate(const RotateProblem &p, bool bwd) {
     a.ws = sums ? static_cast<float *>(p.ws) : nullptr;
     const long long ctas = std::min((tokens * splits + per - 1) / per, bwd && p.norm ? (long long)kBwdCtas : 1LL << 30);
     const bool f32 = p.s.dtype == LA_DTYPE_F32;
-    cudaError_t e = bwd ? (f32 ? pick<float, true>(a, l, (int)ctas, p.norm, p.stream)
-                               : pick<__nv_bfloat16, true>(a, l, (int)ctas, p.norm, p.stream))
-                        : (f32 ? pick<float, false>(a, l, (int)ctas, p.norm, p.stream)
-                               : pick<__nv_bfloat16, false>(a, l, (int)ctas, p.norm, p.stream));
+    cudaError_t e = bwd ? (f32 ? pick<float, true>(a, l, V, (int)ctas, p.norm, p.stream)
+                               : pick<__nv_bfloat16, true>(a, l, V, (int)ctas, p.norm, p.stream))
+                        : (f32 ? pick<float, false>(a, l, V, (int)ctas, p.norm, p.stream)
+                               : pick<__nv_bfloat16, false>(a, l, V, (int)ctas, p.norm, p.stream));
     if (e != cudaSuccess || !sums) return e;
     weight_sums_kernel<<<(2 * p.s.D + 31) / 32, 32 * kSumWarps, 0, p.stream>>>(a.ws, (int)ctas, p.s.D, p.dwq, p.dwk);
     count_launches(1);
