@@ -575,7 +575,7 @@ typedef struct {
  * Norm of every head of the queries and keys, and their rotation, in one pass:
  *   n = x rstd w,  rstd = 1/sqrt(mean(x^2) + eps) over the head's D channels
  *   (y_i, y_j) = (n_i cos - n_j sin, n_j cos + n_i sin) for the pairs (i, j);
- *   the channels behind the 2P rotated ones: y = n.
+ *   the channels behind the 2P rotated ones: y = n, whatever the others hold.
  *   q, qo: [B,Hq,N,D]; k, ko: [B,Hk,N,D], views of dtype s.dtype; Hk = 0: no
  *      keys.  qo may be q and ko may be k (same strides): in place.
  *   norm 0: n = x (wq and wk have to be NULL); else wq, wk: D fp32 values each,

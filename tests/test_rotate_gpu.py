@@ -335,3 +335,49 @@ def test_streams_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pairs", PAIRS)
+@pytest.mark.parametrize("D,P", [(64, 16), (64, 0), (72, 20), (66, 13), (128, 3), (256, 100)])
+def test_channels_behind_the_rotated_ones_stay_apart(D, P, pairs, dtype, bad):
+    """A value that is not finite in a channel behind the rotated ones is seen by that channel alone: bit for bit what
+    the other channels are without it, rows by pieces (16 and 8 bytes) and by single values."""
+    q, k, dqo, dko, pos, freq, axes, wq, wk = inputs(1, 9, 2, 3, D, P, 1, dtype, D + P)
+    for c in {2 * P, 2 * P + 1, P + D // 2, D - 1} - set(range(2 * P)):
+        rest = [i for i in range(D) if i != c]
+        how = dict(norm=False, pairs=pairs)
+        hit = [t.clone() for t in (q, k, dqo, dko)]
+        for t in hit:
+            t[:, :, ::2, c] = bad
+        a, b = (la.la_qk_rotate_forward(x, y, pos, freq, **how) for x, y in ((q, k), hit[:2]))
+        a += la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, **how)[:2]
+        b += la.la_qk_rotate_backward(hit[2], hit[3], q, k, pos, freq, **how)[:2]
+        for clean, got, x in zip(a, b, hit):
+            assert torch.equal(got[..., rest], clean[..., rest])
+            assert torch.equal(torch.nan_to_num(got[..., c], 1, 2, 3), torch.nan_to_num(x[..., c], 1, 2, 3))
+        # with the norm: 1/sqrt(infinity) is 0, so the finite channels are 0; the sums of the weights stay apart
+        if bad == float("inf"):
+            qo, _ = la.la_qk_rotate_forward(hit[0], k, pos, freq, wq, wk, pairs=pairs)
+            assert not qo[:, :, ::2][..., rest].any() and torch.isnan(qo[:, :, ::2, c]).all()
+        clean = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk, pairs=pairs)[2:]
+        got = la.la_qk_rotate_backward(hit[2], hit[3], q, k, pos, freq, wq, wk, pairs=pairs)[2:]
+        for x, y in zip(got, clean):
+            assert torch.equal(x[rest], y[rest]) and not torch.isfinite(x[c])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pairs", PAIRS)
+@pytest.mark.parametrize("D,P", [(64, 16), (64, 0), (72, 20), (66, 13)])
+def test_channels_behind_the_rotated_ones_are_copied(D, P, pairs, dtype):
+    """Without the norm they leave as they came, the signs of zeros among them."""
+    q, k, dqo, dko, pos, freq, axes, _, _ = inputs(2, 11, 3, 2, D, P, 1, dtype, D)
+    for t in (q, k, dqo, dko):
+        t[..., ::3] = 0.0
+        t[..., ::2] *= -1.0
+    got = la.la_qk_rotate_forward(q, k, pos, freq, norm=False, pairs=pairs)
+    got += la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, norm=False, pairs=pairs)[:2]
+    words = torch.int16 if dtype == torch.bfloat16 else torch.int32
+    for y, x in zip(got, (q, k, dqo, dko)):
+        assert torch.equal(y[..., 2 * P:].contiguous().view(words), x[..., 2 * P:].contiguous().view(words))

@@ -21,6 +21,7 @@
 // channels, by 8 bytes, 51 and 77).
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "la_layer.h"
 #include "la_pair.cuh"
@@ -101,6 +102,45 @@ template <int V> struct Pairs {
 
 template <int V, Layout L> __device__ __forceinline__ int pair_of_lane(int lane, int i) {
     return L == kAny ? lane + 32 * i : V * lane + i;
+}
+
+// Two pairs (a, b), turned.
+__device__ __forceinline__ void turn(float2 a, float2 b, float2 c, float2 s, float2 &ta, float2 &tb) {
+    const float2 bs = mul_pair(b, s);
+    ta = fma_pair(a, c, make_float2(-bs.x, -bs.y));
+    tb = fma_pair(b, c, mul_pair(a, s));
+}
+// The same where pairs may not turn (x, y: whether they do), the channels behind the
+// rotated ones: these leave as they came.  With cos 1 and sin 0 a value that is not
+// finite would reach the other channel as 0 times itself, so a zero takes its place (of
+// the sign that adds nothing to a zero of either).  By kernels of their own, as that
+// costs registers (2 x 16384 tokens of 32 heads of 128, bf16, half of the channels: 86 ->
+// 90 us forward, 142 -> 145 backward; in one kernel for both, rows that turn as a whole
+// paid 1 to 4 % too).
+__device__ __forceinline__ void turn_some(float2 a, float2 b, float2 c, float2 s, bool x, bool y, float2 &ta, float2 &tb) {
+    const float2 bs = mul_pair(make_float2(x ? b.x : 0.f, y ? b.y : 0.f), s);
+    const float2 as = mul_pair(make_float2(x ? a.x : -0.f, y ? a.y : -0.f), s);
+    ta = fma_pair(a, c, make_float2(-bs.x, -bs.y));
+    tb = fma_pair(b, c, as);
+}
+// A lane's pairs, turned; back: by the angles' negatives; ALL: every channel turns.
+template <int V, Layout L, bool back, bool ALL>
+__device__ __forceinline__ void turn_pairs(const Pairs<V> &v, const float2 (&c)[V / 2], const float2 (&s)[V / 2], int lane,
+                                           int P, Pairs<V> &o) {
+    const auto &a = back ? v.b : v.a, &b = back ? v.a : v.b;
+    auto &ta = back ? o.b : o.a, &tb = back ? o.a : o.b;
+    [[maybe_unused]] const int left = P - pair_of_lane<V, L>(lane, 0);
+    if constexpr (ALL) {
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) turn(a[i], b[i], c[i], s[i], ta[i], tb[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; i++) {   // halves by pieces: P is a multiple of V
+            const bool x = pair_of_lane<V, L>(0, L == kHalf ? 0 : 2 * i) < left;
+            const bool y = L == kHalf ? x : pair_of_lane<V, L>(0, 2 * i + 1) < left;
+            turn_some(a[i], b[i], c[i], s[i], x, y, ta[i], tb[i]);
+        }
+    }
 }
 
 template <typename T, Layout L, int V>
@@ -251,11 +291,10 @@ __device__ __forceinline__ void angles(const RotArgs &a, int lane, long long at,
 }
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 neg(float2 v) { return make_float2(-v.x, -v.y); }
 
-// G lanes to a token; BWD: the gradients; NORM: with the norm.  U heads are worked on
-// while the next U are on their way.
-template <typename T, int V, int G, Layout L, bool BWD, bool NORM>
+// G lanes to a token; BWD: the gradients; NORM: with the norm; ALL: no channels behind the
+// rotated ones.  U heads are worked on while the next U are on their way.
+template <typename T, int V, int G, Layout L, bool BWD, bool NORM, bool ALL>
 __global__ void __launch_bounds__(kThreads, slots_of(L, BWD)) rotate_kernel(const __grid_constant__ RotArgs a) {
     constexpr int U = L == kAny ? (BWD ? 1 : 2) : BWD && sizeof(T) == 4 ? 2 : 4, E = V / 2;
     const int lane = threadIdx.x % G, D = a.D, P = a.P;
@@ -343,24 +382,19 @@ __global__ void __launch_bounds__(kThreads, slots_of(L, BWD)) rotate_kernel(cons
                     rstd = rsqrtf(fmaf(group_sum<G>(sum.x + sum.y), mean, a.eps));
                 }
                 if constexpr (!BWD) {
+                    if constexpr (NORM) {
 #pragma unroll
-                    for (int i = 0; i < E; i++) {
-                        if constexpr (NORM) {
+                        for (int i = 0; i < E; i++) {
                             const float4 w = weights[s][i][lane];
                             v.a[i] = mul_pair(mul_pair(v.a[i], both(rstd)), make_float2(w.x, w.y));
                             v.b[i] = mul_pair(mul_pair(v.b[i], both(rstd)), make_float2(w.z, w.w));
                         }
-                        o.a[i] = fma_pair(v.a[i], cs[i], neg(mul_pair(v.b[i], sn[i])));
-                        o.b[i] = fma_pair(v.b[i], cs[i], mul_pair(v.a[i], sn[i]));
                     }
+                    turn_pairs<V, L, false, ALL>(v, cs, sn, lane, P, o);
                 } else {
                     const Pairs<V> d = pairs_of<T, L, V>(rd[j]);
                     Pairs<V> u;
-#pragma unroll
-                    for (int i = 0; i < E; i++) {   // turned back
-                        u.a[i] = fma_pair(d.a[i], cs[i], mul_pair(d.b[i], sn[i]));
-                        u.b[i] = fma_pair(d.b[i], cs[i], neg(mul_pair(d.a[i], sn[i])));
-                    }
+                    turn_pairs<V, L, true, ALL>(d, cs, sn, lane, P, u);
                     if constexpr (!NORM) {
                         o = u;
                     } else {
@@ -444,8 +478,13 @@ template <typename T, int V, int G, Layout L, bool BWD>
 cudaError_t launch(const RotArgs &a, int ctas, bool norm, cudaStream_t st) {
     const size_t smem = BWD && norm && a.ws ? (size_t)(kThreads / G) * a.D * sizeof(float) : 0;
     const dim3 grid(ctas, BWD ? 2 : 1);
-    if (norm) rotate_kernel<T, V, G, L, BWD, true><<<grid, kThreads, smem, st>>>(a);
-    else rotate_kernel<T, V, G, L, BWD, false><<<grid, kThreads, smem, st>>>(a);
+    auto run = [&](auto with, auto all) {
+        rotate_kernel<T, V, G, L, BWD, with.value, all.value><<<grid, kThreads, smem, st>>>(a);
+    };
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    if (norm) 2 * a.P == a.D ? run(yes, yes) : run(yes, no);
+    else 2 * a.P == a.D ? run(no, yes) : run(no, no);
     count_launches(1);
     return cudaGetLastError();
 }
