@@ -552,7 +552,8 @@ typedef enum { LA_PAIRS_HALF = 0, LA_PAIRS_ADJACENT = 1 } la_pairs;
  *      (strides in elements, 0 repeats); any int32 value.
  *   freq: device, P fp32 values, radians a position.  The angle is taken mod
  *      a turn in 64-bit fixed point before any rounding to fp32, so that far
- *      positions keep their fraction.  A freq that is not finite gives NaN.
+ *      positions keep their fraction: at any int32 position to 2^-32 turns, for
+ *      freq up to 2^64.  A freq that is not finite gives NaN.
  *   axes: host array of P axis numbers below A, read before the call returns
  *      (NULL: all on axis 0).
  *   A: axes of pos, 1 to 8; P: 0 to D/2.

@@ -381,3 +381,37 @@ def test_channels_behind_the_rotated_ones_are_copied(D, P, pairs, dtype):
     words = torch.int16 if dtype == torch.bfloat16 else torch.int32
     for y, x in zip(got, (q, k, dqo, dko)):
         assert torch.equal(y[..., 2 * P:].contiguous().view(words), x[..., 2 * P:].contiguous().view(words))
+
+
+def _exact_angles(pos, freq):
+    """[B,N,P] from pos [B,N], freq [P], mod a turn in whole numbers: no rounding before the last."""
+    one = 1 << 300
+
+    def arctan(x):     # of 1 / x
+        t, s, n = one // x, 0, 0
+        while t:
+            s += (-1) ** n * (t // (2 * n + 1))
+            t, n = t // (x * x), n + 1
+        return s
+    turn = 2 * (4 * (4 * arctan(5) - arctan(239)))
+    out = np.zeros(pos.shape + freq.shape)
+    for i, f in enumerate(freq.tolist()):
+        num, den = f.as_integer_ratio()
+        for at in np.ndindex(pos.shape):
+            a = int(pos[at]) * num * one // den % turn
+            out[at + (i,)] = float(a if 2 * a < turn else a - turn) / float(one)
+    return out
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_large_frequencies_at_far_positions(dtype):
+    """Up to 2^60 radians a position, to the last positions of 32 bits: the turn's fraction is what is left of it."""
+    q, k, dqo, dko, _, _, _, wq, wk = inputs(2, 12, 2, 2, 64, 32, 1, dtype, 13)
+    pos = torch.tensor([-(1 << 31), (1 << 31) - 1, (1 << 31) - 2, -(1 << 31) + 1, 1 << 30, 0, 1, -1, 12345, -987654321,
+                        2000000011, 77777777], dtype=torch.int32, device=DEV).expand(2, 12)
+    freq = torch.tensor([(-1.0) ** i * 2.0 ** (2 * i - 2) * (1 + i / 64) for i in range(32)], device=DEV)
+    qo, ko = la.la_qk_rotate_forward(q, k, pos, freq, wq, wk)
+    dq, dk, dwq, dwk = la.la_qk_rotate_backward(dqo, dko, q, k, pos, freq, wq, wk)
+    angle = _exact_angles(pos.cpu().numpy(), freq.cpu().numpy().astype(np.float64))
+    check_one("q", q, dqo, wq, qo, dq, dwq, angle, 1e-6, True, "half", dtype)
+    check_one("k", k, dko, wk, ko, dk, dwk, angle, 1e-6, True, "half", dtype)

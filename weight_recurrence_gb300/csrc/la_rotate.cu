@@ -50,20 +50,25 @@ struct RotArgs {
     unsigned char axes[kMaxPairs];
 };
 
-// 2^64 / (2 pi): a position's turn of 2^64 parts per radian
-constexpr unsigned long long kTurn = 0x28BE60DB9391054Aull;
+// 2^128 / (2 pi), rounded down: its halves are turns a radian in 2^-64 and 2^-128
+constexpr unsigned long long kTurnHigh = 0x28BE60DB9391054Aull, kTurnLow = 0x7F09D5F47D4D3770ull;
 
-// f radians in 2^-64 turns, mod a turn: f = m 2^e exactly, so the product with
-// kTurn (its error 2^-62 of itself) and a shift give every bit that counts.
+// f radians in 2^-64 turns, mod a turn, rounded down: f = m 2^e exactly, and the product of
+// m with 1/(2 pi) to 128 bits is off by less than f 2^-128 turns.  An angle is then off by
+// less than 2^-64 + |f| 2^-128 turns times its position: 2^-33 turns for the first at the
+// last positions of 32 bits, as much for the second at |f| = 2^64.
 __device__ __forceinline__ unsigned long long turns(float f) {
     const unsigned bits = __float_as_uint(f);
     const int field = (bits >> 23) & 255;
     const unsigned m = field ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
     const int e = (field ? field : 1) - 150;
-    const unsigned __int128 p = (unsigned __int128)m * kTurn;
+    const unsigned __int128 low = (unsigned __int128)m * kTurnLow;
+    const unsigned __int128 p = (unsigned __int128)m * kTurnHigh + (unsigned long long)(low >> 64);   // 2^-64 turns
+    const unsigned long long rest = (unsigned long long)low;                                          // 2^-128
     unsigned long long t;
-    if (e >= 0) t = e < 64 ? (unsigned long long)p << e : 0ull;
-    else t = e > -100 ? (unsigned long long)(p >> -e) : 0ull;
+    if (e <= 0) t = e > -100 ? (unsigned long long)(p >> -e) : 0ull;
+    else if (e < 64) t = (unsigned long long)p << e | rest >> (64 - e);
+    else t = rest << (e - 64);   // at most 40
     return bits >> 31 ? 0ull - t : t;
 }
 
