@@ -528,3 +528,23 @@ def test_equal_calls_give_equal_bits():
                 for _ in range(3)]
         for r in runs[1:]:
             assert all(torch.equal(a, b) for a, b in zip(r, runs[0]))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("short_of", [0, 1000])
+def test_state_of_the_longest_sequence(short_of, dtype):
+    """The largest token count that is taken, ones without a decay: every element of the state is the count.  A state
+    below 2^31 is off by at most 64 for each chunk that is added to it, of which a segment has less than 2^17 and no
+    rounding comes from the sums of whole segments before it; a segment's tokens alone are 0.7 % at most."""
+    N = (1 << 31) - 1 - (1 << 20)
+    if dtype == torch.float32:      # one row, repeated
+        k = torch.ones(1, 1, 1, 8, device=DEV).expand(1, 1, N, 8)
+    else:                           # rows 16 bytes apart, as the tensor cores' path takes them
+        k = torch.ones(1, 1, N, 8, dtype=dtype, device=DEV)
+    S = torch.zeros(1, 1, 8, 8, device=DEV)
+    lens = torch.tensor([N - short_of], dtype=torch.int32, device=DEV) if short_of else None
+    la.la_decay_forward(None, k, k, torch.zeros(1, device=DEV), SN=S, lens=lens, want_out=False)
+    off = (S.double() - (N - short_of)).abs().max()
+    del k
+    torch.cuda.empty_cache()
+    assert off <= 64 * (1 << 17) < N // 200, float(off)

@@ -284,8 +284,7 @@ __global__ void __launch_bounds__(kThreads, DT == 1 ? 2 : 1) sweep_kernel(const 
         if (out) put_state();
     }
     // the state leaves where the sequence's last segment (backwards: its first) ends
-    const int last = max(0, (len + l.seg_tokens - 1) / l.seg_tokens - 1);
-    if (s.end && (l.sums || seg == (back ? 0 : last))) {
+    if (s.end && (l.sums || seg == (back ? 0 : last_segment(len, l.seg_tokens)))) {
         float *end = s.end + (l.sums ? (size_t)bh * l.segs + seg : (size_t)bh) * DM;
 #pragma unroll
         for (int u = 0; u < DT; u++)
@@ -314,8 +313,8 @@ __global__ void __launch_bounds__(256) scan_kernel(float *ws, const float *start
     if (e >= DM) return;
     float *p = ws + (size_t)bh * segs * DM + e;
     float s = start ? start[(size_t)bh * DM + e] : 0.f;
-    // the segment that ends the sequence, and what the state loses over it and over the whole ones before
-    const int last = len > 0 ? (len - 1) / seg_tokens : -1;
+    // the segment that ends the sequence (-1: there is none), and what the state loses over it and over the whole ones before
+    const int last = len > 0 ? last_segment(len, seg_tokens) : -1;
     const float2 whole = kept(g, seg_tokens), part = kept(g, len - last * seg_tokens);
 #pragma unroll 4
     for (int i = 0; i < segs; i++) {

@@ -34,6 +34,13 @@ __device__ __forceinline__ float2 kept(float g, int n) {
 }
 __device__ __forceinline__ float keep(float2 a, float s) { return fmaf(a.y, s, a.x * s); }
 
+// The segment with a sequence's last token (0 where it has none).  The segments end below
+// 2^31, but a token past one segment more would not.
+__host__ __device__ constexpr int last_segment(int len, int seg_tokens) { return len > 0 ? (len - 1) / seg_tokens : 0; }
+static_assert(last_segment(0, 128) == 0 && last_segment(128, 128) == 0 && last_segment(129, 128) == 1 &&
+                  last_segment(2146435071, 7060736) == 303 && last_segment(2146435071, 2146435071) == 0,
+              "lengths up to the largest");
+
 struct DecaySweep {
     la_view x, y, z, out;      // out.data null: the state alone (x is not read)
     const float *start;        // state before the sweep, null: 0

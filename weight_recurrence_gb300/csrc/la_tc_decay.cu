@@ -731,8 +731,7 @@ __global__ void __launch_bounds__(kDecayThreads, 1) decay_tc_kernel(const __grid
             if (it > 0 && out) put_snap(it);
         }
         // the state leaves where the sequence's last segment (backwards: its first) ends
-        const int last = max(0, (len + args.seg_tokens - 1) / args.seg_tokens - 1);
-        if (sw.end && !*abort && (args.sums || seg == (backwards ? 0 : last))) {
+        if (sw.end && !*abort && (args.sums || seg == (backwards ? 0 : last_segment(len, args.seg_tokens)))) {
             float *end = sw.end + (args.sums ? (size_t)bh * args.segs + seg : (size_t)bh) * DM;
             if (wide(end)) {
 #pragma unroll
