@@ -484,7 +484,9 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
  *      1 <= D, M <= 128 (larger: LA_ERR_UNSUPPORTED, as 8 B H >= 2^31 and
       N >= 2^31 - 2^20).  Inputs may repeat heads or sequences (stride 0).
  *   log_decay: H fp32 values on the device; 0 forgets nothing, -infinity
- *      keeps the token itself alone; above 0 the state grows.
+ *      keeps the token itself alone; above 0 the state grows: up to 1/2, rows
+ *      of 0 add 0 to it however long.  (Values are weighed by up to a^128 in
+ *      fp32: what that takes past its range is not finite.)
  *   S0, SN: [B,H,D,M] contiguous fp32, the state before the first token
  *      (NULL: 0) and the one after the last (NULL: not wanted); SN may be S0.
  *   out.data NULL: the state alone (q is not read and its data may be NULL;

@@ -548,3 +548,70 @@ def test_state_of_the_longest_sequence(short_of, dtype):
     del k
     torch.cuda.empty_cache()
     assert off <= 64 * (1 << 17) < N // 200, float(off)
+
+
+def _growing(dtype, seed):
+    """Sequences that are cut into segments of some hundred tokens."""
+    H, N = (40, 2000) if dtype == torch.float32 else (8, 5000)
+    return H, N, inputs(1, H, N, 16, 16, dtype, seed, decays=[0.3] * H)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_growing_states_that_are_zero_stay_zero(dtype):
+    """a^n over a segment is past fp32's range, but nothing is there yet to grow."""
+    H, N, (q, k, v, dout, _, _, g) = _growing(dtype, 3)
+    k[:, :, :N - 100] = 0.0
+    SN = torch.empty(1, H, 16, 16, device=DEV)
+    out = la.la_decay_forward(q, k, v, g, 0.25, SN=SN)
+    qn, kn, vn, gn = (_np(t) for t in (q, k, v, g))
+    ref, refS = decay.forward(qn, kn, vn, gn, 0.25)
+    H_, HS = decay.forward(np.abs(qn), np.abs(kn), np.abs(vn), gn, 0.25)
+    K = _k(N, 16)
+    _rows("out", out, ref, H_, K, dtype)
+    _close("SN", SN, refS, K * U * HS)
+    # backwards in time: gradients of the first tokens' outputs alone
+    q, k, v, dout = _growing(dtype, 4)[2][:4]
+    dout[:, :, 100:] = 0.0
+    dS0 = torch.empty_like(SN)
+    dq, dk, dv = la.la_decay_backward(q, k, v, dout, g, 0.25, dS0=dS0)
+    part = [_np(t[:, :, :100]) for t in (q, k, v, dout)]
+    refs = decay.backward(*part, gn, 0.25)
+    hs = decay.backward(*(np.abs(t) for t in part), gn, 0.25)
+    for name, got, r, h in zip(("dq", "dk", "dv"), (dq, dk, dv), refs, hs):
+        _rows(name, got[:, :, :100], r, h, K, dtype)
+    assert not dk[:, :, 100:].any() and not dv[:, :, 100:].any()
+    _close("dS0", dS0, refs[3], K * U * hs[3])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_growing_states_that_are_small(dtype):
+    """a^n over a segment is past fp32's range, its product with a small state is not."""
+    H, N, (q, k, v, dout, S0, dSN, _) = _growing(dtype, 5)
+    S0, dSN = 1e-30 * S0, 1e-30 * dSN
+    K = _k(N, 16)
+    qn, kn, vn, Sn, En = (_np(t) for t in (q, k, v, S0, dSN))
+    ab = [np.abs(t) for t in (qn, kn, vn, Sn, En)]
+    n = 500                                     # a segment of 384 and the next
+    g = torch.full((H,), 0.25, device=DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    SN = torch.empty_like(S0)
+    out = la.la_decay_forward(q, torch.zeros_like(k), v, g, 0.25, S0=S0, SN=SN, lens=lens)
+    ref, refS = decay.forward(qn, 0 * kn, vn, _np(g), 0.25, Sn, [n])
+    H_, HS = decay.forward(ab[0], 0 * kn, ab[2], _np(g), 0.25, ab[3], [n])
+    _rows("out", out, ref, H_, K, dtype)
+    _close("SN", SN, refS, K * U * HS)
+    n, by = (620, 0.2) if dtype == torch.float32 else (1100, 0.11)     # backward segments of 512 and 896
+    g, lens = torch.full((H,), by, device=DEV), torch.tensor([n], dtype=torch.int32, device=DEV)
+    dS0 = torch.empty_like(S0)
+    _, dk, dv = la.la_decay_backward(q, k, v, torch.zeros_like(dout), g, 0.25, dSN=dSN, dS0=dS0, lens=lens)
+    refs = decay.backward(qn, kn, vn, 0 * vn, _np(g), 0.25, None, En, [n])
+    hs = decay.backward(*ab[:3], 0 * vn, _np(g), 0.25, None, ab[4], [n])
+    for name, got, r, h in zip(("dk", "dv"), (dk, dv), refs[1:], hs[1:]):
+        _rows(name, got, r, h, K, dtype)
+    _close("dS0", dS0, refs[3], K * U * hs[3])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens", [None, [31], [97]])
+def test_growing_states(lens, dtype):
+    check(1, 2, 150, 64, 64, dtype, decays=[0.5, 0.1], lens=lens)

@@ -34,6 +34,15 @@ __device__ __forceinline__ float2 kept(float g, int n) {
 }
 __device__ __forceinline__ float keep(float2 a, float s) { return fmaf(a.y, s, a.x * s); }
 
+// The same over many tokens of a state that grows, where a^n may be past fp32's range: a
+// state of 0 stays 0, and a small one is not infinite before it has grown so far.  By
+// a^(n/4) four times: where that too is infinite, so is the smallest number's growth.
+__device__ __forceinline__ bool grows_far(float g, int n) { return g * (float)n > 80.f; }
+__device__ __forceinline__ float keep_far(float g, int n, float s) {
+    const float a = expf(0.25f * (g * (float)n));
+    return s == 0.f ? s : s * a * a * a * a;
+}
+
 // The segment with a sequence's last token (0 where it has none).  The segments end below
 // 2^31, but a token past one segment more would not.
 __host__ __device__ constexpr int last_segment(int len, int seg_tokens) { return len > 0 ? (len - 1) / seg_tokens : 0; }

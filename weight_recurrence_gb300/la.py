@@ -583,7 +583,7 @@ def la_decay_forward(q, k, v, log_decay, scale=1.0, S0=None, SN=None, lens=None,
     out_i = scale q_i^T S_i, g = log_decay[h].
 
     q, k: [B,H,N,D], v: [B,H,N,M], any strides but the channels'; log_decay: fp32
-    [H], at most 0 for states that do not grow.  S0, SN: fp32 [B,H,D,M], the
+    [H], at most 0 for states that do not grow, at most 1/2 for ones that do.  S0, SN: fp32 [B,H,D,M], the
     state before the first token and after the last; SN may be S0.  lens: int32
     [B]; rows past a length are 0.  want_out=False: the state alone (q may be
     None).  Returns out."""
