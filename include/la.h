@@ -482,7 +482,7 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
  * q and k enter as they are (no feature map, no denominator).
  *   q, k: [B,H,N,D]; v, out: [B,H,N,M], views of dtype s.dtype; any
  *      1 <= D, M <= 128 (larger: LA_ERR_UNSUPPORTED, as 8 B H >= 2^31 and
-      N >= 2^31 - 2^20).  Inputs may repeat heads or sequences (stride 0).
+ *      N >= 2^31 - 2^20).  Inputs may repeat heads or sequences (stride 0).
  *   log_decay: H fp32 values on the device; 0 forgets nothing, -infinity
  *      keeps the token itself alone; above 0 the state grows: up to 1/2, rows
  *      of 0 add 0 to it however long.  (Values are weighed by up to a^128 in
@@ -503,7 +503,7 @@ la_status la_grad_clip(const la_tensor *tensors, int count, float max_norm, floa
  * that leaves takes the products of the rows as they are, its weights by three
  * bf16 parts (two where outputs alone see it), in fp32.  So do bf16 inputs with
  * D or M no multiple of 8 from N = 64 on, packed into the workspace first.
- * fp32 data, any other bf16, and up to 16 tokens (8 of few heads) run fp32
+ * fp32 data, any other bf16, and up to 16 tokens (8 of few bf16 heads) run fp32
  * arithmetic.
  */
 la_status la_decay_forward(la_view q, la_view k, la_view v, la_view out, const float *log_decay, const int *lens,
@@ -538,7 +538,8 @@ la_status la_decay_step(la_view q, la_view k, la_view v, la_view y, const float 
  *      0; not wanted), two buffers.  Chaining segments of a sequence through
  *      dS0 -> dSN gives the backward of the whole.
  *   workspace: la_decay_workspace_bytes(s, 1) bytes.
- * Arithmetic and everything else as la_decay_forward.
+ * Everything else as la_decay_forward, and the arithmetic too, but that bf16 rows
+ * on 16-byte boundaries run on tensor cores at any N.
  */
 la_status la_decay_backward(la_view q, la_view k, la_view v, la_view dout, la_view dq, la_view dk, la_view dv,
                             const float *log_decay, const int *lens, la_shape s, float scale, const float *S0,
@@ -584,7 +585,8 @@ typedef struct {
  *   norm 0: n = x (wq and wk have to be NULL); else wq, wk: D fp32 values each,
  *      or NULL (1).  eps >= 0.
  *   D even, 2 <= D <= 256, B N < 2^31 - 2^20 (else LA_ERR_UNSUPPORTED).
- * All arithmetic is fp32, y is rounded once.
+ * All arithmetic is fp32, y is rounded once.  The sines and cosines are good to
+ * 2^-21 with bf16 data (also in dwq and dwk), to 2^-22 with fp32.
  */
 la_status la_qk_rotate_forward(la_view q, la_view k, la_view qo, la_view ko, const float *wq, const float *wk,
                                la_rotation rot, la_qk_shape s, int norm, float eps, la_stream_t stream);

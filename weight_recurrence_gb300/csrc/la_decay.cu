@@ -593,13 +593,14 @@ struct Cut {
 };
 
 // What a walk costs, in chunks of 128 tokens: a CTA's start and end, a chunk's sums
-// alone, a scan's launch; the chunk's time; CTAs that an SM holds.
+// alone, a scan's launch; the chunk's time where the SMs are full (it weighs a scan's
+// bytes against the rest); CTAs that an SM holds.
 struct Cost {
     double start, sums, scan, us;
     int slots;
 };
 // tensor cores (bf16) and FMA units
-constexpr Cost kTensor = {6.0, 0.9, 2.0, 2.1, 1}, kFma64 = {0.5, 0.4, 0.4, 13.0, 2}, kFma128 = {0.5, 0.4, 0.4, 20.0, 1};
+constexpr Cost kTensor = {6.0, 0.9, 2.0, 2.1, 1}, kFma64 = {0.5, 0.4, 0.4, 32.0, 2}, kFma128 = {0.5, 0.4, 0.4, 30.0, 1};
 
 // Segments of a sequence.  `ctas` walk over the whole sequences side by side; cut,
 // there are `segs` times as many, which have first to find the states at their
@@ -607,7 +608,7 @@ constexpr Cost kTensor = {6.0, 0.9, 2.0, 2.1, 1}, kFma64 = {0.5, 0.4, 0.4, 13.0,
 // Measured, us: tensor cores, 16 heads of 65536 tokens, D = M = 128: 9 segments (taken)
 // 490, 4 506, 8 540, 19 554, none 1087; backward of 16 heads of 16384: none (taken)
 // 264, 2 383, 3 290; 8 heads of 16384, D = M = 64: 19 (taken) 45, 4 126, none 262.
-// FMA units, 35 heads of 1537, D = M = 64: 8 (taken) 103, 4 118, none 248.
+// FMA units, 35 heads of 1537, D = M = 64: 7 (taken) and 13 107, 4 119, none 236.
 Cut cut_of(long long ctas, long long sums, double states, int N, const Cost &cost) {
     const long long chunks = ((long long)N + 127) / 128, slots = (long long)kSms * cost.slots;
     long long best = 1;

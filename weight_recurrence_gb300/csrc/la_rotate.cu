@@ -17,7 +17,7 @@
 // rows ahead 71 and 122).  The bf16 backward takes pieces of 8 bytes, four heads
 // ahead: with 16 the weights' sums leave room for one (107 us).  fp32 rows reach
 // 6.4 TB/s both ways; rows by single values are bound by their instructions (16384
-// tokens of 32 heads of 66 channels, bf16: 87 and 169 us, 1.6 and 1.2 TB/s; of 72
+// tokens of 32 heads of 66 channels, bf16: 87 and 166 us, 1.6 and 1.3 TB/s; of 72
 // channels, by 8 bytes, 51 and 77).
 #include <algorithm>
 #include <cstring>
