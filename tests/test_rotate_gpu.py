@@ -415,3 +415,24 @@ def test_large_frequencies_at_far_positions(dtype):
     angle = _exact_angles(pos.cpu().numpy(), freq.cpu().numpy().astype(np.float64))
     check_one("q", q, dqo, wq, qo, dq, dwq, angle, 1e-6, True, "half", dtype)
     check_one("k", k, dko, wk, ko, dk, dwk, angle, 1e-6, True, "half", dtype)
+
+
+def test_most_tokens():
+    """The largest token count that is taken: its first, middle and last rows are what they are by themselves, forward
+    and backward in place."""
+    N = (1 << 31) - 1 - (1 << 20)
+    q = torch.ones(1, 1, N, 2, device=DEV, dtype=torch.bfloat16)
+    pos = torch.arange(N, device=DEV, dtype=torch.int32)
+    freq = torch.tensor([0.7], device=DEV)
+    at = [slice(0, 70), slice((1 << 30) - 40, (1 << 30) + 40), slice(N - 100000, N)]
+    for s in at:
+        q[:, :, s].normal_(generator=torch.Generator(DEV).manual_seed(1))
+    out = la.la_qk_rotate_forward(q, None, pos, freq)[0]
+    alone = [la.la_qk_rotate_forward(q[:, :, s], None, pos[s], freq)[0] for s in at]
+    assert all(torch.equal(out[:, :, s], a) for s, a in zip(at, alone))
+    la.la_qk_rotate_backward(out, None, q, None, pos, freq, dq=out)
+    grads = [la.la_qk_rotate_backward(a, None, q[:, :, s], None, pos[s], freq)[0] for s, a in zip(at, alone)]
+    same = all(torch.equal(out[:, :, s], a) for s, a in zip(at, grads))
+    del q, pos, out
+    torch.cuda.empty_cache()
+    assert same
